@@ -336,6 +336,94 @@ class Engine:
         torch.cuda.synchronize(self.device)
         _check(lib.mk_seq_set(self.ctx, dst, info["length"], _np_ptr(new), n), "mk_seq_set")
 
+    # ------------------------------------------- the cache outside the step
+    def kv_pool(self, layer: int):
+        """KV layer `layer` of the pool (gated-attention layers in order, then
+        the MTP head's) as an ops.KVPool: for ops.kv_write, kv_read, attend."""
+        from . import ops
+        views = self.kv_views()
+        names = ("kq", "vq", "ks", "vs") if self.layout.kv_dtype == MK_KV_Q8 else ("k", "v")
+        if not 0 <= layer < views[names[0]].shape[0]:
+            raise MkError(-1, "kv_pool (layer)")
+        return ops.KVPool(*(views[n][layer] for n in names))
+
+    def seq_rows(self, seqs, new_rows):
+        """ops.KVRows of committed sequences: the last new_rows[i] cached
+        tokens of each seqs[i], in order."""
+        from . import ops
+        torch = self.torch
+        info = [self.seq_get(s) for s in seqs]
+        new_rows = [int(n) for n in new_rows]
+        if len(new_rows) != len(info) or any(not 0 <= n <= i["length"] for n, i in zip(new_rows, info)):
+            raise MkError(-1, "seq_rows (0 to length rows of each sequence)")
+        start = np.concatenate([[0], np.cumsum(new_rows)]).astype(np.int32)
+        tables = np.full((len(info), max([len(i["pages"]) for i in info] + [1])), -1, np.int32)
+        for t, i in zip(tables, info):
+            t[:len(i["pages"])] = i["pages"]
+        dev = [torch.from_numpy(a).to(self.device) for a in
+               (start, np.array([i["length"] for i in info], np.int32), tables)]
+        return ops.KVRows(*dev, n_rows=int(start[-1]), max_q=max(new_rows + [0]))
+
+    def seq_load(self, seq: int, k, v, S=None, conv=None):
+        """Install sequence seq from dense K and V of its tokens, computed or
+        saved elsewhere: CUDA tensors [kv layers][tokens][kv heads][head dim]
+        (K after RoPE), stored on the lowest free pages, rounded or quantised
+        as the step stores its own rows. S, conv: its recurrent state, as in
+        seq_set; zero when not given."""
+        from . import ops
+        torch, m = self.torch, self.model
+        n_kv = sum(1 for x in m["kinds"] if x == 1) + (1 if self.layout.has_mtp else 0)
+        if k.dim() != 4 or k.shape != v.shape or k.shape[0] != n_kv:
+            raise MkError(-1, "seq_load (k, v [kv layers][tokens][kv heads][head dim])")
+        if not 0 <= seq < self.max_seqs:
+            raise MkError(-1, "seq_load (sequence)")
+        used = set()
+        for s in range(self.max_seqs):
+            if s != seq:
+                used.update(int(p) for p in self.seq_get(s)["pages"])
+        n = k.shape[1]
+        need = -(-n // 16)
+        if need > self.layout.max_pages_per_seq:
+            raise MkError(-1, "seq_load (more pages than max_pages_per_seq)")
+        pages = [p for p in range(self.layout.n_pages) if p not in used][:need]
+        if len(pages) < need:
+            raise MkError(-2, "seq_load (no free pages)")
+        if n:
+            dev = [torch.tensor(x, dtype=torch.int32, device=self.device) for x in ([0, n], [n], [pages])]
+            rows = ops.KVRows(*dev, n_rows=n)
+            for i in range(n_kv):
+                ops.kv_write(self.kv_pool(i), rows, k[i], v[i])
+        Sv, Cv = self.state_views()
+        if Sv is not None:
+            if S is None:
+                Sv[seq, 0].zero_()
+            if conv is None:
+                Cv[seq, 0].zero_()
+        self.seq_set(seq, n, pages, S, conv)
+
+    def seq_kv(self, seq: int, dtype=None):
+        """Dense K and V of a committed sequence, [kv layers][tokens][kv heads]
+        [head dim] of type dtype (float16 by default): what seq_load takes."""
+        from . import ops
+        torch, m = self.torch, self.model
+        n = self.seq_get(seq)["length"]
+        n_kv = sum(1 for x in m["kinds"] if x == 1) + (1 if self.layout.has_mtp else 0)
+        k, v = (torch.empty((n_kv, n, m["hkv"], m["dh"]), dtype=dtype or torch.float16, device=self.device) for _ in "kv")
+        if n:
+            rows = self.seq_rows([seq], [n])
+            for i in range(n_kv):
+                ops.kv_read(self.kv_pool(i), rows, out=(k[i], v[i]))
+        return k, v
+
+    def attend(self, layer: int, q, seqs, new_rows, window: int = 0, sinks: int = 0, gate=None, out=None):
+        """Attention of the last new_rows[i] cached tokens of each seqs[i]
+        over KV layer `layer` (ops.attend): q [sum of new_rows][fa_hq][fa_dh]."""
+        from . import ops
+        if q.dim() != 3 or q.shape[1] != self.layout.fa_hq:
+            raise MkError(-1, "attend (q [rows][query heads][head dim])")
+        return ops.attend(self.kv_pool(layer), self.seq_rows(seqs, new_rows), q, window=window, sinks=sinks, gate=gate,
+                          out=out)
+
     # ----------------------------------------------------------------- step
     @staticmethod
     def _rows(tokens, positions, seq_ids, flags):
