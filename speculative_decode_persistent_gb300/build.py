@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 SO = os.path.join(HERE, "libmk.so")
-SOURCES = ["mk_kernel.cu", "mk_api.cu", "mk_pack.cu", "ops/kv_rows.cu", "ops/attend.cu"]
+SOURCES = ["mk_kernel.cu", "mk_api.cu", "mk_pack.cu", "ops/kv_rows.cu", "ops/attend.cu",
+           "ops/attend_f16.cu", "ops/attend_q8.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,

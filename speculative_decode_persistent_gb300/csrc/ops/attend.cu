@@ -1,77 +1,54 @@
-// Attention of a chunk of new rows over the paged cache: one warp per (row,
-// query head), the online softmax over the tokens one by one.
-#include <cuda_runtime.h>
+// C entry of the chunk attention: argument checks, tensor maps of the pool,
+// choice of the kernel.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include <cmath>
 
-#include "ops_internal.cuh"
+#include "attend.cuh"
 
 namespace mk {
 namespace ops {
+cudaError_t launch_attend_f16(int ns, int cg, const AttendParams& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                              int device, cudaStream_t stream);
+cudaError_t launch_attend_q8(int ns, int cg, const AttendParams& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                             int device, cudaStream_t stream);
+
 namespace {
-
-constexpr int kWarpsPerBlock = 4;
-
-struct Args {
-  mk_kv_pool pool;
-  mk_kv_rows rows;
-  mk_attend_args a;
-};
-
-__device__ __forceinline__ float pool_value(const void* codes, const void* scale, int q8, int64_t e) {
-  if (!q8) return __half2float(static_cast<const __half*>(codes)[e]);
-  return __half2float(static_cast<const __half*>(scale)[e / 32]) * static_cast<float>(static_cast<const int8_t*>(codes)[e]);
-}
-
-template <int DT>
-__global__ void attend_rows_kernel(const Args g) {
-  using T = typename Elem<DT>::T;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarpsPerBlock + threadIdx.x / 32;
-  if (w >= static_cast<int64_t>(g.rows.n_rows) * g.a.hq) return;
-  const int r = static_cast<int>(w / g.a.hq), h = static_cast<int>(w % g.a.hq);
-  int s = 0;
-  SeqView v{0, 0, 0};
-  for (; s < g.rows.n_seqs; ++s) {
-    v = seq_view(g.rows, s);
-    if (r >= v.r0 && r < v.r0 + v.q_len) break;
-  }
-  if (s == g.rows.n_seqs) return;
-  const int pos = v.kv_len - v.q_len + (r - v.r0), dh = g.pool.dh, kh = h / (g.a.hq / g.pool.hkv);
-  const int nd = dh / 32, q8 = g.pool.kv_dtype == MK_KV_Q8;
-  float q[8], o[8] = {}, m = -INFINITY, l = 0.f;
-  const T* qp = static_cast<const T*>(g.a.q.data) + r * g.a.q.row_stride + h * g.a.q.head_stride;
-  for (int i = 0; i < nd; ++i) q[i] = Elem<DT>::get(qp[32 * i + lane]) * g.a.scale;
-  for (int t = 0; t <= pos; ++t) {
-    if (g.a.window > 0 && pos - t >= g.a.window && t >= g.a.sinks) continue;
-    const int page = g.rows.tables[static_cast<int64_t>(s) * g.rows.table_stride + t / kPage];
-    if (page < 0 || page >= g.pool.n_pages) continue;
-    const int64_t e = ((static_cast<int64_t>(page) * g.pool.hkv + kh) * kPage + t % kPage) * dh + lane;
-    float x = 0.f;
-    for (int i = 0; i < nd; ++i) x += q[i] * pool_value(g.pool.k, g.pool.k_scale, q8, e + 32 * i);
-    for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-    if (x == -INFINITY) continue;
-    const float nm = fmaxf(m, x), f = expf(m - nm), p = expf(x - nm);
-    m = nm;
-    l = l * f + p;
-    for (int i = 0; i < nd; ++i) o[i] = o[i] * f + p * pool_value(g.pool.v, g.pool.v_scale, q8, e + 32 * i);
-  }
-  for (int i = 0; i < nd; ++i) {
-    float y = l > 0.f || l != l ? o[i] / l : 0.f;
-    if (g.a.gate.data) {
-      const T* gp = static_cast<const T*>(g.a.gate.data) + r * g.a.gate.row_stride + h * g.a.gate.head_stride;
-      y /= 1.f + expf(-Elem<DT>::get(gp[32 * i + lane]));
-    }
-    static_cast<T*>(g.a.out.data)[r * g.a.out.row_stride + h * g.a.out.head_stride + 32 * i + lane] = Elem<DT>::put(y);
-  }
-}
 
 mk_status check_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, int32_t hq) {
   mk_status st = check_pool(pool);
   if (st == MK_OK) st = check_rows(rows);
   if (st != MK_OK) return st;
   if (hq <= 0 || hq % pool->hkv) return MK_ERR_INVALID;
-  return hq / pool->hkv > 256 ? MK_ERR_UNSUPPORTED : MK_OK;
+  if (hq / pool->hkv > 256) return MK_ERR_UNSUPPORTED;
+  // (row, head) pairs are counted with 32 bits
+  return static_cast<int64_t>(rows->n_rows) * hq > 0x7fff0000ll ? MK_ERR_UNSUPPORTED : MK_OK;
+}
+
+constexpr size_t kJoinBytes = (kMaxWorkers * sizeof(JoinInfo) + 255) / 256 * 256;
+// two parts per worker of 128 rows a block
+constexpr size_t kMlBytes = 2ull * kMaxWorkers * 128 * sizeof(float2);
+
+// The pool as token rows of dh elements; boxes of one page by 128 bytes
+// (binary16, swizzled as the products read it) or by `box` codes.
+bool encode_map(CUtensorMap* m, void* base, const mk_kv_pool& p, int box) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }();
+  if (!encode) return false;
+  const bool q8 = p.kv_dtype == MK_KV_Q8;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.dh), static_cast<cuuint64_t>(p.n_pages) * p.hkv * kPage};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.dh) * (q8 ? 1 : 2)};
+  const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box), kPage}, one[2] = {1, 1};
+  return encode(m, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, boxes,
+                one, CU_TENSOR_MAP_INTERLEAVE_NONE, q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -79,7 +56,9 @@ mk_status check_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, int32_t h
 }  // namespace mk
 
 extern "C" size_t mk_attend_work_bytes(const mk_kv_pool* pool, const mk_kv_rows* rows, int32_t hq) {
-  return mk::ops::check_attend(pool, rows, hq) == MK_OK ? 256 : 0;
+  using namespace mk::ops;
+  if (check_attend(pool, rows, hq) != MK_OK) return 0;
+  return kJoinBytes + kMlBytes + 2ull * kMaxWorkers * 128 * pool->dh * sizeof(float);
 }
 
 extern "C" mk_status mk_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, const mk_attend_args* a, void* stream) {
@@ -97,14 +76,38 @@ extern "C" mk_status mk_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, c
   if (((reinterpret_cast<uintptr_t>(a->q.data) | reinterpret_cast<uintptr_t>(a->out.data) |
         reinterpret_cast<uintptr_t>(a->gate.data)) & 1u))
     return MK_ERR_INVALID;
-  const int64_t warps = static_cast<int64_t>(rows->n_rows) * a->hq;
-  const int64_t grid = (warps + kWarpsPerBlock - 1) / kWarpsPerBlock;
-  if (grid > 0x7fffffffll) return MK_ERR_UNSUPPORTED;
-  const Args g{*pool, *rows, *a};
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a->dtype == MK_F16)
-    attend_rows_kernel<MK_F16><<<static_cast<unsigned>(grid), kWarpsPerBlock * 32, 0, s>>>(g);
-  else
-    attend_rows_kernel<MK_BF16><<<static_cast<unsigned>(grid), kWarpsPerBlock * 32, 0, s>>>(g);
-  return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+
+  AttendParams p{};
+  p.pool = *pool;
+  p.rows = *rows;
+  p.q = a->q;
+  p.gate = a->gate;
+  p.out = a->out;
+  p.hq = a->hq;
+  p.G = a->hq / pool->hkv;
+  p.dtype = a->dtype;
+  // a window beyond every length is none, and keeps the positions' arithmetic in range
+  p.window = a->window >= rows->table_stride * kPage ? 0 : a->window;
+  p.sinks = p.window ? a->sinks : 0;
+  p.c = std::fmin(std::fmax(a->scale * 1.44269504088896341f, 1.2e-38f), 3e38f);
+  p.vq = dense_vec(a->q, a->dtype);
+  p.vo = dense_vec(a->out, a->dtype);
+  p.vg = dense_vec(a->gate, a->dtype);
+  uint8_t* w = static_cast<uint8_t*>(a->work);
+  p.join = reinterpret_cast<JoinInfo*>(w);
+  p.ml = reinterpret_cast<float2*>(w + kJoinBytes);
+  p.part = reinterpret_cast<float*>(w + kJoinBytes + kMlBytes);
+
+  const int ns = pool->dh / 64, q8 = pool->kv_dtype == MK_KV_Q8;
+  // Pairs of blocks where a sequence fills more than one 128-row tile: they
+  // fetch half the bytes per product. Below that the second block of a pair
+  // would have no rows, and single blocks keep twice as many copies going.
+  const int cg = ns % 2 == 0 && static_cast<int64_t>(rows->max_q) * p.G > 128 ? 2 : 1;
+  CUtensorMap tk, tv;
+  const int box = q8 ? q8_box(ns, cg) : 64;
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || !encode_map(&tk, pool->k, *pool, box) || !encode_map(&tv, pool->v, *pool, box))
+    return MK_ERR_CUDA;
+  const cudaError_t e = (q8 ? launch_attend_q8 : launch_attend_f16)(ns, cg, p, tk, tv, device, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }

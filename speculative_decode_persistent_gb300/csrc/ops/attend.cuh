@@ -1,0 +1,955 @@
+// Attention of a chunk of new rows over the paged cache, on the tensor cores.
+//
+// Mathematics. For a row at position p: s_t = scale q.k_t over the tokens it
+// sees, out = sum_t 2^(s_t' - m) v_t / sum_t 2^(s_t' - m) with s' = s log2(e)
+// and m any reference near the maximum: one pass over the tokens, 128 at a
+// time. m moves only when a score passes it by more than 2^8, so the output
+// accumulator is rescaled a few times per row, not once per block of tokens.
+//
+// Shape. The (row, query head) pairs that share a kv head are the rows of a
+// tile, 128 of them per thread block (row R of a sequence is token R / group,
+// head R % group of the kv head's group). S = Q K^T [128 x 128] and O += P V
+// [128 x dh] run as tcgen05.mma with S (two buffers), P (binary16, over S's
+// own columns) and O in tensor memory: 2 x 128 + 256 of its 512 columns. P is
+// the A operand straight from tensor memory; K is the K-major and V the
+// MN-major B operand as TMA lays the pages down (128-byte swizzle).
+//
+// CG = 1: a block works alone. CG = 2: two blocks of a cluster share one tile
+// of 256 rows; each holds half of every K and V block and the instruction
+// reads both halves, so a block fetches and stores half the bytes per product.
+//
+// Work. All (sequence, kv head, tile) items are cut into 128-token blocks of
+// what their rows can see (a window skips the middle); the blocks of all items
+// form one line that is cut evenly among the workers (blocks or pairs). An
+// item cut in two or more leaves unnormalised parts, which attend_join adds
+// in a fixed order: results do not depend on timing. Every worker finds its
+// piece from the lengths on the device, so nothing is planned on the host.
+//
+// Warps: 0 copies pages, 1 issues products, 4-7 take the softmax (thread =
+// row) and write results, 8.. prepare operands: they load Q, turn q8 codes
+// into binary16 tiles, and clear what must not enter a product (below).
+//
+// Unseen values. A masked score is replaced before the softmax, so K may hold
+// anything. A masked probability is 0, but 0 x inf is NaN inside a product:
+// in blocks that some row sees only in part, non-finite V values are cleared
+// in shared memory before the product, and rows that do see one add it when
+// they write their result (a rare path). Missing pages arrive as zeros.
+//
+// Every wait is bounded; a worker that gives up writes NaN for its rows.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "ops_internal.cuh"
+#include "sm103.cuh"
+
+namespace mk {
+namespace ops {
+
+constexpr int kBN = 128;             // tokens per block: eight pages
+constexpr int kMaxWorkers = 160;     // at least the SM count
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+// A worker's first item, when it began at an earlier worker: what the join needs.
+struct JoinInfo {
+  int s, h, mt, w0, w1, slot0, rows, pad;  // w0 < 0: nothing to join here
+};
+
+struct AttendParams {
+  mk_kv_pool pool;
+  mk_kv_rows rows;
+  mk_dense q, gate, out;
+  int hq, G, dtype, window, sinks, workers;
+  float c;         // scale x log2(e)
+  int vq, vo, vg;  // 16-byte access to q, out, gate
+  JoinInfo* join;  // [kMaxWorkers]
+  float2* ml;      // [2 workers][128 CG] reference and sum of a part
+  float* part;     // [2 workers][128 CG][dh] unnormalised output
+};
+
+// ------------------------------------------------------------------ geometry
+// Tile mt of a sequence: M rows of (token, head in group) pairs.
+struct Tile {
+  int rows;         // valid rows
+  int p0, p1;       // positions of its first and last token
+  int nblk;         // 128-token blocks some row may see, at least 1
+  int sink_b, lo;   // block i is i < sink_b ? i : lo + i - sink_b
+  __device__ __forceinline__ int block(int i) const { return i < sink_b ? i : lo + i - sink_b; }
+};
+__device__ __forceinline__ int tiles_of(const SeqView& v, int G, int M) { return (v.q_len * G + M - 1) / M; }
+__device__ __forceinline__ Tile make_tile(const SeqView& v, int G, int M, int mt, int window, int sinks) {
+  Tile t;
+  const int R0 = mt * M, R1 = min(R0 + M, v.q_len * G);
+  t.rows = R1 - R0;
+  t.p0 = v.kv_len - v.q_len + R0 / G;
+  t.p1 = v.kv_len - v.q_len + (R1 - 1) / G;
+  t.sink_b = t.lo = 0;
+  t.nblk = 1;
+  if (t.p1 >= 0) {
+    const int hi = t.p1 / kBN;
+    if (window > 0) {
+      t.lo = max(0, t.p0 - window + 1) / kBN;
+      t.sink_b = (min(sinks, t.p1 + 1) + kBN - 1) / kBN;
+      if (t.sink_b >= t.lo) t.lo = t.sink_b = 0;
+    }
+    t.nblk = t.sink_b + hi - t.lo + 1;
+  }
+  return t;
+}
+// Whether rows at positions p0..p1 all see every token of block b.
+__device__ __forceinline__ bool block_full(int b, int p0, int p1, int window, int sinks) {
+  const int last = b * kBN + kBN - 1;
+  return last <= p0 && (window == 0 || b * kBN > p1 - window || last < sinks);
+}
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+// Tokens base .. base+31 that a row at position p sees (missing pages aside).
+__device__ __forceinline__ uint32_t seen_bits(int p, int base, int window, int sinks) {
+  uint32_t m = low_bits(p - base + 1);
+  if (window > 0) m &= ~low_bits(p - window + 1 - base) | low_bits(sinks - base);
+  return m;
+}
+
+// A worker's walk through the line of blocks: segments of consecutive blocks
+// of one item. Every role walks it for itself.
+struct Start {
+  int s, h, mt, blk;
+  int64_t n;  // blocks of this worker
+};
+struct Walk {
+  const AttendParams* a;
+  int s, h, mt, blk, n_mt, M, seg;
+  int64_t left;
+  SeqView v;
+  Tile t;
+  int b0, b1;  // block indices [b0, b1) of the current segment
+  __device__ __forceinline__ Walk(const AttendParams& p, const Start& st, int M_)
+      : a(&p), s(st.s), h(st.h), mt(st.mt), blk(st.blk), M(M_), seg(-1), left(st.n) {
+    if (left > 0) {
+      v = seq_view(p.rows, s);
+      n_mt = tiles_of(v, p.G, M);
+    }
+  }
+  __device__ __forceinline__ bool next() {
+    if (seg >= 0) {
+      left -= b1 - b0;
+      if (left <= 0) return false;
+      blk = 0;
+      if (++mt == n_mt) {
+        mt = 0;
+        if (++h == a->pool.hkv) {
+          h = 0;
+          do {
+            if (++s >= a->rows.n_seqs) return false;  // (only if the lengths changed under the kernel)
+            v = seq_view(a->rows, s);
+            n_mt = tiles_of(v, a->G, M);
+          } while (n_mt == 0);
+        }
+      }
+    } else if (left <= 0) {
+      return false;
+    }
+    ++seg;
+    t = make_tile(v, a->G, M, mt, a->window, a->sinks);
+    b0 = blk;
+    b1 = static_cast<int>(min(static_cast<int64_t>(t.nblk), blk + left));
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return b0 == 0 && b1 == t.nblk; }
+  // page of the block's i-th 16 tokens, -1 when there is none
+  __device__ __forceinline__ int page(int b, int i) const {
+    const int e = b * (kBN / kPage) + i;
+    if (e >= a->rows.table_stride) return -1;
+    const int pg = __ldg(a->rows.tables + static_cast<int64_t>(s) * a->rows.table_stride + e);
+    return pg >= 0 && pg < a->pool.n_pages ? pg : -1;
+  }
+};
+
+// -------------------------------------------------------------------- layout
+// Bytes per row of a q8 tensor-copy box: 128 where every unit's width is a multiple of it.
+__host__ __device__ constexpr int q8_box(int ns, int cg) { return ns % 2 || ns / cg == 1 ? 64 : 128; }
+template <int NS, bool Q8, int CG>
+struct Cfg {
+  static constexpr int DH = NS * 64, M = 128 * CG;
+  // units: what one ring slot holds, nkeys tokens x nsl slabs of 64 dims
+  static constexpr int KU = CG == 2 ? 1 : (NS + 1) / 2;  // K: all 128 tokens, two slabs each (pair: 64 tokens, all slabs)
+  static constexpr int VU = CG == 2 ? 1 : NS > 2 ? 2 : 1;  // V: all slabs, split over the tokens (pair: half the slabs)
+  static constexpr int kKeysK = CG == 2 ? 64 : 128, kKeysV = CG == 2 ? 128 : 128 / VU;
+  static constexpr int kSlabsV = CG == 2 ? NS / 2 : NS;
+  static __host__ __device__ constexpr int slabs_k(int u) { return CG == 2 ? NS : (NS - 2 * u < 2 ? NS - 2 * u : 2); }
+  static constexpr int kUnitK = kKeysK * slabs_k(0) * 128, kUnitV = kKeysV * kSlabsV * 128;
+  static constexpr int kSlot = kUnitK > kUnitV ? kUnitK : kUnitV;
+  static constexpr int kQ = NS * 16384;
+  static constexpr int kMisc = 5120;
+  static constexpr int kRaw = kSlot / 2 + 128 * NS * 4;  // q8 codes, then 2 NS scales per token
+  static constexpr int kBudget = 232448 - 1024 - kMisc - kQ;
+  static constexpr int kRawSlots = Q8 ? 3 : 0;
+  static constexpr int kFit = (kBudget - kRawSlots * kRaw) / kSlot;
+  static constexpr int kSlots = kFit > 8 ? 8 : kFit;
+  static constexpr int kBox = q8_box(NS, CG);
+  static constexpr int kPrep = Q8 ? 8 : 4;        // preparing warps
+  static constexpr int kThreads = 256 + 32 * kPrep;
+  static constexpr int kSmem = 1024 + kMisc + kQ + kSlots * kSlot + kRawSlots * kRaw;
+  static_assert(kSlots >= 3, "ring");
+  static_assert(!Q8 || (slabs_k(0) * 64 % kBox == 0 && kSlabsV * 64 % kBox == 0), "boxes");
+};
+
+struct Misc {
+  uint64_t ready[8], full[8], empty[8], raw_full[4], raw_empty[4];
+  uint64_t s_full[2], p_ready[2], pv_done, q_ready, q_free;
+  uint32_t tmem;
+  int dead;
+  Start start;
+  int flag[4];           // segment + 1 in which non-finite V values were cleared
+  int raw_pages[4];      // bit i: page i of a raw unit is missing
+  float qc[4][128];      // per row: scale x log2(e) x 2^e of the row's query
+};
+static_assert(sizeof(Misc) <= 5120, "misc area");
+
+// Output of eight or more neighbouring dims: gate, rounding, store.
+template <int N>
+__device__ __forceinline__ void put_out(const AttendParams& a, int row, int head, int d0, const float* x) {
+  const int64_t oo = row * a.out.row_stride + head * a.out.head_stride + d0;
+  const int64_t go = row * a.gate.row_stride + head * a.gate.head_stride + d0;
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+    float y[8], g[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = x[i + k];
+    if (a.gate.data) {
+      if (a.dtype == MK_F16) {
+        const __half* gp = static_cast<const __half*>(a.gate.data) + go + i;
+        if (a.vg) load8<MK_F16, true>(gp, g); else load8<MK_F16, false>(gp, g);
+      } else {
+        const __nv_bfloat16* gp = static_cast<const __nv_bfloat16*>(a.gate.data) + go + i;
+        if (a.vg) load8<MK_BF16, true>(gp, g); else load8<MK_BF16, false>(gp, g);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = __fdividef(y[k], 1.f + __expf(-g[k]));
+    }
+    if (a.dtype == MK_F16) {
+      __half* op = static_cast<__half*>(a.out.data) + oo + i;
+      if (a.vo) store8<MK_F16, true>(op, y); else store8<MK_F16, false>(op, y);
+    } else {
+      __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out.data) + oo + i;
+      if (a.vo) store8<MK_BF16, true>(op, y); else store8<MK_BF16, false>(op, y);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- scheduling
+// Total blocks of the line and this worker's piece of it. scratch: int64
+// [n_seqs + 1]. All threads of the block call it.
+template <int M>
+__device__ void find_start(const AttendParams& a, int64_t* scratch, Start* out, int worker, bool leader) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, nw = blockDim.x / 32;
+  for (int s = warp; s < a.rows.n_seqs; s += nw) {
+    const SeqView v = seq_view(a.rows, s);
+    const int n = tiles_of(v, a.G, M);
+    int64_t sum = 0;
+    for (int mt = lane; mt < n; mt += 32) sum += make_tile(v, a.G, M, mt, a.window, a.sinks).nblk;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    if (lane == 0) scratch[s] = sum;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  int64_t total = 0;
+  for (int s0 = 0; s0 < a.rows.n_seqs; s0 += 32) {
+    int64_t x = s0 + lane < a.rows.n_seqs ? scratch[s0 + lane] : 0;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
+    total += x;
+  }
+  total *= a.pool.hkv;
+  const int64_t quota = max(static_cast<int64_t>(1), (total + a.workers - 1) / a.workers);
+  const int64_t g0 = worker * quota, n = min(quota, total - g0);
+  if (leader && lane == 0) a.join[worker].w0 = -1;
+  if (lane == 0) out->n = n;
+  if (n <= 0) return;
+  // the sequence whose blocks hold g0, then the head, then the tile
+  int64_t at = 0, cost = 0;
+  int s = 0;
+  for (;; ++s) {
+    cost = scratch[s];
+    if (g0 < at + cost * a.pool.hkv) break;
+    at += cost * a.pool.hkv;
+  }
+  const SeqView v = seq_view(a.rows, s);
+  const int h = static_cast<int>((g0 - at) / cost);
+  at += h * cost;
+  const int n_mt = tiles_of(v, a.G, M);
+  int mt = 0;
+  for (;; mt += 32) {
+    if (mt >= n_mt) {  // (only if the lengths changed under the kernel)
+      if (lane == 0) out->n = 0;
+      return;
+    }
+    const int nb = mt + lane < n_mt ? make_tile(v, a.G, M, mt + lane, a.window, a.sinks).nblk : 0;
+    int64_t inc = nb;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, k);
+      if (lane >= k) inc += y;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, g0 < at + inc && nb > 0);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      at += __shfl_sync(0xffffffffu, inc - nb, l);
+      mt += l;
+      break;
+    }
+    at += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) {
+    *out = Start{s, h, mt, static_cast<int>(g0 - at), n};
+    if (leader && g0 > at) {
+      const Tile t = make_tile(v, a.G, M, mt, a.window, a.sinks);
+      JoinInfo j;
+      j.s = s;
+      j.h = h;
+      j.mt = mt;
+      j.w0 = static_cast<int>(at / quota);
+      j.w1 = static_cast<int>((at + t.nblk - 1) / quota);
+      j.slot0 = 2 * j.w0 + (at == j.w0 * quota ? 0 : 1);
+      j.rows = t.rows;
+      j.pad = 0;
+      a.join[worker] = j;
+    }
+  }
+}
+
+// Adds the parts of items that were cut: one warp per row, the blocks of an
+// item's cuts share its rows.
+template <int NS, int CG>
+__global__ void __launch_bounds__(256) attend_join(const AttendParams a) {
+  constexpr int DH = NS * 64, M = 128 * CG, kPer = DH / 32;
+  const JoinInfo j = a.join[blockIdx.x];
+  if (j.w0 < 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int cuts = j.w1 - j.w0, w = blockIdx.x;
+  const SeqView v = seq_view(a.rows, j.s);
+  for (int r = ((w - j.w0 - 1) * gridDim.y + blockIdx.y) * 8 + warp; r < j.rows; r += cuts * gridDim.y * 8) {
+    float m = -INFINITY;
+    for (int k = lane; k <= cuts; k += 32) m = fmaxf(m, a.ml[(k ? 2 * (j.w0 + k) : j.slot0) * M + r].x);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    if (m == -INFINITY) m = 0.f;
+    float l = 0.f, o[kPer] = {};
+    for (int k = 0; k <= cuts; ++k) {
+      const int slot = k ? 2 * (j.w0 + k) : j.slot0;
+      const float2 x = a.ml[slot * M + r];
+      const float f = ex2(x.x - m);
+      l += f * x.y;
+      const float* p = a.part + (static_cast<int64_t>(slot) * M + r) * DH + lane * kPer;
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) {
+        const float2 y = *reinterpret_cast<const float2*>(p + i);
+        o[i] += f * y.x;
+        o[i + 1] += f * y.y;
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    float x[8];  // eight dims per store
+    const int R = j.mt * M + r, row = v.r0 + R / a.G, head = j.h * a.G + R % a.G;
+    if (kPer == 8) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[i] = l == 0.f ? 0.f : o[i] * inv;
+      put_out<8>(a, row, head, lane * 8, x);
+    } else {
+      // through shared memory: a row's dims, eight per lane
+      __shared__ float buf[8][192];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) buf[warp][lane * kPer + i] = l == 0.f ? 0.f : o[i] * inv;
+      __syncwarp();
+      if (lane < DH / 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = buf[warp][lane * 8 + i];
+        put_out<8>(a, row, head, lane * 8, x);
+      }
+      __syncwarp();
+    }
+  }
+}
+
+template <int NS, bool Q8, int CG>
+__global__ void __launch_bounds__(Cfg<NS, Q8, CG>::kThreads, 1)
+    attend_kernel(const __grid_constant__ AttendParams a, const __grid_constant__ CUtensorMap tk,
+                  const __grid_constant__ CUtensorMap tv) {
+  using C = Cfg<NS, Q8, CG>;
+  constexpr int M = C::M, DH = C::DH;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* const sq = smem;                          // Q [NS][128 rows][128 B], swizzled
+  uint8_t* const ring = sq + C::kQ;                  // operand units
+  uint8_t* const raw = ring + C::kSlots * C::kSlot;  // q8 units as stored
+  Misc& ms = *reinterpret_cast<Misc*>(raw + C::kRawSlots * C::kRaw);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+  const int rank = CG == 2 ? static_cast<int>(blockIdx.x & 1) : 0;
+  const int worker = blockIdx.x / CG;
+  volatile int* const dead = &ms.dead;
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+  auto wait1 = [&](uint64_t& b, uint32_t parity) { return bar_wait(smem_u32(&b), parity, dead, kWaitNs); };
+  auto wait = [&](uint64_t& b, uint32_t parity) { return __all_sync(0xffffffffu, wait1(b, parity)) != 0; };  // whole warps
+  // barriers the product-issuing block waits on, reached from both blocks
+  auto lead_arrive = [&](uint64_t& b) {
+    if (CG == 1) bar_arrive(smem_u32(&b)); else bar_arrive_cluster(peer_addr(smem_u32(&b), 0));
+  };
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      bar_init(bar(ms.full[i]), 1);
+      bar_init(bar(ms.ready[i]), CG * C::kPrep);
+      bar_init(bar(ms.empty[i]), 1);
+    }
+    for (int i = 0; i < C::kRawSlots; ++i) {
+      bar_init(bar(ms.raw_full[i]), 1);
+      bar_init(bar(ms.raw_empty[i]), C::kPrep);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bar(ms.s_full[i]), 1);
+      bar_init(bar(ms.p_ready[i]), 4 * CG);
+    }
+    bar_init(bar(ms.pv_done), 1);
+    bar_init(bar(ms.q_ready), CG * C::kPrep);
+    bar_init(bar(ms.q_free), 1);
+    ms.dead = 0;
+    for (int i = 0; i < 4; ++i) ms.flag[i] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc<CG>(smem_u32(&ms.tmem), 512);
+  find_start<M>(a, reinterpret_cast<int64_t*>(ring), &ms.start, worker, rank == 0);
+  tc_fence_before();
+  fence_async_shared();  // the scratch lay where tensor copies go
+  __syncthreads();
+  if (CG == 2) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  tc_fence_after();
+  const uint32_t tm = ms.tmem;
+  Walk wk(a, ms.start, M);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ page copies
+    int n = 0;       // units issued
+    bool ok = true;
+    // unit u of K (kv = 0) or V of block b, whose page ids the lanes 0..7 hold
+    auto unit = [&](int kv, int u, int pg) {
+      const int nkeys = kv ? C::kKeysV : C::kKeysK, nsl = kv ? C::kSlabsV : C::slabs_k(u);
+      const int key0 = CG == 2 ? (kv ? 0 : 64 * rank) : (kv ? u * C::kKeysV : 0);
+      const int slab0 = CG == 2 ? (kv ? rank * C::kSlabsV : 0) : (kv ? 0 : 2 * u);
+      const int np = nkeys / kPage, p0 = key0 / kPage;
+      const CUtensorMap* map = kv ? &tv : &tk;
+      const int none = a.pool.n_pages * a.pool.hkv * kPage;  // a row behind the pool reads as zeros
+      if constexpr (!Q8) {
+        const int slot = n % C::kSlots;
+        if (!wait(ms.empty[slot], ((n / C::kSlots) & 1) ^ 1)) return false;
+        if (lane == 0) bar_expect(bar(ms.full[slot]), nkeys * nsl * 128);
+        __syncwarp();
+        const int i = lane / nsl, sl = lane - i * nsl;
+        const int page = __shfl_sync(0xffffffffu, pg, (p0 + i) & 7);
+        if (lane < np * nsl)
+          tma_2d(smem_u32(ring + slot * C::kSlot + sl * nkeys * 128 + i * 2048), map, (slab0 + sl) * 64,
+                 page < 0 ? none : (page * a.pool.hkv + wk.h) * kPage, bar(ms.full[slot]));
+      } else {
+        const int slot = n % C::kRawSlots;
+        if (!wait(ms.raw_empty[slot], ((n / C::kRawSlots) & 1) ^ 1)) return false;
+        const uint32_t gone = __ballot_sync(0xffffffffu, lane < 8 && pg < 0);
+        const uint32_t mine = (gone >> p0) & ((1u << np) - 1);
+        constexpr int kScaleBytes = kPage * NS * 4;
+        if (lane == 0) {
+          ms.raw_pages[slot] = static_cast<int>(mine);
+          bar_expect(bar(ms.raw_full[slot]), nkeys * nsl * 64 + (np - __popc(mine)) * kScaleBytes);
+        }
+        __syncwarp();
+        const int nbx = nsl * 64 / C::kBox;
+        uint8_t* dst = raw + slot * C::kRaw;
+        {
+          const int i = lane / nbx, bx = lane - i * nbx;
+          const int page = __shfl_sync(0xffffffffu, pg, (p0 + i) & 7);
+          if (lane < np * nbx)
+            tma_2d(smem_u32(dst + lane * kPage * C::kBox), map, slab0 * 64 + bx * C::kBox,
+                   page < 0 ? none : (page * a.pool.hkv + wk.h) * kPage, bar(ms.raw_full[slot]));
+        }
+        const int page = __shfl_sync(0xffffffffu, pg, (p0 + lane) & 7);
+        if (lane < np && page >= 0)
+          bulk_copy(smem_u32(dst + C::kSlot / 2 + lane * kScaleBytes),
+                    static_cast<const uint8_t*>(kv ? a.pool.v_scale : a.pool.k_scale) +
+                        (static_cast<int64_t>(page) * a.pool.hkv + wk.h) * kScaleBytes,
+                    kScaleBytes, bar(ms.raw_full[slot]));
+      }
+      ++n;
+      return true;
+    };
+    while (ok && wk.next()) {
+      int pg = lane < 8 ? wk.page(wk.t.block(wk.b0), lane) : -1, pg_v = -1;
+      for (int i = wk.b0; ok && i <= wk.b1; ++i) {
+        const int pg_next = i + 1 < wk.b1 && lane < 8 ? wk.page(wk.t.block(i + 1), lane) : -1;
+        if (i < wk.b1)
+          for (int u = 0; ok && u < C::KU; ++u) ok = unit(0, u, pg);
+        if (i > wk.b0)
+          for (int u = 0; ok && u < C::VU; ++u) ok = unit(1, u, pg_v);
+        pg_v = pg;
+        pg = pg_next;
+      }
+    }
+    if (*dead) {  // let the copies in flight land before the block goes away
+      const int ns = Q8 ? C::kRawSlots : C::kSlots;
+      for (int k = max(0, n - ns); k < n; ++k) {
+        uint64_t& b = Q8 ? ms.raw_full[k % ns] : ms.full[k % ns];
+        const uint64_t t0 = now_ns();
+        while (!bar_try(bar(b), (k / ns) & 1) && now_ns() - t0 < 50000000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------- product issuer
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t kIdS = instr_desc(M, kBN, 0), kIdO = instr_desc(M, DH, 1);
+      const uint32_t qa = smem_u32(sq), ra = smem_u32(ring);
+      int n = 0, nb = 0;  // units and blocks consumed
+      bool ok = true;
+      auto scores = [&](int blk) {  // S[blk & 1] = Q K^T
+        bool first = true;
+        for (int u = 0; u < C::KU; ++u, ++n) {
+          const int slot = n % C::kSlots;
+          if (!wait1(ms.ready[slot], (n / C::kSlots) & 1)) return false;
+          tc_fence_after();
+          const uint32_t kb = ra + slot * C::kSlot;
+#pragma unroll
+          for (int sl = 0; sl < C::slabs_k(0); ++sl) {
+            if (sl >= C::slabs_k(u)) break;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              mma_ss<CG>(tm + 256 + (blk & 1) * kBN, smem_desc(qa + ((CG == 2 ? 0 : 2 * u) + sl) * 16384 + k * 32, 16, 1024),
+                         smem_desc(kb + sl * C::kKeysK * 128 + k * 32, 16, 1024), kIdS, !first);
+              first = false;
+            }
+          }
+          mma_commit<CG>(bar(ms.empty[slot]));
+        }
+        mma_commit<CG>(bar(ms.s_full[blk & 1]));
+        return true;
+      };
+      while (ok && wk.next()) {
+        ok = wait1(ms.q_ready, wk.seg & 1);
+        if (!ok) break;
+        tc_fence_after();
+        for (int i = wk.b0; i <= wk.b1; ++i) {
+          if (i < wk.b1) {
+            ok = scores(nb + (i - wk.b0));
+            if (!ok) break;
+            if (i + 1 == wk.b1) mma_commit<CG>(bar(ms.q_free));
+          }
+          if (i == wk.b0) continue;
+          const int blk = nb + (i - 1 - wk.b0);
+          ok = wait1(ms.p_ready[blk & 1], (blk >> 1) & 1);
+          if (!ok) break;
+          for (int u = 0; u < C::VU; ++u, ++n) {
+            const int slot = n % C::kSlots;
+            ok = wait1(ms.ready[slot], (n / C::kSlots) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t vb = ra + slot * C::kSlot;
+#pragma unroll
+            for (int k = 0; k < C::kKeysV / 16; ++k)
+              mma_ts<CG>(tm, tm + 256 + (blk & 1) * kBN + (u * C::kKeysV + k * 16) / 2,
+                         smem_desc(vb + k * 2048, C::kKeysV * 128, 1024), kIdO, !(i - 1 == wk.b0 && u == 0 && k == 0));
+            mma_commit<CG>(bar(ms.empty[slot]));
+          }
+          if (!ok) break;
+          mma_commit<CG>(bar(ms.pv_done));
+        }
+        nb += wk.b1 - wk.b0;
+      }
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------ softmax, results
+    const int wr = (warp & 3) * 32 + lane;  // row of this block's half of the tile
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane field
+    int nb = 0;
+    bool ok = true;
+    while (wk.next()) {
+      const int r = rank * 128 + wr, r_warp = rank * 128 + (warp & 3) * 32;
+      const bool valid = r < wk.t.rows, warp_valid = r_warp < wk.t.rows;
+      const int R0 = wk.mt * M, base_p = wk.v.kv_len - wk.v.q_len;
+      const int p = base_p + (R0 + min(r, wk.t.rows - 1)) / a.G;
+      const int wp0 = base_p + (R0 + min(r_warp, wk.t.rows - 1)) / a.G;
+      const int wp1 = base_p + (R0 + min(r_warp + 31, wk.t.rows - 1)) / a.G;
+      float m = valid ? -INFINITY : 0.f, l = 0.f, c = 0.f;
+      int gone_pg = lane < 8 ? wk.page(wk.t.block(wk.b0), lane) : 0;
+      for (int i = wk.b0; ok && i < wk.b1; ++i, ++nb) {
+        const int b = wk.t.block(i);
+        const uint32_t gone = __ballot_sync(0xffffffffu, gone_pg < 0) & 0xffu;
+        if (i + 1 < wk.b1 && lane < 8) gone_pg = wk.page(wk.t.block(i + 1), lane);
+        ok = wait(ms.s_full[nb & 1], (nb >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (warp_valid) {
+          if (i == wk.b0 && valid) c = ms.qc[wk.seg & 3][wr];
+          const uint32_t sa = tm + lanes + 256 + (nb & 1) * kBN;
+          const bool part = gone || !block_full(b, wp0, wp1, a.window, a.sinks);
+          uint32_t x[32];
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            tmem_ld32(sa + 32 * k, x);
+            tmem_wait_ld(x);
+            if (part) {
+              uint32_t see = seen_bits(p, b * kBN + 32 * k, a.window, a.sinks);
+              if (gone >> (2 * k) & 1) see &= 0xffff0000u;
+              if (gone >> (2 * k) & 2) see &= 0x0000ffffu;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!(see >> j & 1)) x[j] = 0xff800000u;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(x[j]));
+          }
+          mx *= c;  // c > 0
+          const bool move = mx > m + 8.f;
+          if (__any_sync(0xffffffffu, move)) {
+            const float nm = fmaxf(m, mx);
+            const float f = nm == -INFINITY ? 1.f : ex2(m - nm);
+            m = nm;
+            l *= f;
+            if (i > wk.b0) {  // rescale O, once the product before is done (these scores show that those before it are)
+              ok = wait(ms.pv_done, (nb - 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int k = 0; k < DH / 32; ++k) {
+                tmem_ld32(tm + lanes + 32 * k, x);
+                tmem_wait_ld(x);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
+                tmem_st32(tm + lanes + 32 * k, x);
+              }
+            }
+          }
+          const float mm = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            tmem_ld32(sa + 32 * k, x);
+            tmem_wait_ld(x);
+            if (part) {
+              uint32_t see = seen_bits(p, b * kBN + 32 * k, a.window, a.sinks);
+              if (gone >> (2 * k) & 1) see &= 0xffff0000u;
+              if (gone >> (2 * k) & 2) see &= 0x0000ffffu;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!(see >> j & 1)) x[j] = 0xff800000u;
+            }
+            uint32_t h[16];
+            float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float e0 = ex2(fmaf(__uint_as_float(x[2 * j]), c, -mm)), e1 = ex2(fmaf(__uint_as_float(x[2 * j + 1]), c, -mm));
+              l0 += e0;
+              l1 += e1;
+              h[j] = pack_half2(e0, e1);
+            }
+            l += l0 + l1;
+            tmem_st16(sa + 16 * k, h);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) lead_arrive(ms.p_ready[nb & 1]);
+      }
+      // the result of the segment: O, once its last product is done. A parity
+      // says which of two phases is meant, and the last scores only show that
+      // the product three blocks back is done: wait for the last but one first.
+      if (ok && wk.b1 - wk.b0 > 1) ok = wait(ms.pv_done, (nb - 2) & 1);
+      if (ok) ok = wait(ms.pv_done, (nb - 1) & 1);
+      if (!warp_valid) continue;
+      tc_fence_after();
+      const bool whole = wk.whole();
+      const int slot = 2 * worker + (wk.seg == 0 ? 0 : 1);
+      const int R = R0 + r, row = wk.v.r0 + R / a.G, head = wk.h * a.G + R % a.G;
+      const bool patch = *const_cast<volatile int*>(&ms.flag[wk.seg & 3]) == wk.seg + 1;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (!whole && valid) a.ml[slot * M + r] = ok ? make_float2(m, l) : make_float2(0.f, NAN);
+#pragma unroll 1
+      for (int k = 0; k < DH / 32; ++k) {
+        uint32_t x[32];
+        float y[32];
+        if (ok) {
+          tmem_ld32(tm + lanes + 32 * k, x);
+          tmem_wait_ld(x);
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) y[j] = ok ? __uint_as_float(x[j]) : NAN;
+        if (valid && ok && patch) {
+          // rows that see a cleared value add it: +-inf or NaN whatever its weight
+          for (int i = wk.b0; i < wk.b1; ++i) {
+            const int b = wk.t.block(i);
+            for (int t = 0; t < kBN; ++t) {
+              const int pg = wk.page(b, t / kPage);
+              if (pg < 0 || !(seen_bits(p, b * kBN + (t & ~31), a.window, a.sinks) >> (t & 31) & 1)) continue;
+              const int64_t e = ((static_cast<int64_t>(pg) * a.pool.hkv + wk.h) * kPage + t % kPage) * DH + 32 * k;
+              if (Q8) {
+                const float d = __half2float(static_cast<const __half*>(a.pool.v_scale)[e / 32]);
+                if (isfinite(d)) continue;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) y[j] += d * static_cast<float>(static_cast<const int8_t*>(a.pool.v)[e + j]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  const float d = __half2float(static_cast<const __half*>(a.pool.v)[e + j]);
+                  if (!isfinite(d)) y[j] += d;
+                }
+              }
+            }
+          }
+        }
+        if (valid && !whole) {
+          float4* dst = reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(slot) * M + r) * DH + 32 * k);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dst[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+        } else if (valid) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) y[j] = !ok ? NAN : l == 0.f ? 0.f : y[j] * inv;
+          put_out<32>(a, row, head, 32 * k, y);
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------ operand preparing
+    const int pw = warp - 8, pt = tid - 256;
+    constexpr int kPT = C::kPrep * 32;
+    int n = 0;
+    bool ok = true;
+    // unit u of K or V of block b: hand it over, converted (q8) and cleared (V of a partly seen block)
+    auto unit = [&](int kv, int u, int b) {
+      const int nkeys = kv ? C::kKeysV : C::kKeysK, nsl = kv ? C::kSlabsV : C::slabs_k(u);
+      const int key0 = CG == 2 ? (kv ? 0 : 64 * rank) : (kv ? u * C::kKeysV : 0);
+      const int slab0 = CG == 2 ? (kv ? rank * C::kSlabsV : 0) : (kv ? 0 : 2 * u);
+      const int slot = n % C::kSlots;
+      uint8_t* const dst = ring + slot * C::kSlot;
+      bool found = false;
+      const bool partly = kv && !block_full(b, wk.t.p0, wk.t.p1, a.window, a.sinks);
+      if constexpr (!Q8) {
+        if (!wait(ms.full[slot], (n / C::kSlots) & 1)) return false;
+        if (partly) {
+          const int end = wk.v.kv_len - b * kBN - key0;  // tokens from here on do not exist
+          for (int q = pt; q < nkeys * nsl * 8; q += kPT) {
+            uint4* ptr = reinterpret_cast<uint4*>(dst + q * 16);
+            uint4 x = *ptr;
+            const int key = (q / 8) % nkeys;
+            if (key >= end) {
+              x = make_uint4(0, 0, 0, 0);
+            } else {
+              uint32_t* w = &x.x;
+              bool bad = false;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if ((w[j] & 0x7c00u) == 0x7c00u) { w[j] &= 0xffff0000u; bad = true; }
+                if ((w[j] & 0x7c000000u) == 0x7c000000u) { w[j] &= 0x0000ffffu; bad = true; }
+              }
+              found |= bad;
+            }
+            *ptr = x;
+          }
+          fence_async_shared();
+        }
+      } else {
+        const int rs = n % C::kRawSlots;
+        if (!wait(ms.raw_full[rs], (n / C::kRawSlots) & 1)) return false;
+        if (!wait(ms.empty[slot], ((n / C::kSlots) & 1) ^ 1)) return false;
+        const uint8_t* src = raw + rs * C::kRaw;
+        const __half* sc = reinterpret_cast<const __half*>(src + C::kSlot / 2);
+        const uint32_t gone = static_cast<uint32_t>(ms.raw_pages[rs]);
+        const int end = partly ? wk.v.kv_len - b * kBN - key0 : nkeys;
+        constexpr int kBC = C::kBox / 16;  // 16-code chunks per box row
+        const int nbx = nsl * 64 / C::kBox;
+#pragma unroll 2
+        for (int q = pt; q < nkeys * nsl * 4; q += kPT) {
+          const uint4 codes = *reinterpret_cast<const uint4*>(src + q * 16);
+          const int cc = q % kBC, tok = (q / kBC) % kPage, pb = q / (kBC * kPage);
+          const int page = pb / nbx, key = page * kPage + tok, dim = (pb - page * nbx) * C::kBox + cc * 16;
+          __half d = sc[key * (2 * NS) + (slab0 * 64 + dim) / 32];
+          uint32_t o[8];
+          const uint32_t* cw = &codes.x;
+          if ((gone >> page & 1) || (kv && (key >= end || (partly && (__half_as_ushort(d) & 0x7c00u) == 0x7c00u)))) {
+            found |= !(gone >> page & 1) && key < end;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = 0;
+          } else {
+            const __half2 d2 = __half2half2(d), off = __half2half2(__ushort_as_half(0x6480));  // 1152
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t w = cw[j] ^ 0x80808080u;  // code + 128; 0x6400 | byte is 1024 + byte
+              const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
+              const __half2 a2 = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&lo), off), d2);
+              const __half2 b2 = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&hi), off), d2);
+              o[2 * j] = *reinterpret_cast<const uint32_t*>(&a2);
+              o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+          }
+          const int sl = dim / 64, ch = (dim % 64) / 8;
+          uint8_t* row = dst + sl * nkeys * 128 + key * 128;
+          *reinterpret_cast<uint4*>(row + ((ch ^ (key & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (key & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(ms.raw_empty[rs]));
+        fence_async_shared();
+      }
+      if (found) {
+        if (CG == 1) {
+          *const_cast<volatile int*>(&ms.flag[wk.seg & 3]) = wk.seg + 1;
+        } else {
+          for (int k = 0; k < 2; ++k) st_cluster(peer_addr(smem_u32(&ms.flag[wk.seg & 3]), k), wk.seg + 1);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) lead_arrive(ms.ready[slot]);
+      ++n;
+      return true;
+    };
+    while (ok && wk.next()) {
+      // Q of the tile, once the products of the segment before no longer read it
+      ok = wk.seg == 0 || wait(ms.q_free, (wk.seg - 1) & 1);
+      if (!ok) break;
+      constexpr int kLPR = NS == 3 ? 32 : 8 * NS;  // lanes per row
+      constexpr int kRPP = 32 / kLPR;              // rows per warp and pass
+      const int ch = lane % kLPR, R0 = wk.mt * M + rank * 128;
+      const int rows = min(128, wk.t.rows - rank * 128);
+#pragma unroll 4
+      for (int r = pw * kRPP + lane / kLPR; r - lane / kLPR < rows; r += C::kPrep * kRPP) {
+        const int rr = min(r, rows - 1);
+        const int R = R0 + rr;
+        const int64_t off = (wk.v.r0 + R / a.G) * a.q.row_stride + (wk.h * a.G + R % a.G) * a.q.head_stride + ch * 8;
+        uint32_t o[4] = {0, 0, 0, 0};
+        float qc = a.c;
+        if (a.dtype == MK_F16) {
+          if (ch < 8 * NS) {
+            const __half* qp = static_cast<const __half*>(a.q.data) + off;
+            if (a.vq) {
+              const uint4 x = __ldg(reinterpret_cast<const uint4*>(qp));
+              o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                o[j] = static_cast<uint32_t>(__half_as_ushort(qp[2 * j])) |
+                       static_cast<uint32_t>(__half_as_ushort(qp[2 * j + 1])) << 16;
+            }
+          }
+        } else {
+          // bf16: the row times a power of two that brings its largest value to [1, 2)
+          float x[8] = {};
+          if (ch < 8 * NS) {
+            const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q.data) + off;
+            if (a.vq) load8<MK_BF16, true>(qp, x); else load8<MK_BF16, false>(qp, x);
+          }
+          float mx = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(x[j]));
+#pragma unroll
+          for (int k = kLPR / 2; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+          int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+          if (e > 127 || mx == 0.f) e = 0;   // infinities stay, zero rows too
+          e = max(-100, min(100, e));
+          const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          // (kept normal and finite, so that -inf x c is -inf)
+          qc = fminf(fmaxf(a.c * __uint_as_float(static_cast<uint32_t>(127 + e) << 23), 1.2e-38f), 3e38f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = pack_half2(x[2 * j] * f, x[2 * j + 1] * f);
+        }
+        if (ch < 8 * NS && r < rows)
+          *reinterpret_cast<uint4*>(sq + (ch / 8) * 16384 + r * 128 + (((ch % 8) ^ (r & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+        if (ch == 0 && r < rows) ms.qc[wk.seg & 3][r] = qc;
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) lead_arrive(ms.q_ready);
+      for (int i = wk.b0; ok && i <= wk.b1; ++i) {
+        if (i < wk.b1)
+          for (int u = 0; ok && u < C::KU; ++u) ok = unit(0, u, wk.t.block(i));
+        if (i > wk.b0)
+          for (int u = 0; ok && u < C::VU; ++u) ok = unit(1, u, wk.t.block(i - 1));
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (warp == 1) tmem_free<CG>(tm, 512);
+}
+
+// ------------------------------------------------------------------- launch
+// Blocks (pairs) that are resident at once, found once per device; 0 on error.
+template <int NS, bool Q8, int CG>
+int resident_workers(int device) {
+  using C = Cfg<NS, Q8, CG>;
+  static std::atomic<int> known[64];
+  if (device < 0 || device >= 64) return 0;
+  int n = known[device].load();
+  if (n) return n;
+  const auto fn = attend_kernel<NS, Q8, CG>;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return 0;
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return 0;
+  n = sms;
+  if (CG == 2) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {2, 1, 1};
+    cfg.gridDim = dim3(2 * (sms / 2));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) return 0;
+  }
+  if (n > kMaxWorkers / CG) n = kMaxWorkers / CG;
+  known[device].store(n);
+  return n;
+}
+
+template <int NS, bool Q8, int CG>
+cudaError_t launch_attend(AttendParams a, const CUtensorMap& tk, const CUtensorMap& tv, int device, cudaStream_t stream) {
+  using C = Cfg<NS, Q8, CG>;
+  a.workers = resident_workers<NS, Q8, CG>(device);
+  if (!a.workers) {
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? cudaErrorInvalidDevice : e;
+  }
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {CG, 1, 1};
+  cfg.gridDim = dim3(a.workers * CG);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel<NS, Q8, CG>, a, tk, tv);
+  if (e != cudaSuccess) return e;
+  attend_join<NS, CG><<<dim3(a.workers, 4), 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <bool Q8>
+cudaError_t launch_any(int ns, int cg, const AttendParams& a, const CUtensorMap& tk, const CUtensorMap& tv, int device,
+                       cudaStream_t stream) {
+  switch (ns * 2 + (cg - 1)) {
+    case 2: return launch_attend<1, Q8, 1>(a, tk, tv, device, stream);
+    case 4: return launch_attend<2, Q8, 1>(a, tk, tv, device, stream);
+    case 5: return launch_attend<2, Q8, 2>(a, tk, tv, device, stream);
+    case 6: return launch_attend<3, Q8, 1>(a, tk, tv, device, stream);
+    case 8: return launch_attend<4, Q8, 1>(a, tk, tv, device, stream);
+    case 9: return launch_attend<4, Q8, 2>(a, tk, tv, device, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace ops
+}  // namespace mk
