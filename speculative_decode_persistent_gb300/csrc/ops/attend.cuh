@@ -25,8 +25,9 @@
 // in a fixed order: results do not depend on timing. Every worker finds its
 // piece from the lengths on the device, so nothing is planned on the host.
 //
-// Warps: 0 copies pages, 1 issues products, 4-7 take the softmax (thread =
-// row) and write results, 8.. prepare operands: they load Q, turn q8 codes
+// Warps: 0-7 take the softmax and write results (two threads a row, 64 tokens
+// each, so that a block's softmax is shorter than its products), 8 copies
+// pages, 9 issues products, 10-15 prepare operands: they load Q, turn q8 codes
 // into binary16 tiles, and clear what must not enter a product (below).
 //
 // Unseen values. A masked score is replaced before the softmax, so K may hold
@@ -41,6 +42,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "ops_internal.cuh"
 #include "sm103.cuh"
@@ -181,31 +183,39 @@ struct Cfg {
   static constexpr int kUnitK = kKeysK * slabs_k(0) * 128, kUnitV = kKeysV * kSlabsV * 128;
   static constexpr int kSlot = kUnitK > kUnitV ? kUnitK : kUnitV;
   static constexpr int kQ = NS * 16384;
-  static constexpr int kMisc = 5120;
+  static constexpr int kMisc = 3072;
   static constexpr int kRaw = kSlot / 2 + 128 * NS * 4;  // q8 codes, then 2 NS scales per token
-  static constexpr int kBudget = 232448 - 1024 - kMisc - kQ;
-  static constexpr int kRawSlots = Q8 ? 3 : 0;
-  static constexpr int kFit = (kBudget - kRawSlots * kRaw) / kSlot;
-  static constexpr int kSlots = kFit > 8 ? 8 : kFit;
+  static constexpr int kBudget = 232448 - kMisc - kQ;
+  // binary16 pool: all room for operand units. q8: units as stored are what is
+  // in flight from memory, so two operand units are kept and the rest is for those.
+  static constexpr int kFit = kBudget / kSlot;
+  static constexpr int kSlots = Q8 ? 2 : kFit > 8 ? 8 : kFit;
+  static constexpr int kRawFit = (kBudget - kSlots * kSlot) / kRaw / 2 * 2;
+  static constexpr int kRawSlots = !Q8 ? 0 : kRawFit > 6 ? 6 : kRawFit;
   static constexpr int kBox = q8_box(NS, CG);
-  static constexpr int kPrep = Q8 ? 8 : 4;        // preparing warps
-  static constexpr int kThreads = 256 + 32 * kPrep;
-  static constexpr int kSmem = 1024 + kMisc + kQ + kSlots * kSlot + kRawSlots * kRaw;
-  static_assert(kSlots >= 3, "ring");
+  static constexpr int kSmem = kMisc + kQ + kSlots * kSlot + kRawSlots * kRaw;
+  static_assert(kSlots >= 2 && (!Q8 || kRawSlots >= 4) && kSmem <= 232448, "ring");
+  // a preparing group must see every phase of the slots it waits on: slot parity is its own
+  static_assert(!Q8 || (kSlots % 2 == 0 && kRawSlots % 2 == 0), "groups");
   static_assert(!Q8 || (slabs_k(0) * 64 % kBox == 0 && kSlabsV * 64 % kBox == 0), "boxes");
 };
 
+constexpr int kWarpCopy = 8, kWarpMma = 9, kWarpPrep = 10;
+constexpr int kPrep = 6;        // preparing warps, in two groups that share the units
+constexpr int kThreads = 32 * (kWarpPrep + kPrep);
+
 struct Misc {
-  uint64_t ready[8], full[8], empty[8], raw_full[4], raw_empty[4];
+  uint64_t ready[8], full[8], empty[8], raw_full[6], raw_empty[6];
   uint64_t s_full[2], p_ready[2], pv_done, q_ready, q_free;
   uint32_t tmem;
   int dead;
   Start start;
   int flag[4];           // segment + 1 in which non-finite V values were cleared
-  int raw_pages[4];      // bit i: page i of a raw unit is missing
-  float qc[4][128];      // per row: scale x log2(e) x 2^e of the row's query
+  int raw_pages[6];      // bit i: page i of a raw unit is missing
+  int8_t qe[4][128];     // per row: the power of two its query was divided by
+  float swap[2][2][128];  // [block parity][half]: the halves' maxima, at the end their sums
 };
-static_assert(sizeof(Misc) <= 5120, "misc area");
+static_assert(sizeof(Misc) <= 3072, "misc area");
 
 // Output of eight or more neighbouring dims: gate, rounding, store.
 template <int N>
@@ -271,10 +281,23 @@ __device__ void find_start(const AttendParams& a, int64_t* scratch, Start* out, 
   // the sequence whose blocks hold g0, then the head, then the tile
   int64_t at = 0, cost = 0;
   int s = 0;
-  for (;; ++s) {
-    cost = scratch[s];
-    if (g0 < at + cost * a.pool.hkv) break;
-    at += cost * a.pool.hkv;
+  for (;; s += 32) {  // (g0 < total, so one of them holds it)
+    cost = s + lane < a.rows.n_seqs ? scratch[s + lane] : 0;
+    int64_t inc = cost * a.pool.hkv;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, k);
+      if (lane >= k) inc += y;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, g0 < at + inc);
+    const int l = hit ? __ffs(hit) - 1 : 31;
+    if (hit) {
+      at += __shfl_sync(0xffffffffu, inc - cost * a.pool.hkv, l);
+      cost = __shfl_sync(0xffffffffu, cost, l);
+      s += l;
+      break;
+    }
+    at += __shfl_sync(0xffffffffu, inc, 31);
   }
   const SeqView v = seq_view(a.rows, s);
   const int h = static_cast<int>((g0 - at) / cost);
@@ -325,6 +348,7 @@ __device__ void find_start(const AttendParams& a, int64_t* scratch, Start* out, 
 template <int NS, int CG>
 __global__ void __launch_bounds__(256) attend_join(const AttendParams a) {
   constexpr int DH = NS * 64, M = 128 * CG, kPer = DH / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched early: the parts are written from here on
   const JoinInfo j = a.join[blockIdx.x];
   if (j.w0 < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -374,13 +398,12 @@ __global__ void __launch_bounds__(256) attend_join(const AttendParams a) {
 }
 
 template <int NS, bool Q8, int CG>
-__global__ void __launch_bounds__(Cfg<NS, Q8, CG>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ AttendParams a, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv) {
   using C = Cfg<NS, Q8, CG>;
   constexpr int M = C::M, DH = C::DH;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const sq = smem;                          // Q [NS][128 rows][128 B], swizzled
   uint8_t* const ring = sq + C::kQ;                  // operand units
   uint8_t* const raw = ring + C::kSlots * C::kSlot;  // q8 units as stored
@@ -400,25 +423,25 @@ __global__ void __launch_bounds__(Cfg<NS, Q8, CG>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       bar_init(bar(ms.full[i]), 1);
-      bar_init(bar(ms.ready[i]), CG * C::kPrep);
+      bar_init(bar(ms.ready[i]), CG * kPrep / 2);
       bar_init(bar(ms.empty[i]), 1);
     }
     for (int i = 0; i < C::kRawSlots; ++i) {
       bar_init(bar(ms.raw_full[i]), 1);
-      bar_init(bar(ms.raw_empty[i]), C::kPrep);
+      bar_init(bar(ms.raw_empty[i]), kPrep / 2);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(bar(ms.s_full[i]), 1);
-      bar_init(bar(ms.p_ready[i]), 4 * CG);
+      bar_init(bar(ms.p_ready[i]), 8 * CG);
     }
     bar_init(bar(ms.pv_done), 1);
-    bar_init(bar(ms.q_ready), CG * C::kPrep);
+    bar_init(bar(ms.q_ready), CG * kPrep);
     bar_init(bar(ms.q_free), 1);
-    ms.dead = 0;
+    ms.dead = (smem_u32(smem) & 1023u) != 0;  // (the swizzled tiles need the alignment)
     for (int i = 0; i < 4; ++i) ms.flag[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tmem_alloc<CG>(smem_u32(&ms.tmem), 512);
+  if (warp == kWarpMma) tmem_alloc<CG>(smem_u32(&ms.tmem), 512);
   find_start<M>(a, reinterpret_cast<int64_t*>(ring), &ms.start, worker, rank == 0);
   tc_fence_before();
   fence_async_shared();  // the scratch lay where tensor copies go
@@ -426,9 +449,10 @@ __global__ void __launch_bounds__(Cfg<NS, Q8, CG>::kThreads, 1)
   if (CG == 2) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   tc_fence_after();
   const uint32_t tm = ms.tmem;
+  asm volatile("griddepcontrol.launch_dependents;");
   Walk wk(a, ms.start, M);
 
-  if (warp == 0) {
+  if (warp == kWarpCopy) {
     // ------------------------------------------------------------ page copies
     int n = 0;       // units issued
     bool ok = true;
@@ -492,7 +516,9 @@ __global__ void __launch_bounds__(Cfg<NS, Q8, CG>::kThreads, 1)
         pg = pg_next;
       }
     }
-    if (*dead) {  // let the copies in flight land before the block goes away
+    {
+      // no copy may be in flight when the block goes away (the last units' ones
+      // have landed unless a wait gave up): at most one phase per slot is open
       const int ns = Q8 ? C::kRawSlots : C::kSlots;
       for (int k = max(0, n - ns); k < n; ++k) {
         uint64_t& b = Q8 ? ms.raw_full[k % ns] : ms.full[k % ns];
@@ -501,7 +527,7 @@ __global__ void __launch_bounds__(Cfg<NS, Q8, CG>::kThreads, 1)
         }
       }
     }
-  } else if (warp == 1) {
+  } else if (warp == kWarpMma) {
     // -------------------------------------------------------- product issuer
     if (rank == 0 && lane == 0) {
       constexpr uint32_t kIdS = instr_desc(M, kBN, 0), kIdO = instr_desc(M, DH, 1);
@@ -562,95 +588,109 @@ __global__ void __launch_bounds__(Cfg<NS, Q8, CG>::kThreads, 1)
         nb += wk.b1 - wk.b0;
       }
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp < 8) {
     // ------------------------------------------------------ softmax, results
-    const int wr = (warp & 3) * 32 + lane;  // row of this block's half of the tile
-    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane field
+    // Threads of warps w and w + 4 share a row: half 0 takes tokens 0-63 of a
+    // block and the first half of the dims, half 1 the others. A wait that
+    // gave up does not end the loop, so that the halves keep meeting.
+    const int half = warp >> 2, quad = warp & 3;
+    const int wr = quad * 32 + lane;  // row of this block's half of the tile
+    const uint32_t lanes = static_cast<uint32_t>(quad) << 21;  // TMEM lane field
     int nb = 0;
     bool ok = true;
     while (wk.next()) {
-      const int r = rank * 128 + wr, r_warp = rank * 128 + (warp & 3) * 32;
+      const int r = rank * 128 + wr, r_warp = rank * 128 + quad * 32;
       const bool valid = r < wk.t.rows, warp_valid = r_warp < wk.t.rows;
       const int R0 = wk.mt * M, base_p = wk.v.kv_len - wk.v.q_len;
       const int p = base_p + (R0 + min(r, wk.t.rows - 1)) / a.G;
       const int wp0 = base_p + (R0 + min(r_warp, wk.t.rows - 1)) / a.G;
       const int wp1 = base_p + (R0 + min(r_warp + 31, wk.t.rows - 1)) / a.G;
       float m = valid ? -INFINITY : 0.f, l = 0.f, c = 0.f;
-      int gone_pg = lane < 8 ? wk.page(wk.t.block(wk.b0), lane) : 0;
-      for (int i = wk.b0; ok && i < wk.b1; ++i, ++nb) {
+      int gone_pg = lane < 4 ? wk.page(wk.t.block(wk.b0), 4 * half + lane) : 0;
+      for (int i = wk.b0; i < wk.b1; ++i, ++nb) {
         const int b = wk.t.block(i);
-        const uint32_t gone = __ballot_sync(0xffffffffu, gone_pg < 0) & 0xffu;
-        if (i + 1 < wk.b1 && lane < 8) gone_pg = wk.page(wk.t.block(i + 1), lane);
-        ok = wait(ms.s_full[nb & 1], (nb >> 1) & 1);
-        if (!ok) break;
+        const uint32_t gone = __ballot_sync(0xffffffffu, gone_pg < 0) & 0xfu;
+        if (i + 1 < wk.b1 && lane < 4) gone_pg = wk.page(wk.t.block(i + 1), 4 * half + lane);
+        ok &= wait(ms.s_full[nb & 1], (nb >> 1) & 1);
         tc_fence_after();
         if (warp_valid) {
-          if (i == wk.b0 && valid) c = ms.qc[wk.seg & 3][wr];
+          if (i == wk.b0 && valid)  // scale x log2(e) x 2^e, kept normal and finite so that -inf x c is -inf
+            c = fminf(fmaxf(a.c * __uint_as_float(static_cast<uint32_t>(127 + ms.qe[wk.seg & 3][wr]) << 23), 1.2e-38f), 3e38f);
           const uint32_t sa = tm + lanes + 256 + (nb & 1) * kBN;
-          const bool part = gone || !block_full(b, wp0, wp1, a.window, a.sinks);
-          uint32_t x[32];
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            tmem_ld32(sa + 32 * k, x);
-            tmem_wait_ld(x);
-            if (part) {
-              uint32_t see = seen_bits(p, b * kBN + 32 * k, a.window, a.sinks);
-              if (gone >> (2 * k) & 1) see &= 0xffff0000u;
-              if (gone >> (2 * k) & 2) see &= 0x0000ffffu;
+          uint32_t x[32], y[32];
+          tmem_ld32(sa + 64 * half, x);
+          tmem_ld32(sa + 64 * half + 32, y);
+          tmem_wait_ld(x);
+          tmem_wait_ld(y);
+          if (gone || !block_full(b, wp0, wp1, a.window, a.sinks)) {
+            uint32_t sx = seen_bits(p, b * kBN + 64 * half, a.window, a.sinks);
+            uint32_t sy = seen_bits(p, b * kBN + 64 * half + 32, a.window, a.sinks);
+            if (gone & 1) sx &= 0xffff0000u;
+            if (gone & 2) sx &= 0x0000ffffu;
+            if (gone & 4) sy &= 0xffff0000u;
+            if (gone & 8) sy &= 0x0000ffffu;
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(see >> j & 1)) x[j] = 0xff800000u;
+            for (int j = 0; j < 32; ++j) {
+              if (!(sx >> j & 1)) x[j] = 0xff800000u;
+              if (!(sy >> j & 1)) y[j] = 0xff800000u;
             }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(x[j]));
           }
-          mx *= c;  // c > 0
-          const bool move = mx > m + 8.f;
-          if (__any_sync(0xffffffffu, move)) {
-            const float nm = fmaxf(m, mx);
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            mx[j & 2] = fmaxf(fmaxf(mx[j & 2], __uint_as_float(x[j])), __uint_as_float(x[j + 1]));
+            mx[(j & 2) + 1] = fmaxf(fmaxf(mx[(j & 2) + 1], __uint_as_float(y[j])), __uint_as_float(y[j + 1]));
+          }
+          float my = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;  // c > 0
+          ms.swap[nb & 1][half][wr] = my;
+          named_sync(1 + quad, 64);  // and both halves' scores are in registers: P may overwrite them
+          my = fmaxf(my, ms.swap[nb & 1][half ^ 1][wr]);
+          if (__any_sync(0xffffffffu, my > m + 8.f)) {  // the same in both halves
+            const float nm = fmaxf(m, my);
             const float f = nm == -INFINITY ? 1.f : ex2(m - nm);
             m = nm;
             l *= f;
             if (i > wk.b0) {  // rescale O, once the product before is done (these scores show that those before it are)
-              ok = wait(ms.pv_done, (nb - 1) & 1);
-              if (!ok) break;
+              ok &= wait(ms.pv_done, (nb - 1) & 1);
               tc_fence_after();
+              uint32_t z[32];
 #pragma unroll 1
-              for (int k = 0; k < DH / 32; ++k) {
-                tmem_ld32(tm + lanes + 32 * k, x);
-                tmem_wait_ld(x);
+              for (int k = half * NS; k < half * NS + NS; ++k) {
+                tmem_ld32(tm + lanes + 32 * k, z);
+                tmem_wait_ld(z);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
-                tmem_st32(tm + lanes + 32 * k, x);
+                for (int j = 0; j < 32; ++j) z[j] = __float_as_uint(__uint_as_float(z[j]) * f);
+                tmem_st32(tm + lanes + 32 * k, z);
               }
             }
           }
           const float mm = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            tmem_ld32(sa + 32 * k, x);
-            tmem_wait_ld(x);
-            if (part) {
-              uint32_t see = seen_bits(p, b * kBN + 32 * k, a.window, a.sinks);
-              if (gone >> (2 * k) & 1) see &= 0xffff0000u;
-              if (gone >> (2 * k) & 2) see &= 0x0000ffffu;
+          const uint64_t c2 = pack2(c, c), m2 = pack2(-mm, -mm);
+          uint64_t l2 = pack2(0.f, 0.f), l3 = l2;
+          uint32_t h[16];
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(see >> j & 1)) x[j] = 0xff800000u;
-            }
-            uint32_t h[16];
-            float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float e0 = ex2(fmaf(__uint_as_float(x[2 * j]), c, -mm)), e1 = ex2(fmaf(__uint_as_float(x[2 * j + 1]), c, -mm));
-              l0 += e0;
-              l1 += e1;
-              h[j] = pack_half2(e0, e1);
-            }
-            l += l0 + l1;
-            tmem_st16(sa + 16 * k, h);
+          for (int j = 0; j < 16; ++j) {
+            float e0, e1;
+            unpack2(fma2(pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), c2, m2), e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            l2 = add2(l2, pack2(e0, e1));
+            h[j] = pack_half2(e0, e1);
           }
+          tmem_st16(sa + 32 * half, h);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float e0, e1;
+            unpack2(fma2(pack2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])), c2, m2), e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            l3 = add2(l3, pack2(e0, e1));
+            h[j] = pack_half2(e0, e1);
+          }
+          tmem_st16(sa + 32 * half + 16, h);
+          float a0, a1;
+          unpack2(add2(l2, l3), a0, a1);
+          l += a0 + a1;
           tmem_wait_st();
         }
         tc_fence_before();
@@ -660,24 +700,26 @@ __global__ void __launch_bounds__(Cfg<NS, Q8, CG>::kThreads, 1)
       // the result of the segment: O, once its last product is done. A parity
       // says which of two phases is meant, and the last scores only show that
       // the product three blocks back is done: wait for the last but one first.
-      if (ok && wk.b1 - wk.b0 > 1) ok = wait(ms.pv_done, (nb - 2) & 1);
-      if (ok) ok = wait(ms.pv_done, (nb - 1) & 1);
+      if (wk.b1 - wk.b0 > 1) ok &= wait(ms.pv_done, (nb - 2) & 1);
+      ok &= wait(ms.pv_done, (nb - 1) & 1);
       if (!warp_valid) continue;
       tc_fence_after();
+      ms.swap[nb & 1][half][wr] = l;  // (read there last two blocks ago)
+      named_sync(1 + quad, 64);
+      l += ms.swap[nb & 1][half ^ 1][wr];
+      named_sync(1 + quad, 64);
       const bool whole = wk.whole();
       const int slot = 2 * worker + (wk.seg == 0 ? 0 : 1);
       const int R = R0 + r, row = wk.v.r0 + R / a.G, head = wk.h * a.G + R % a.G;
       const bool patch = *const_cast<volatile int*>(&ms.flag[wk.seg & 3]) == wk.seg + 1;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      if (!whole && valid) a.ml[slot * M + r] = ok ? make_float2(m, l) : make_float2(0.f, NAN);
+      if (!whole && valid && half == 0) a.ml[slot * M + r] = ok ? make_float2(m, l) : make_float2(0.f, NAN);
 #pragma unroll 1
-      for (int k = 0; k < DH / 32; ++k) {
+      for (int k = half * NS; k < half * NS + NS; ++k) {
         uint32_t x[32];
         float y[32];
-        if (ok) {
-          tmem_ld32(tm + lanes + 32 * k, x);
-          tmem_wait_ld(x);
-        }
+        tmem_ld32(tm + lanes + 32 * k, x);
+        tmem_wait_ld(x);
 #pragma unroll
         for (int j = 0; j < 32; ++j) y[j] = ok ? __uint_as_float(x[j]) : NAN;
         if (valid && ok && patch) {
@@ -716,69 +758,85 @@ __global__ void __launch_bounds__(Cfg<NS, Q8, CG>::kThreads, 1)
       }
       tc_fence_before();
     }
-  } else if (warp >= 8) {
+  } else {
     // ------------------------------------------------------ operand preparing
-    const int pw = warp - 8, pt = tid - 256;
-    constexpr int kPT = C::kPrep * 32;
+    // Group g takes the units in slots of that parity. A wait tells two phases
+    // of a barrier apart, no more: a group that took every other unit of a
+    // slot could mistake the phase before the last for the one it waits for.
+    const int pw = warp - kWarpPrep, group = pw & 1;
+    const int pt = (pw >> 1) * 32 + lane;               // thread of its group
+    constexpr int kPT = kPrep / 2 * 32;
     int n = 0;
     bool ok = true;
     // unit u of K or V of block b: hand it over, converted (q8) and cleared (V of a partly seen block)
-    auto unit = [&](int kv, int u, int b) {
+    auto unit = [&](auto kvc, int u, int b) {
+      constexpr int kv = decltype(kvc)::value;
+      const int slot = n % C::kSlots, phase = (n / C::kSlots) & 1;
+      [[maybe_unused]] const int rs = Q8 ? n % C::kRawSlots : 0, rphase = Q8 ? (n / C::kRawSlots) & 1 : 0;
+      ++n;
+      if ((slot & 1) != group) return true;
       const int nkeys = kv ? C::kKeysV : C::kKeysK, nsl = kv ? C::kSlabsV : C::slabs_k(u);
       const int key0 = CG == 2 ? (kv ? 0 : 64 * rank) : (kv ? u * C::kKeysV : 0);
-      const int slab0 = CG == 2 ? (kv ? rank * C::kSlabsV : 0) : (kv ? 0 : 2 * u);
-      const int slot = n % C::kSlots;
+      [[maybe_unused]] const int slab0 = CG == 2 ? (kv ? rank * C::kSlabsV : 0) : (kv ? 0 : 2 * u);
       uint8_t* const dst = ring + slot * C::kSlot;
       bool found = false;
       const bool partly = kv && !block_full(b, wk.t.p0, wk.t.p1, a.window, a.sinks);
       if constexpr (!Q8) {
-        if (!wait(ms.full[slot], (n / C::kSlots) & 1)) return false;
+        if (!wait(ms.full[slot], phase)) return false;
         if (partly) {
           const int end = wk.v.kv_len - b * kBN - key0;  // tokens from here on do not exist
+#pragma unroll 4
           for (int q = pt; q < nkeys * nsl * 8; q += kPT) {
             uint4* ptr = reinterpret_cast<uint4*>(dst + q * 16);
             uint4 x = *ptr;
             const int key = (q / 8) % nkeys;
-            if (key >= end) {
-              x = make_uint4(0, 0, 0, 0);
-            } else {
-              uint32_t* w = &x.x;
-              bool bad = false;
+            bool bad = false;
+            uint32_t* w = &x.x;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if ((w[j] & 0x7c00u) == 0x7c00u) { w[j] &= 0xffff0000u; bad = true; }
-                if ((w[j] & 0x7c000000u) == 0x7c000000u) { w[j] &= 0x0000ffffu; bad = true; }
-              }
-              found |= bad;
+            for (int j = 0; j < 4; ++j) {
+              if ((w[j] & 0x7c00u) == 0x7c00u) { w[j] &= 0xffff0000u; bad = true; }
+              if ((w[j] & 0x7c000000u) == 0x7c000000u) { w[j] &= 0x0000ffffu; bad = true; }
             }
-            *ptr = x;
+            if (key >= end) *ptr = make_uint4(0, 0, 0, 0);
+            else if (bad) {
+              *ptr = x;
+              found = true;
+            }
           }
           fence_async_shared();
         }
       } else {
-        const int rs = n % C::kRawSlots;
-        if (!wait(ms.raw_full[rs], (n / C::kRawSlots) & 1)) return false;
-        if (!wait(ms.empty[slot], ((n / C::kSlots) & 1) ^ 1)) return false;
+        if (!wait(ms.raw_full[rs], rphase)) return false;
+        if (!wait(ms.empty[slot], phase ^ 1)) return false;
         const uint8_t* src = raw + rs * C::kRaw;
         const __half* sc = reinterpret_cast<const __half*>(src + C::kSlot / 2);
         const uint32_t gone = static_cast<uint32_t>(ms.raw_pages[rs]);
         const int end = partly ? wk.v.kv_len - b * kBN - key0 : nkeys;
         constexpr int kBC = C::kBox / 16;  // 16-code chunks per box row
-        const int nbx = nsl * 64 / C::kBox;
-#pragma unroll 2
-        for (int q = pt; q < nkeys * nsl * 4; q += kPT) {
-          const uint4 codes = *reinterpret_cast<const uint4*>(src + q * 16);
-          const int cc = q % kBC, tok = (q / kBC) % kPage, pb = q / (kBC * kPage);
-          const int page = pb / nbx, key = page * kPage + tok, dim = (pb - page * nbx) * C::kBox + cc * 16;
-          __half d = sc[key * (2 * NS) + (slab0 * 64 + dim) / 32];
-          uint32_t o[8];
-          const uint32_t* cw = &codes.x;
-          if ((gone >> page & 1) || (kv && (key >= end || (partly && (__half_as_ushort(d) & 0x7c00u) == 0x7c00u)))) {
-            found |= !(gone >> page & 1) && key < end;
+        const int nbx = nsl * 64 / C::kBox, total = nkeys * nsl * 4;
+        const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+#pragma unroll 1
+        for (int q0 = pt; q0 < total; q0 += 4 * kPT) {
+          uint4 codes[4];
+          __half d[4];
+          int key[4], dim[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = 0;
-          } else {
-            const __half2 d2 = __half2half2(d), off = __half2half2(__ushort_as_half(0x6480));  // 1152
+          for (int t = 0; t < 4; ++t) {
+            const int q = q0 + t * kPT;
+            if (q < total) {
+              codes[t] = *reinterpret_cast<const uint4*>(src + q * 16);
+              const int cc = q % kBC, tok = (q / kBC) % kPage, pb = q / (kBC * kPage), page = pb / nbx;
+              key[t] = page * kPage + tok;
+              dim[t] = (pb - page * nbx) * C::kBox + cc * 16;
+              d[t] = sc[key[t] * (2 * NS) + (slab0 * 64 + dim[t]) / 32];
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            if (q0 + t * kPT >= total) break;
+            uint32_t o[8];
+            const uint32_t* cw = &codes[t].x;
+            const __half2 d2 = __half2half2(d[t]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const uint32_t w = cw[j] ^ 0x80808080u;  // code + 128; 0x6400 | byte is 1024 + byte
@@ -788,15 +846,26 @@ __global__ void __launch_bounds__(Cfg<NS, Q8, CG>::kThreads, 1)
               o[2 * j] = *reinterpret_cast<const uint32_t*>(&a2);
               o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&b2);
             }
+            if (gone || partly) {
+              const bool none = gone >> (key[t] / kPage) & 1;
+              const bool bad = partly && !none && key[t] < end && (__half_as_ushort(d[t]) & 0x7c00u) == 0x7c00u;
+              if (none || bad || (kv && key[t] >= end)) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = 0;
+              }
+              found |= bad;
+            }
+            // the two 16-byte pieces in an order that keeps the 128-byte rows of neighbouring slabs on other banks
+            const int sl = dim[t] / 64, ch = (dim[t] % 64) / 8, odd = sl & 1;
+            uint8_t* row = dst + sl * nkeys * 128 + key[t] * 128;
+            const uint4 v0 = make_uint4(o[0], o[1], o[2], o[3]), v1 = make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4*>(row + (((ch + odd) ^ (key[t] & 7)) << 4)) = odd ? v1 : v0;
+            *reinterpret_cast<uint4*>(row + (((ch + 1 - odd) ^ (key[t] & 7)) << 4)) = odd ? v0 : v1;
           }
-          const int sl = dim / 64, ch = (dim % 64) / 8;
-          uint8_t* row = dst + sl * nkeys * 128 + key * 128;
-          *reinterpret_cast<uint4*>(row + ((ch ^ (key & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (key & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
+        fence_async_shared();
         __syncwarp();
         if (lane == 0) bar_arrive(bar(ms.raw_empty[rs]));
-        fence_async_shared();
       }
       if (found) {
         if (CG == 1) {
@@ -807,71 +876,75 @@ __global__ void __launch_bounds__(Cfg<NS, Q8, CG>::kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) lead_arrive(ms.ready[slot]);
-      ++n;
       return true;
     };
+    constexpr int kLPR = NS == 3 ? 32 : 8 * NS;  // lanes per row of Q
+    constexpr int kRPP = 32 / kLPR;              // rows per warp and pass
+    constexpr int kPass = (128 + kPrep * kRPP - 1) / (kPrep * kRPP), kBatch = kPass < 8 ? kPass : 8;
+    const int ch = lane % kLPR, sub = lane / kLPR;
     while (ok && wk.next()) {
-      // Q of the tile, once the products of the segment before no longer read it
-      ok = wk.seg == 0 || wait(ms.q_free, (wk.seg - 1) & 1);
-      if (!ok) break;
-      constexpr int kLPR = NS == 3 ? 32 : 8 * NS;  // lanes per row
-      constexpr int kRPP = 32 / kLPR;              // rows per warp and pass
-      const int ch = lane % kLPR, R0 = wk.mt * M + rank * 128;
-      const int rows = min(128, wk.t.rows - rank * 128);
-#pragma unroll 4
-      for (int r = pw * kRPP + lane / kLPR; r - lane / kLPR < rows; r += C::kPrep * kRPP) {
-        const int rr = min(r, rows - 1);
-        const int R = R0 + rr;
-        const int64_t off = (wk.v.r0 + R / a.G) * a.q.row_stride + (wk.h * a.G + R % a.G) * a.q.head_stride + ch * 8;
-        uint32_t o[4] = {0, 0, 0, 0};
-        float qc = a.c;
-        if (a.dtype == MK_F16) {
-          if (ch < 8 * NS) {
-            const __half* qp = static_cast<const __half*>(a.q.data) + off;
+      // Q of the tile: the first rows are fetched before the products of the
+      // segment before are known to no longer read it, and stored after that
+      const int R0 = wk.mt * M + rank * 128, rows = min(128, wk.t.rows - rank * 128);
+#pragma unroll 1
+      for (int pass = 0; pass < kPass; pass += kBatch) {
+        uint32_t o[kBatch][4];
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t) {
+          const int r = ((pass + t) * kPrep + pw) * kRPP + sub, R = R0 + r;
+          if (r < rows && ch < 8 * NS) {
+            const int64_t off = (wk.v.r0 + R / a.G) * a.q.row_stride + (wk.h * a.G + R % a.G) * a.q.head_stride + ch * 8;
+            const uint16_t* qp = static_cast<const uint16_t*>(a.q.data) + off;
             if (a.vq) {
               const uint4 x = __ldg(reinterpret_cast<const uint4*>(qp));
-              o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+              o[t][0] = x.x; o[t][1] = x.y; o[t][2] = x.z; o[t][3] = x.w;
             } else {
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                o[j] = static_cast<uint32_t>(__half_as_ushort(qp[2 * j])) |
-                       static_cast<uint32_t>(__half_as_ushort(qp[2 * j + 1])) << 16;
+              for (int j = 0; j < 4; ++j) o[t][j] = qp[2 * j] | static_cast<uint32_t>(qp[2 * j + 1]) << 16;
             }
+          } else {
+            o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0;
           }
-        } else {
-          // bf16: the row times a power of two that brings its largest value to [1, 2)
-          float x[8] = {};
-          if (ch < 8 * NS) {
-            const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q.data) + off;
-            if (a.vq) load8<MK_BF16, true>(qp, x); else load8<MK_BF16, false>(qp, x);
-          }
-          float mx = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(x[j]));
-#pragma unroll
-          for (int k = kLPR / 2; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-          int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-          if (e > 127 || mx == 0.f) e = 0;   // infinities stay, zero rows too
-          e = max(-100, min(100, e));
-          const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          // (kept normal and finite, so that -inf x c is -inf)
-          qc = fminf(fmaxf(a.c * __uint_as_float(static_cast<uint32_t>(127 + e) << 23), 1.2e-38f), 3e38f);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = pack_half2(x[2 * j] * f, x[2 * j + 1] * f);
         }
-        if (ch < 8 * NS && r < rows)
-          *reinterpret_cast<uint4*>(sq + (ch / 8) * 16384 + r * 128 + (((ch % 8) ^ (r & 7)) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
-        if (ch == 0 && r < rows) ms.qc[wk.seg & 3][r] = qc;
+        if (pass == 0 && wk.seg > 0) ok = wait(ms.q_free, (wk.seg - 1) & 1);
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t) {
+          const int r0 = ((pass + t) * kPrep + pw) * kRPP, r = r0 + sub;
+          if (r0 >= rows) break;  // whole warps
+          int e = 0;
+          if (a.dtype == MK_BF16) {
+            // the row times a power of two that brings its largest value to [1, 2): exact, and within binary16's range
+            float x[8], mx = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              x[2 * j] = __uint_as_float(o[t][j] << 16);
+              x[2 * j + 1] = __uint_as_float(o[t][j] & 0xffff0000u);
+              mx = fmaxf(mx, fmaxf(fabsf(x[2 * j]), fabsf(x[2 * j + 1])));
+            }
+#pragma unroll
+            for (int k = kLPR / 2; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+            e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+            if (e > 127 || mx == 0.f) e = 0;  // infinities stay, zero rows too
+            e = max(-100, min(100, e));
+            const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[t][j] = pack_half2(x[2 * j] * f, x[2 * j + 1] * f);
+          }
+          if (r < rows && ch < 8 * NS)
+            *reinterpret_cast<uint4*>(sq + (ch / 8) * 16384 + r * 128 + (((ch % 8) ^ (r & 7)) << 4)) =
+                make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
+          if (ch == 0 && r < rows) ms.qe[wk.seg & 3][r] = static_cast<int8_t>(e);
+        }
       }
+      if (!ok) break;
       fence_async_shared();
       __syncwarp();
       if (lane == 0) lead_arrive(ms.q_ready);
       for (int i = wk.b0; ok && i <= wk.b1; ++i) {
         if (i < wk.b1)
-          for (int u = 0; ok && u < C::KU; ++u) ok = unit(0, u, wk.t.block(i));
+          for (int u = 0; ok && u < C::KU; ++u) ok = unit(std::integral_constant<int, 0>(), u, wk.t.block(i));
         if (i > wk.b0)
-          for (int u = 0; ok && u < C::VU; ++u) ok = unit(1, u, wk.t.block(i - 1));
+          for (int u = 0; ok && u < C::VU; ++u) ok = unit(std::integral_constant<int, 1>(), u, wk.t.block(i - 1));
       }
     }
   }
@@ -879,7 +952,7 @@ __global__ void __launch_bounds__(Cfg<NS, Q8, CG>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (CG == 2) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (warp == 1) tmem_free<CG>(tm, 512);
+  if (warp == kWarpMma) tmem_free<CG>(tm, 512);
 }
 
 // ------------------------------------------------------------------- launch
@@ -902,7 +975,7 @@ int resident_workers(int device) {
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim = {2, 1, 1};
     cfg.gridDim = dim3(2 * (sms / 2));
-    cfg.blockDim = dim3(C::kThreads);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.attrs = at;
     cfg.numAttrs = 1;
@@ -926,15 +999,23 @@ cudaError_t launch_attend(AttendParams a, const CUtensorMap& tk, const CUtensorM
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim = {CG, 1, 1};
   cfg.gridDim = dim3(a.workers * CG);
-  cfg.blockDim = dim3(C::kThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel<NS, Q8, CG>, a, tk, tv);
   if (e != cudaSuccess) return e;
-  attend_join<NS, CG><<<dim3(a.workers, 4), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t jc{};
+  cudaLaunchAttribute ja[1];
+  ja[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  ja[0].val.programmaticStreamSerializationAllowed = 1;
+  jc.gridDim = dim3(a.workers, 4);
+  jc.blockDim = dim3(256);
+  jc.stream = stream;
+  jc.attrs = ja;
+  jc.numAttrs = 1;
+  return cudaLaunchKernelEx(&jc, attend_join<NS, CG>, a);
 }
 
 template <bool Q8>
