@@ -85,6 +85,7 @@ extern "C" mk_status mk_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, c
   p.out = a->out;
   p.hq = a->hq;
   p.G = a->hq / pool->hkv;
+  p.g_inv = (1 << 20) / p.G + 1;
   p.dtype = a->dtype;
   // a window beyond every length is none, and keeps the positions' arithmetic in range
   p.window = a->window >= rows->table_stride * kPage ? 0 : a->window;

@@ -42,7 +42,6 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
-#include <type_traits>
 
 #include "ops_internal.cuh"
 #include "sm103.cuh"
@@ -63,7 +62,7 @@ struct AttendParams {
   mk_kv_pool pool;
   mk_kv_rows rows;
   mk_dense q, gate, out;
-  int hq, G, dtype, window, sinks, workers;
+  int hq, G, g_inv, dtype, window, sinks, workers;  // g_inv = 2^20 / G + 1: x / G = x g_inv >> 20 for x < 2^20 / G
   float c;         // scale x log2(e)
   int vq, vo, vg;  // 16-byte access to q, out, gate
   JoinInfo* join;  // [kMaxWorkers]
@@ -75,6 +74,7 @@ struct AttendParams {
 // Tile mt of a sequence: M rows of (token, head in group) pairs.
 struct Tile {
   int rows;         // valid rows
+  int t0, h0;       // token (within the new rows) and head (within the group) of the first row
   int p0, p1;       // positions of its first and last token
   int nblk;         // 128-token blocks some row may see, at least 1
   int sink_b, lo;   // block i is i < sink_b ? i : lo + i - sink_b
@@ -85,7 +85,9 @@ __device__ __forceinline__ Tile make_tile(const SeqView& v, int G, int M, int mt
   Tile t;
   const int R0 = mt * M, R1 = min(R0 + M, v.q_len * G);
   t.rows = R1 - R0;
-  t.p0 = v.kv_len - v.q_len + R0 / G;
+  t.t0 = R0 / G;
+  t.h0 = R0 - t.t0 * G;
+  t.p0 = v.kv_len - v.q_len + t.t0;
   t.p1 = v.kv_len - v.q_len + (R1 - 1) / G;
   t.sink_b = t.lo = 0;
   t.nblk = 1;
@@ -100,6 +102,14 @@ __device__ __forceinline__ Tile make_tile(const SeqView& v, int G, int M, int mt
   }
   return t;
 }
+// Token and head of row r (below 256) of a tile, relative to its first row's token.
+struct RowOf {
+  int tok, head;
+};
+__device__ __forceinline__ RowOf row_of(const Tile& t, int r, int G, int g_inv) {
+  const int x = t.h0 + r, q = (x * g_inv) >> 20;
+  return {t.t0 + q, x - q * G};
+}
 // Whether rows at positions p0..p1 all see every token of block b.
 __device__ __forceinline__ bool block_full(int b, int p0, int p1, int window, int sinks) {
   const int last = b * kBN + kBN - 1;
@@ -112,6 +122,9 @@ __device__ __forceinline__ uint32_t seen_bits(int p, int base, int window, int s
   if (window > 0) m &= ~low_bits(p - window + 1 - base) | low_bits(sinks - base);
   return m;
 }
+
+// Column of S's 128 in which P of token t (even) lies: each half over its own scores.
+__host__ __device__ constexpr int p_col(int t) { return t / 64 * 64 + t % 64 / 2; }
 
 // A worker's walk through the line of blocks: segments of consecutive blocks
 // of one item. Every role walks it for itself.
@@ -159,13 +172,13 @@ struct Walk {
     return true;
   }
   __device__ __forceinline__ bool whole() const { return b0 == 0 && b1 == t.nblk; }
-  // page of the block's i-th 16 tokens, -1 when there is none
-  __device__ __forceinline__ int page(int b, int i) const {
+  // Table entry of the block's i-th 16 tokens, -1 behind the table; as loaded,
+  // so that a load ahead is waited for only where has_page() looks at it.
+  __device__ __forceinline__ int entry(int b, int i) const {
     const int e = b * (kBN / kPage) + i;
-    if (e >= a->rows.table_stride) return -1;
-    const int pg = __ldg(a->rows.tables + static_cast<int64_t>(s) * a->rows.table_stride + e);
-    return pg >= 0 && pg < a->pool.n_pages ? pg : -1;
+    return e < a->rows.table_stride ? __ldg(a->rows.tables + static_cast<int64_t>(s) * a->rows.table_stride + e) : -1;
   }
+  __device__ __forceinline__ bool has_page(int entry) const { return entry >= 0 && entry < a->pool.n_pages; }
 };
 
 // -------------------------------------------------------------------- layout
@@ -190,23 +203,24 @@ struct Cfg {
   // in flight from memory, so two operand units are kept and the rest is for those.
   static constexpr int kFit = kBudget / kSlot;
   static constexpr int kSlots = Q8 ? 2 : kFit > 8 ? 8 : kFit;
-  static constexpr int kRawFit = (kBudget - kSlots * kSlot) / kRaw / 2 * 2;
+  static constexpr int kRawFit = (kBudget - kSlots * kSlot) / kRaw;
   static constexpr int kRawSlots = !Q8 ? 0 : kRawFit > 6 ? 6 : kRawFit;
   static constexpr int kBox = q8_box(NS, CG);
   static constexpr int kSmem = kMisc + kQ + kSlots * kSlot + kRawSlots * kRaw;
   static_assert(kSlots >= 2 && (!Q8 || kRawSlots >= 4) && kSmem <= 232448, "ring");
-  // a preparing group must see every phase of the slots it waits on: slot parity is its own
-  static_assert(!Q8 || (kSlots % 2 == 0 && kRawSlots % 2 == 0), "groups");
   static_assert(!Q8 || (slabs_k(0) * 64 % kBox == 0 && kSlabsV * 64 % kBox == 0), "boxes");
 };
 
+// 16 warps: 128 registers a thread, which the softmax's 64 live scores need
+// (with 20 warps and 96 registers they spilled and the softmax took twice as
+// long; ptxas did not use what setmaxnreg would have moved to them).
 constexpr int kWarpCopy = 8, kWarpMma = 9, kWarpPrep = 10;
-constexpr int kPrep = 6;        // preparing warps, in two groups that share the units
+constexpr int kPrep = 6;  // preparing warps
 constexpr int kThreads = 32 * (kWarpPrep + kPrep);
 
 struct Misc {
   uint64_t ready[8], full[8], empty[8], raw_full[6], raw_empty[6];
-  uint64_t s_full[2], p_ready[2], pv_done, q_ready, q_free;
+  uint64_t s_full[2], p_ready[2], pv_done, o_full, q_ready, q_free;
   uint32_t tmem;
   int dead;
   Start start;
@@ -376,7 +390,7 @@ __global__ void __launch_bounds__(256) attend_join(const AttendParams a) {
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     float x[8];  // eight dims per store
-    const int R = j.mt * M + r, row = v.r0 + R / a.G, head = j.h * a.G + R % a.G;
+    const int R = j.mt * M + r, tok = R / a.G, row = v.r0 + tok, head = j.h * a.G + R - tok * a.G;
     if (kPer == 8) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) x[i] = l == 0.f ? 0.f : o[i] * inv;
@@ -423,18 +437,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       bar_init(bar(ms.full[i]), 1);
-      bar_init(bar(ms.ready[i]), CG * kPrep / 2);
+      bar_init(bar(ms.ready[i]), CG * kPrep);
       bar_init(bar(ms.empty[i]), 1);
     }
     for (int i = 0; i < C::kRawSlots; ++i) {
       bar_init(bar(ms.raw_full[i]), 1);
-      bar_init(bar(ms.raw_empty[i]), kPrep / 2);
+      bar_init(bar(ms.raw_empty[i]), kPrep);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(bar(ms.s_full[i]), 1);
       bar_init(bar(ms.p_ready[i]), 8 * CG);
     }
     bar_init(bar(ms.pv_done), 1);
+    bar_init(bar(ms.o_full), 1);
     bar_init(bar(ms.q_ready), CG * kPrep);
     bar_init(bar(ms.q_free), 1);
     ms.dead = (smem_u32(smem) & 1023u) != 0;  // (the swizzled tiles need the alignment)
@@ -473,11 +488,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int page = __shfl_sync(0xffffffffu, pg, (p0 + i) & 7);
         if (lane < np * nsl)
           tma_2d(smem_u32(ring + slot * C::kSlot + sl * nkeys * 128 + i * 2048), map, (slab0 + sl) * 64,
-                 page < 0 ? none : (page * a.pool.hkv + wk.h) * kPage, bar(ms.full[slot]));
+                 !wk.has_page(page) ? none : (page * a.pool.hkv + wk.h) * kPage, bar(ms.full[slot]));
       } else {
         const int slot = n % C::kRawSlots;
         if (!wait(ms.raw_empty[slot], ((n / C::kRawSlots) & 1) ^ 1)) return false;
-        const uint32_t gone = __ballot_sync(0xffffffffu, lane < 8 && pg < 0);
+        const uint32_t gone = __ballot_sync(0xffffffffu, lane < 8 && !wk.has_page(pg));
         const uint32_t mine = (gone >> p0) & ((1u << np) - 1);
         constexpr int kScaleBytes = kPage * NS * 4;
         if (lane == 0) {
@@ -492,10 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int page = __shfl_sync(0xffffffffu, pg, (p0 + i) & 7);
           if (lane < np * nbx)
             tma_2d(smem_u32(dst + lane * kPage * C::kBox), map, slab0 * 64 + bx * C::kBox,
-                   page < 0 ? none : (page * a.pool.hkv + wk.h) * kPage, bar(ms.raw_full[slot]));
+                   !wk.has_page(page) ? none : (page * a.pool.hkv + wk.h) * kPage, bar(ms.raw_full[slot]));
         }
         const int page = __shfl_sync(0xffffffffu, pg, (p0 + lane) & 7);
-        if (lane < np && page >= 0)
+        if (lane < np && wk.has_page(page))
           bulk_copy(smem_u32(dst + C::kSlot / 2 + lane * kScaleBytes),
                     static_cast<const uint8_t*>(kv ? a.pool.v_scale : a.pool.k_scale) +
                         (static_cast<int64_t>(page) * a.pool.hkv + wk.h) * kScaleBytes,
@@ -505,9 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     while (ok && wk.next()) {
-      int pg = lane < 8 ? wk.page(wk.t.block(wk.b0), lane) : -1, pg_v = -1;
+      int pg = lane < 8 ? wk.entry(wk.t.block(wk.b0), lane) : -1, pg_v = -1;
       for (int i = wk.b0; ok && i <= wk.b1; ++i) {
-        const int pg_next = i + 1 < wk.b1 && lane < 8 ? wk.page(wk.t.block(i + 1), lane) : -1;
+        const int pg_next = i + 1 < wk.b1 && lane < 8 ? wk.entry(wk.t.block(i + 1), lane) : -1;
         if (i < wk.b1)
           for (int u = 0; ok && u < C::KU; ++u) ok = unit(0, u, pg);
         if (i > wk.b0)
@@ -578,12 +593,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t vb = ra + slot * C::kSlot;
 #pragma unroll
             for (int k = 0; k < C::kKeysV / 16; ++k)
-              mma_ts<CG>(tm, tm + 256 + (blk & 1) * kBN + (u * C::kKeysV + k * 16) / 2,
+              mma_ts<CG>(tm, tm + 256 + (blk & 1) * kBN + p_col(u * C::kKeysV + k * 16),
                          smem_desc(vb + k * 2048, C::kKeysV * 128, 1024), kIdO, !(i - 1 == wk.b0 && u == 0 && k == 0));
             mma_commit<CG>(bar(ms.empty[slot]));
           }
           if (!ok) break;
           mma_commit<CG>(bar(ms.pv_done));
+          if (i == wk.b1) mma_commit<CG>(bar(ms.o_full));
         }
         nb += wk.b1 - wk.b0;
       }
@@ -601,16 +617,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (wk.next()) {
       const int r = rank * 128 + wr, r_warp = rank * 128 + quad * 32;
       const bool valid = r < wk.t.rows, warp_valid = r_warp < wk.t.rows;
-      const int R0 = wk.mt * M, base_p = wk.v.kv_len - wk.v.q_len;
-      const int p = base_p + (R0 + min(r, wk.t.rows - 1)) / a.G;
-      const int wp0 = base_p + (R0 + min(r_warp, wk.t.rows - 1)) / a.G;
-      const int wp1 = base_p + (R0 + min(r_warp + 31, wk.t.rows - 1)) / a.G;
+      const int base_p = wk.v.kv_len - wk.v.q_len, last = wk.t.rows - 1;
+      const RowOf at = row_of(wk.t, min(r, last), a.G, a.g_inv);
+      const int p = base_p + at.tok;
+      const int wp0 = base_p + row_of(wk.t, min(r_warp, last), a.G, a.g_inv).tok;
+      const int wp1 = base_p + row_of(wk.t, min(r_warp + 31, last), a.G, a.g_inv).tok;
       float m = valid ? -INFINITY : 0.f, l = 0.f, c = 0.f;
-      int gone_pg = lane < 4 ? wk.page(wk.t.block(wk.b0), 4 * half + lane) : 0;
+      int pages = lane < 4 ? wk.entry(wk.t.block(wk.b0), 4 * half + lane) : 0;
       for (int i = wk.b0; i < wk.b1; ++i, ++nb) {
         const int b = wk.t.block(i);
-        const uint32_t gone = __ballot_sync(0xffffffffu, gone_pg < 0) & 0xfu;
-        if (i + 1 < wk.b1 && lane < 4) gone_pg = wk.page(wk.t.block(i + 1), 4 * half + lane);
+        const uint32_t gone = __ballot_sync(0xffffffffu, !wk.has_page(pages)) & 0xfu;
+        if (i + 1 < wk.b1 && lane < 4) pages = wk.entry(wk.t.block(i + 1), 4 * half + lane);
         ok &= wait(ms.s_full[nb & 1], (nb >> 1) & 1);
         tc_fence_after();
         if (warp_valid) {
@@ -618,32 +635,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             c = fminf(fmaxf(a.c * __uint_as_float(static_cast<uint32_t>(127 + ms.qe[wk.seg & 3][wr]) << 23), 1.2e-38f), 3e38f);
           const uint32_t sa = tm + lanes + 256 + (nb & 1) * kBN;
           uint32_t x[32], y[32];
-          tmem_ld32(sa + 64 * half, x);
-          tmem_ld32(sa + 64 * half + 32, y);
-          tmem_wait_ld(x);
-          tmem_wait_ld(y);
-          if (gone || !block_full(b, wp0, wp1, a.window, a.sinks)) {
-            uint32_t sx = seen_bits(p, b * kBN + 64 * half, a.window, a.sinks);
-            uint32_t sy = seen_bits(p, b * kBN + 64 * half + 32, a.window, a.sinks);
+          uint32_t sx = 0xffffffffu, sy = 0xffffffffu;
+          const bool part = gone || !block_full(b, wp0, wp1, a.window, a.sinks);
+          if (part) {
+            sx = seen_bits(p, b * kBN + 64 * half, a.window, a.sinks);
+            sy = seen_bits(p, b * kBN + 64 * half + 32, a.window, a.sinks);
             if (gone & 1) sx &= 0xffff0000u;
             if (gone & 2) sx &= 0x0000ffffu;
             if (gone & 4) sy &= 0xffff0000u;
             if (gone & 8) sy &= 0x0000ffffu;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (!(sx >> j & 1)) x[j] = 0xff800000u;
-              if (!(sy >> j & 1)) y[j] = 0xff800000u;
-            }
           }
+          auto hide = [&](uint32_t (&v)[32], uint32_t seen) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(seen >> j & 1)) v[j] = 0xff800000u;  // -inf
+          };
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto top = [&](const uint32_t (&v)[32]) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            mx[j & 2] = fmaxf(fmaxf(mx[j & 2], __uint_as_float(x[j])), __uint_as_float(x[j + 1]));
-            mx[(j & 2) + 1] = fmaxf(fmaxf(mx[(j & 2) + 1], __uint_as_float(y[j])), __uint_as_float(y[j + 1]));
+            for (int j = 0; j < 32; j += 2)
+              mx[j / 2 & 3] = fmaxf(fmaxf(mx[j / 2 & 3], __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
+          };
+          tmem_ld32(sa + 64 * half, x);
+          tmem_ld32(sa + 64 * half + 32, y);
+          tmem_wait_ld(x);
+          tmem_wait_ld(y);
+          if (part) {
+            hide(x, sx);
+            hide(y, sy);
           }
+          top(x);
+          top(y);
           float my = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;  // c > 0
           ms.swap[nb & 1][half][wr] = my;
-          named_sync(1 + quad, 64);  // and both halves' scores are in registers: P may overwrite them
+          named_sync(1 + quad, 64);
           my = fmaxf(my, ms.swap[nb & 1][half ^ 1][wr]);
           if (__any_sync(0xffffffffu, my > m + 8.f)) {  // the same in both halves
             const float nm = fmaxf(m, my);
@@ -667,27 +692,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mm = m == -INFINITY ? 0.f : m;
           const uint64_t c2 = pack2(c, c), m2 = pack2(-mm, -mm);
           uint64_t l2 = pack2(0.f, 0.f), l3 = l2;
-          uint32_t h[16];
+          // P of the half lies over its own scores, which are in registers
+          auto weigh = [&](const uint32_t (&v)[32], uint64_t& sum, uint32_t dst) {
+            uint32_t h[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float e0, e1;
-            unpack2(fma2(pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), c2, m2), e0, e1);
-            e0 = ex2(e0);
-            e1 = ex2(e1);
-            l2 = add2(l2, pack2(e0, e1));
-            h[j] = pack_half2(e0, e1);
-          }
-          tmem_st16(sa + 32 * half, h);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float e0, e1;
-            unpack2(fma2(pack2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])), c2, m2), e0, e1);
-            e0 = ex2(e0);
-            e1 = ex2(e1);
-            l3 = add2(l3, pack2(e0, e1));
-            h[j] = pack_half2(e0, e1);
-          }
-          tmem_st16(sa + 32 * half + 16, h);
+            for (int j = 0; j < 16; ++j) {
+              float e0, e1;
+              unpack2(fma2(pack2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), c2, m2), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum = add2(sum, pack2(e0, e1));
+              h[j] = pack_half2(e0, e1);
+            }
+            tmem_st16(dst, h);
+          };
+          weigh(x, l2, sa + 64 * half);
+          weigh(y, l3, sa + 64 * half + 16);
           float a0, a1;
           unpack2(add2(l2, l3), a0, a1);
           l += a0 + a1;
@@ -697,11 +717,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) lead_arrive(ms.p_ready[nb & 1]);
       }
-      // the result of the segment: O, once its last product is done. A parity
-      // says which of two phases is meant, and the last scores only show that
-      // the product three blocks back is done: wait for the last but one first.
-      if (wk.b1 - wk.b0 > 1) ok &= wait(ms.pv_done, (nb - 2) & 1);
-      ok &= wait(ms.pv_done, (nb - 1) & 1);
+      // the result of the segment: O, once its last product is done. (Not by
+      // pv_done: a wait tells only two neighbouring phases apart, and here the
+      // one before the last may be open as well as the last one over.)
+      ok &= wait(ms.o_full, wk.seg & 1);
       if (!warp_valid) continue;
       tc_fence_after();
       ms.swap[nb & 1][half][wr] = l;  // (read there last two blocks ago)
@@ -710,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_sync(1 + quad, 64);
       const bool whole = wk.whole();
       const int slot = 2 * worker + (wk.seg == 0 ? 0 : 1);
-      const int R = R0 + r, row = wk.v.r0 + R / a.G, head = wk.h * a.G + R % a.G;
+      const int row = wk.v.r0 + at.tok, head = wk.h * a.G + at.head;
       const bool patch = *const_cast<volatile int*>(&ms.flag[wk.seg & 3]) == wk.seg + 1;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       if (!whole && valid && half == 0) a.ml[slot * M + r] = ok ? make_float2(m, l) : make_float2(0.f, NAN);
@@ -727,8 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = wk.b0; i < wk.b1; ++i) {
             const int b = wk.t.block(i);
             for (int t = 0; t < kBN; ++t) {
-              const int pg = wk.page(b, t / kPage);
-              if (pg < 0 || !(seen_bits(p, b * kBN + (t & ~31), a.window, a.sinks) >> (t & 31) & 1)) continue;
+              const int pg = wk.entry(b, t / kPage);
+              if (!wk.has_page(pg) || !(seen_bits(p, b * kBN + (t & ~31), a.window, a.sinks) >> (t & 31) & 1)) continue;
               const int64_t e = ((static_cast<int64_t>(pg) * a.pool.hkv + wk.h) * kPage + t % kPage) * DH + 32 * k;
               if (Q8) {
                 const float d = __half2float(static_cast<const __half*>(a.pool.v_scale)[e / 32]);
@@ -760,24 +779,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------ operand preparing
-    // Group g takes the units in slots of that parity. A wait tells two phases
-    // of a barrier apart, no more: a group that took every other unit of a
-    // slot could mistake the phase before the last for the one it waits for.
-    const int pw = warp - kWarpPrep, group = pw & 1;
-    const int pt = (pw >> 1) * 32 + lane;               // thread of its group
-    constexpr int kPT = kPrep / 2 * 32;
+    const int pw = warp - kWarpPrep, pt = pw * 32 + lane;
+    constexpr int kPT = kPrep * 32;
     int n = 0;
     bool ok = true;
-    // unit u of K or V of block b: hand it over, converted (q8) and cleared (V of a partly seen block)
-    auto unit = [&](auto kvc, int u, int b) {
-      constexpr int kv = decltype(kvc)::value;
+    [[maybe_unused]] int turn = 0;  // warp whose turn it is to convert a box
+    // unit u of K or V of block b: hand it over, converted (q8) and cleared (V
+    // of a partly seen block). One body of code for K and V: more would not
+    // stay in the instruction cache.
+    auto unit = [&](int kv, int u, int b) {
       const int slot = n % C::kSlots, phase = (n / C::kSlots) & 1;
       [[maybe_unused]] const int rs = Q8 ? n % C::kRawSlots : 0, rphase = Q8 ? (n / C::kRawSlots) & 1 : 0;
       ++n;
-      if ((slot & 1) != group) return true;
       const int nkeys = kv ? C::kKeysV : C::kKeysK, nsl = kv ? C::kSlabsV : C::slabs_k(u);
       const int key0 = CG == 2 ? (kv ? 0 : 64 * rank) : (kv ? u * C::kKeysV : 0);
-      [[maybe_unused]] const int slab0 = CG == 2 ? (kv ? rank * C::kSlabsV : 0) : (kv ? 0 : 2 * u);
       uint8_t* const dst = ring + slot * C::kSlot;
       bool found = false;
       const bool partly = kv && !block_full(b, wk.t.p0, wk.t.p1, a.window, a.sinks);
@@ -808,34 +823,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         if (!wait(ms.raw_full[rs], rphase)) return false;
         if (!wait(ms.empty[slot], phase ^ 1)) return false;
+        const int slab0 = CG == 2 ? (kv ? rank * C::kSlabsV : 0) : (kv ? 0 : 2 * u);
         const uint8_t* src = raw + rs * C::kRaw;
         const __half* sc = reinterpret_cast<const __half*>(src + C::kSlot / 2);
         const uint32_t gone = static_cast<uint32_t>(ms.raw_pages[rs]);
         const int end = partly ? wk.v.kv_len - b * kBN - key0 : nkeys;
-        constexpr int kBC = C::kBox / 16;  // 16-code chunks per box row
-        const int nbx = nsl * 64 / C::kBox, total = nkeys * nsl * 4;
+        // A warp converts a box (16 tokens x kBox codes) at a time, 16 codes a
+        // lane and step; the warps take the boxes of all units in turn.
+        constexpr int kBC = C::kBox / 16, kTok = 32 / kBC, kSteps = kPage / kTok;
+        const int nbx = nsl * 64 / C::kBox, boxes = nkeys / kPage * nbx, inv = 256 / nbx + 1;
+        const int cc = lane % kBC, tok0 = lane / kBC;
         const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+        int pb = pw - turn;
+        if (pb < 0) pb += kPrep;
+        turn = (turn + boxes) % kPrep;
 #pragma unroll 1
-        for (int q0 = pt; q0 < total; q0 += 4 * kPT) {
-          uint4 codes[4];
-          __half d[4];
-          int key[4], dim[4];
+        for (; pb < boxes; pb += kPrep) {
+          const int page = (pb * inv) >> 8, dim = (pb - page * nbx) * C::kBox + cc * 16;
+          const int sl = dim / 64, ch = (dim % 64) / 8, odd = sl & 1;
+          uint4 codes[kSteps];
+          __half d[kSteps];
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int q = q0 + t * kPT;
-            if (q < total) {
-              codes[t] = *reinterpret_cast<const uint4*>(src + q * 16);
-              const int cc = q % kBC, tok = (q / kBC) % kPage, pb = q / (kBC * kPage), page = pb / nbx;
-              key[t] = page * kPage + tok;
-              dim[t] = (pb - page * nbx) * C::kBox + cc * 16;
-              d[t] = sc[key[t] * (2 * NS) + (slab0 * 64 + dim[t]) / 32];
-            }
+          for (int t = 0; t < kSteps; ++t) {
+            codes[t] = *reinterpret_cast<const uint4*>(src + pb * (kPage * C::kBox) + t * 512 + lane * 16);
+            d[t] = sc[(page * kPage + tok0 + t * kTok) * (2 * NS) + (slab0 * 64 + dim) / 32];
           }
+          uint8_t* const slab = dst + sl * nkeys * 128 + page * kPage * 128;
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            if (q0 + t * kPT >= total) break;
+          for (int t = 0; t < kSteps; ++t) {
+            const int tok = tok0 + t * kTok;
             uint32_t o[8];
-            const uint32_t* cw = &codes[t].x;
+            const uint32_t cw[4] = {codes[t].x, codes[t].y, codes[t].z, codes[t].w};
             const __half2 d2 = __half2half2(d[t]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -847,20 +865,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&b2);
             }
             if (gone || partly) {
-              const bool none = gone >> (key[t] / kPage) & 1;
-              const bool bad = partly && !none && key[t] < end && (__half_as_ushort(d[t]) & 0x7c00u) == 0x7c00u;
-              if (none || bad || (kv && key[t] >= end)) {
+              const int key = page * kPage + tok;
+              const bool none = gone >> page & 1;
+              const bool bad = partly && !none && key < end && (__half_as_ushort(d[t]) & 0x7c00u) == 0x7c00u;
+              if (none || bad || (kv && key >= end)) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] = 0;
               }
               found |= bad;
             }
             // the two 16-byte pieces in an order that keeps the 128-byte rows of neighbouring slabs on other banks
-            const int sl = dim[t] / 64, ch = (dim[t] % 64) / 8, odd = sl & 1;
-            uint8_t* row = dst + sl * nkeys * 128 + key[t] * 128;
+            uint8_t* row = slab + tok * 128;
             const uint4 v0 = make_uint4(o[0], o[1], o[2], o[3]), v1 = make_uint4(o[4], o[5], o[6], o[7]);
-            *reinterpret_cast<uint4*>(row + (((ch + odd) ^ (key[t] & 7)) << 4)) = odd ? v1 : v0;
-            *reinterpret_cast<uint4*>(row + (((ch + 1 - odd) ^ (key[t] & 7)) << 4)) = odd ? v0 : v1;
+            *reinterpret_cast<uint4*>(row + (((ch + odd) ^ (tok & 7)) << 4)) = odd ? v1 : v0;
+            *reinterpret_cast<uint4*>(row + (((ch + 1 - odd) ^ (tok & 7)) << 4)) = odd ? v0 : v1;
           }
         }
         fence_async_shared();
@@ -872,6 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *const_cast<volatile int*>(&ms.flag[wk.seg & 3]) = wk.seg + 1;
         } else {
           for (int k = 0; k < 2; ++k) st_cluster(peer_addr(smem_u32(&ms.flag[wk.seg & 3]), k), wk.seg + 1);
+          asm volatile("fence.acq_rel.cluster;" ::: "memory");
         }
       }
       __syncwarp();
@@ -880,30 +899,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     constexpr int kLPR = NS == 3 ? 32 : 8 * NS;  // lanes per row of Q
     constexpr int kRPP = 32 / kLPR;              // rows per warp and pass
-    constexpr int kPass = (128 + kPrep * kRPP - 1) / (kPrep * kRPP), kBatch = kPass < 8 ? kPass : 8;
+    constexpr int kPass = (128 + kPrep * kRPP - 1) / (kPrep * kRPP), kBatch = kPass < 11 ? kPass : 11;
     const int ch = lane % kLPR, sub = lane / kLPR;
     while (ok && wk.next()) {
       // Q of the tile: the first rows are fetched before the products of the
       // segment before are known to no longer read it, and stored after that
-      const int R0 = wk.mt * M + rank * 128, rows = min(128, wk.t.rows - rank * 128);
+      const int rows = min(128, wk.t.rows - rank * 128);
 #pragma unroll 1
       for (int pass = 0; pass < kPass; pass += kBatch) {
+        // Addresses are clamped to valid rows and columns rather than the loads
+        // made conditional: all of a batch are in flight at once.
         uint32_t o[kBatch][4];
+        auto row_ptr = [&](int t) {
+          const int r = min(((pass + t) * kPrep + pw) * kRPP + sub, max(rows, 1) - 1);
+          const RowOf at = row_of(wk.t, min(rank * 128 + r, wk.t.rows - 1), a.G, a.g_inv);
+          return static_cast<const uint16_t*>(a.q.data) + (wk.v.r0 + at.tok) * a.q.row_stride +
+                 (wk.h * a.G + at.head) * a.q.head_stride + min(ch, 8 * NS - 1) * 8;
+        };
+        if (a.vq) {
 #pragma unroll
-        for (int t = 0; t < kBatch; ++t) {
-          const int r = ((pass + t) * kPrep + pw) * kRPP + sub, R = R0 + r;
-          if (r < rows && ch < 8 * NS) {
-            const int64_t off = (wk.v.r0 + R / a.G) * a.q.row_stride + (wk.h * a.G + R % a.G) * a.q.head_stride + ch * 8;
-            const uint16_t* qp = static_cast<const uint16_t*>(a.q.data) + off;
-            if (a.vq) {
-              const uint4 x = __ldg(reinterpret_cast<const uint4*>(qp));
-              o[t][0] = x.x; o[t][1] = x.y; o[t][2] = x.z; o[t][3] = x.w;
-            } else {
+          for (int t = 0; t < kBatch; ++t) {
+            if (t >= 2 && (pass + t) * kPrep * kRPP >= rows) break;
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(row_ptr(t)));
+            o[t][0] = x.x; o[t][1] = x.y; o[t][2] = x.z; o[t][3] = x.w;
+          }
+        } else {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) o[t][j] = qp[2 * j] | static_cast<uint32_t>(qp[2 * j + 1]) << 16;
-            }
-          } else {
-            o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0;
+          for (int t = 0; t < kBatch; ++t) {
+            const uint16_t* qp = row_ptr(t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[t][j] = qp[2 * j] | static_cast<uint32_t>(qp[2 * j + 1]) << 16;
           }
         }
         if (pass == 0 && wk.seg > 0) ok = wait(ms.q_free, (wk.seg - 1) & 1);
@@ -940,11 +965,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_async_shared();
       __syncwarp();
       if (lane == 0) lead_arrive(ms.q_ready);
+      if (wk.left > wk.b1 - wk.b0) {  // the next tile's rows on their way to L2
+        const bool wrap = wk.mt + 1 == wk.n_mt;
+        const int h = wk.h + wrap, R0 = (wrap ? 0 : wk.mt + 1) * M + rank * 128;
+        const int left_rows = h < a.pool.hkv ? min(128, wk.v.q_len * a.G - R0) : 0;
+        const int t0 = R0 / a.G, h0 = R0 - t0 * a.G;
+        for (int k = pt; k < left_rows * NS; k += kPT) {
+          const int x = h0 + k / NS, q = (x * a.g_inv) >> 20;
+          const uint16_t* line = static_cast<const uint16_t*>(a.q.data) + (wk.v.r0 + t0 + q) * a.q.row_stride +
+                                 (h * a.G + x - q * a.G) * a.q.head_stride + k % NS * 64;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+        }
+      }
       for (int i = wk.b0; ok && i <= wk.b1; ++i) {
         if (i < wk.b1)
-          for (int u = 0; ok && u < C::KU; ++u) ok = unit(std::integral_constant<int, 0>(), u, wk.t.block(i));
+          for (int u = 0; ok && u < C::KU; ++u) ok = unit(0, u, wk.t.block(i));
         if (i > wk.b0)
-          for (int u = 0; ok && u < C::VU; ++u) ok = unit(std::integral_constant<int, 1>(), u, wk.t.block(i - 1));
+          for (int u = 0; ok && u < C::VU; ++u) ok = unit(1, u, wk.t.block(i - 1));
       }
     }
   }
