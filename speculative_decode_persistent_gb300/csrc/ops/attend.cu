@@ -30,9 +30,10 @@ constexpr size_t kJoinBytes = (kMaxWorkers * sizeof(JoinInfo) + 255) / 256 * 256
 // two parts per worker of 128 rows a block
 constexpr size_t kMlBytes = 2ull * kMaxWorkers * 128 * sizeof(float2);
 
-// The pool as token rows of dh elements; boxes of one page by 128 bytes
-// (binary16, swizzled as the products read it) or by `box` codes.
-bool encode_map(CUtensorMap* m, void* base, const mk_kv_pool& p, int box) {
+// The pool as token rows of dh elements. binary16: [slab of 64][token][64],
+// boxes of `slabs` x `tokens` rows of 128 bytes, swizzled as the products read
+// them. q8: boxes of 16 tokens x `box` codes.
+bool encode_map(CUtensorMap* m, void* base, const mk_kv_pool& p, int box, int tokens, int slabs) {
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -42,13 +43,20 @@ bool encode_map(CUtensorMap* m, void* base, const mk_kv_pool& p, int box) {
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }();
   if (!encode) return false;
-  const bool q8 = p.kv_dtype == MK_KV_Q8;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.dh), static_cast<cuuint64_t>(p.n_pages) * p.hkv * kPage};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.dh) * (q8 ? 1 : 2)};
-  const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box), kPage}, one[2] = {1, 1};
-  return encode(m, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, boxes,
-                one, CU_TENSOR_MAP_INTERLEAVE_NONE, q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint64_t dh = static_cast<cuuint64_t>(p.dh), rows = static_cast<cuuint64_t>(p.n_pages) * p.hkv * kPage;
+  const cuuint32_t one[3] = {1, 1, 1};
+  if (p.kv_dtype == MK_KV_Q8) {
+    const cuuint64_t dims[2] = {dh, rows}, strides[1] = {dh};
+    const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box), kPage};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
+  const cuuint64_t dims[3] = {64, rows, dh / 64}, strides[2] = {dh * 2, 128};
+  const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(tokens), static_cast<cuuint32_t>(slabs)};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -105,9 +113,10 @@ extern "C" mk_status mk_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, c
   // would have no rows, and single blocks keep twice as many copies going.
   const int cg = ns % 2 == 0 && static_cast<int64_t>(rows->max_q) * p.G > 128 ? 2 : 1;
   CUtensorMap tk, tv;
-  const int box = q8 ? q8_box(ns, cg) : 64;
+  const int box = q8_box(ns, cg), slabs_k = cg == 2 || ns < 2 ? ns : 2, slabs_v = ns / cg;
   int device = 0;
-  if (cudaGetDevice(&device) != cudaSuccess || !encode_map(&tk, pool->k, *pool, box) || !encode_map(&tv, pool->v, *pool, box))
+  if (cudaGetDevice(&device) != cudaSuccess || !encode_map(&tk, pool->k, *pool, box, 8, slabs_k) ||
+      !encode_map(&tv, pool->v, *pool, box, kPage, slabs_v))
     return MK_ERR_CUDA;
   const cudaError_t e = (q8 ? launch_attend_q8 : launch_attend_f16)(ns, cg, p, tk, tv, device, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;

@@ -25,6 +25,10 @@
 // in a fixed order: results do not depend on timing. Every worker finds its
 // piece from the lengths on the device, so nothing is planned on the host.
 //
+// Operand units in shared memory, 128-byte rows of 64 dims (a slab), swizzled:
+// K as [8 tokens][slab][8 rows], V as [page][slab][16 rows], so that one copy
+// brings all slabs of its tokens and a product of 16 tokens reads one page.
+//
 // Warps: 0-7 take the softmax and write results (two threads a row, 64 tokens
 // each, so that a block's softmax is shorter than its products), 8 copies
 // pages, 9 issues products, 10-15 prepare operands: they load Q, turn q8 codes
@@ -193,7 +197,8 @@ struct Cfg {
   static constexpr int kKeysK = CG == 2 ? 64 : 128, kKeysV = CG == 2 ? 128 : 128 / VU;
   static constexpr int kSlabsV = CG == 2 ? NS / 2 : NS;
   static __host__ __device__ constexpr int slabs_k(int u) { return CG == 2 ? NS : (NS - 2 * u < 2 ? NS - 2 * u : 2); }
-  static constexpr int kUnitK = kKeysK * slabs_k(0) * 128, kUnitV = kKeysV * kSlabsV * 128;
+  static constexpr int kBoxSlabsK = CG == 2 || NS < 2 ? NS : 2;  // slabs a K copy fills (of a last odd one: zeros behind it)
+  static constexpr int kUnitK = kKeysK * kBoxSlabsK * 128, kUnitV = kKeysV * kSlabsV * 128;
   static constexpr int kSlot = kUnitK > kUnitV ? kUnitK : kUnitV;
   static constexpr int kQ = NS * 16384;
   static constexpr int kMisc = 3072;
@@ -479,53 +484,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int np = nkeys / kPage, p0 = key0 / kPage;
       const CUtensorMap* map = kv ? &tv : &tk;
       const int none = a.pool.n_pages * a.pool.hkv * kPage;  // a row behind the pool reads as zeros
+      // A lane issues each copy, with the page id of the lane that holds it
+      // (75 cycles a copy; one lane for all of them: 125).
       if constexpr (!Q8) {
+        // K: boxes of 8 tokens x the unit's slabs, V: of a page x the unit's slabs
         const int slot = n % C::kSlots;
         if (!wait(ms.empty[slot], ((n / C::kSlots) & 1) ^ 1)) return false;
-        if (lane == 0) bar_expect(bar(ms.full[slot]), nkeys * nsl * 128);
+        const uint32_t fb = bar(ms.full[slot]), dst = smem_u32(ring + slot * C::kSlot);
+        const int bytes = kv ? kPage * 128 * C::kSlabsV : 8 * 128 * C::kBoxSlabsK, copies = kv ? np : 2 * np;
+        if (lane == 0) bar_expect(fb, copies * bytes);
+        const int page = __shfl_sync(0xffffffffu, pg, (p0 + (kv ? lane : lane >> 1)) & 7);
         __syncwarp();
-        const int i = lane / nsl, sl = lane - i * nsl;
-        const int page = __shfl_sync(0xffffffffu, pg, (p0 + i) & 7);
-        if (lane < np * nsl)
-          tma_2d(smem_u32(ring + slot * C::kSlot + sl * nkeys * 128 + i * 2048), map, (slab0 + sl) * 64,
-                 !wk.has_page(page) ? none : (page * a.pool.hkv + wk.h) * kPage, bar(ms.full[slot]));
+        if (lane < copies)
+          tma_3d(dst + lane * bytes, map, 0,
+                 (!wk.has_page(page) ? none : (page * a.pool.hkv + wk.h) * kPage) + (kv ? 0 : (lane & 1) * 8), slab0, fb);
       } else {
         const int slot = n % C::kRawSlots;
         if (!wait(ms.raw_empty[slot], ((n / C::kRawSlots) & 1) ^ 1)) return false;
         const uint32_t gone = __ballot_sync(0xffffffffu, lane < 8 && !wk.has_page(pg));
         const uint32_t mine = (gone >> p0) & ((1u << np) - 1);
         constexpr int kScaleBytes = kPage * NS * 4;
+        const uint32_t fb = bar(ms.raw_full[slot]), dst = smem_u32(raw + slot * C::kRaw);
         if (lane == 0) {
           ms.raw_pages[slot] = static_cast<int>(mine);
-          bar_expect(bar(ms.raw_full[slot]), nkeys * nsl * 64 + (np - __popc(mine)) * kScaleBytes);
+          bar_expect(fb, nkeys * nsl * 64 + (np - __popc(mine)) * kScaleBytes);
         }
+        const int nbx = nsl * 64 / C::kBox, i = lane / nbx;
+        const int page = __shfl_sync(0xffffffffu, pg, (p0 + i) & 7), page_s = __shfl_sync(0xffffffffu, pg, (p0 + lane) & 7);
         __syncwarp();
-        const int nbx = nsl * 64 / C::kBox;
-        uint8_t* dst = raw + slot * C::kRaw;
-        {
-          const int i = lane / nbx, bx = lane - i * nbx;
-          const int page = __shfl_sync(0xffffffffu, pg, (p0 + i) & 7);
-          if (lane < np * nbx)
-            tma_2d(smem_u32(dst + lane * kPage * C::kBox), map, slab0 * 64 + bx * C::kBox,
-                   !wk.has_page(page) ? none : (page * a.pool.hkv + wk.h) * kPage, bar(ms.raw_full[slot]));
-        }
-        const int page = __shfl_sync(0xffffffffu, pg, (p0 + lane) & 7);
-        if (lane < np && wk.has_page(page))
-          bulk_copy(smem_u32(dst + C::kSlot / 2 + lane * kScaleBytes),
+        if (lane < np * nbx)
+          tma_2d(dst + lane * kPage * C::kBox, map, slab0 * 64 + (lane - i * nbx) * C::kBox,
+                 !wk.has_page(page) ? none : (page * a.pool.hkv + wk.h) * kPage, fb);
+        if (lane < np && wk.has_page(page_s))
+          bulk_copy(dst + C::kSlot / 2 + lane * kScaleBytes,
                     static_cast<const uint8_t*>(kv ? a.pool.v_scale : a.pool.k_scale) +
-                        (static_cast<int64_t>(page) * a.pool.hkv + wk.h) * kScaleBytes,
-                    kScaleBytes, bar(ms.raw_full[slot]));
+                        (static_cast<int64_t>(page_s) * a.pool.hkv + wk.h) * kScaleBytes,
+                    kScaleBytes, fb);
       }
       ++n;
       return true;
     };
-    while (ok && wk.next()) {
-      int pg = lane < 8 ? wk.entry(wk.t.block(wk.b0), lane) : -1, pg_v = -1;
-      for (int i = wk.b0; ok && i <= wk.b1; ++i) {
-        const int pg_next = i + 1 < wk.b1 && lane < 8 ? wk.entry(wk.t.block(i + 1), lane) : -1;
-        if (i < wk.b1)
+    while (ok && __any_sync(0xffffffffu, wk.next())) {
+      const int b0 = __shfl_sync(0xffffffffu, wk.b0, 0), b1 = __shfl_sync(0xffffffffu, wk.b1, 0);
+      int pg = lane < 8 ? wk.entry(wk.t.block(b0), lane) : -1, pg_v = -1;
+      for (int i = b0; ok && i <= b1; ++i) {
+        const int pg_next = i + 1 < b1 && lane < 8 ? wk.entry(wk.t.block(i + 1), lane) : -1;
+        if (i < b1)
           for (int u = 0; ok && u < C::KU; ++u) ok = unit(0, u, pg);
-        if (i > wk.b0)
+        if (i > b0)
           for (int u = 0; ok && u < C::VU; ++u) ok = unit(1, u, pg_v);
         pg_v = pg;
         pg = pg_next;
@@ -544,64 +550,84 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kWarpMma) {
     // -------------------------------------------------------- product issuer
-    if (rank == 0 && lane == 0) {
+    // The whole warp walks along, with loop bounds and waits that are uniform
+    // by construction (votes, shuffles), and one elected lane issues: so the
+    // operands sit in uniform registers. In one lane's own branch each product
+    // took about 100 cycles to issue.
+    if (rank == 0) {
       constexpr uint32_t kIdS = instr_desc(M, kBN, 0), kIdO = instr_desc(M, DH, 1);
       const uint32_t qa = smem_u32(sq), ra = smem_u32(ring);
-      int n = 0, nb = 0;  // units and blocks consumed
+      int slot = 0, phase = 0, blk = 0;  // ring position, block whose scores come next
       bool ok = true;
-      auto scores = [&](int blk) {  // S[blk & 1] = Q K^T
-        bool first = true;
-        for (int u = 0; u < C::KU; ++u, ++n) {
-          const int slot = n % C::kSlots;
-          if (!wait1(ms.ready[slot], (n / C::kSlots) & 1)) return false;
-          tc_fence_after();
-          const uint32_t kb = ra + slot * C::kSlot;
-#pragma unroll
-          for (int sl = 0; sl < C::slabs_k(0); ++sl) {
-            if (sl >= C::slabs_k(u)) break;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              mma_ss<CG>(tm + 256 + (blk & 1) * kBN, smem_desc(qa + ((CG == 2 ? 0 : 2 * u) + sl) * 16384 + k * 32, 16, 1024),
-                         smem_desc(kb + sl * C::kKeysK * 128 + k * 32, 16, 1024), kIdS, !first);
-              first = false;
-            }
-          }
-          mma_commit<CG>(bar(ms.empty[slot]));
+      auto step_slot = [&] {
+        if (++slot == C::kSlots) {
+          slot = 0;
+          phase ^= 1;
         }
-        mma_commit<CG>(bar(ms.s_full[blk & 1]));
+      };
+      auto scores = [&]() {  // S[blk & 1] = Q K^T
+        const uint32_t d = tm + 256 + (blk & 1) * kBN;
+#pragma unroll
+        for (int u = 0; u < C::KU; ++u) {
+          if (!wait(ms.ready[slot], phase)) return false;
+          tc_fence_after();
+          const uint64_t da = smem_desc(qa + (CG == 2 ? 0 : 2 * u) * 16384, 16, 1024);
+          const uint64_t db = smem_desc(ra + slot * C::kSlot, 16, C::kBoxSlabsK * 1024);
+          if (elect_one()) {
+#pragma unroll
+            for (int sl = 0; sl < C::slabs_k(u); ++sl)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ss<CG>(d, da + sl * 1024 + k * 2, db + sl * 64 + k * 2, kIdS, u + sl + k > 0);
+            mma_commit<CG>(bar(ms.empty[slot]));
+            if (u + 1 == C::KU) mma_commit<CG>(bar(ms.s_full[blk & 1]));
+          }
+          __syncwarp();
+          step_slot();
+        }
+        ++blk;
         return true;
       };
-      while (ok && wk.next()) {
-        ok = wait1(ms.q_ready, wk.seg & 1);
+      while (ok && __any_sync(0xffffffffu, wk.next())) {
+        const int count = __shfl_sync(0xffffffffu, wk.b1 - wk.b0, 0);
+        ok = wait(ms.q_ready, wk.seg & 1);
         if (!ok) break;
         tc_fence_after();
-        for (int i = wk.b0; i <= wk.b1; ++i) {
-          if (i < wk.b1) {
-            ok = scores(nb + (i - wk.b0));
+        for (int i = 0; i <= count; ++i) {
+          if (i < count) {
+            ok = scores();
             if (!ok) break;
-            if (i + 1 == wk.b1) mma_commit<CG>(bar(ms.q_free));
+            if (i + 1 == count) {
+              if (elect_one()) mma_commit<CG>(bar(ms.q_free));
+              __syncwarp();
+            }
           }
-          if (i == wk.b0) continue;
-          const int blk = nb + (i - 1 - wk.b0);
-          ok = wait1(ms.p_ready[blk & 1], (blk >> 1) & 1);
+          if (i == 0) continue;
+          const int pb = blk - (i < count ? 2 : 1);  // the block whose weights are next
+          ok = wait(ms.p_ready[pb & 1], (pb >> 1) & 1);
           if (!ok) break;
-          for (int u = 0; u < C::VU; ++u, ++n) {
-            const int slot = n % C::kSlots;
-            ok = wait1(ms.ready[slot], (n / C::kSlots) & 1);
+#pragma unroll
+          for (int u = 0; u < C::VU; ++u) {
+            ok = wait(ms.ready[slot], phase);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t vb = ra + slot * C::kSlot;
+            const uint32_t pa = tm + 256 + (pb & 1) * kBN;
+            const uint64_t db = smem_desc(ra + slot * C::kSlot, 2048, 1024);
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < C::kKeysV / 16; ++k)
-              mma_ts<CG>(tm, tm + 256 + (blk & 1) * kBN + p_col(u * C::kKeysV + k * 16),
-                         smem_desc(vb + k * 2048, C::kKeysV * 128, 1024), kIdO, !(i - 1 == wk.b0 && u == 0 && k == 0));
-            mma_commit<CG>(bar(ms.empty[slot]));
+              for (int k = 0; k < C::kKeysV / 16; ++k)
+                mma_ts<CG>(tm, pa + p_col(u * C::kKeysV + k * 16), db + k * C::kSlabsV * 128, kIdO, u + k > 0 || i > 1);
+              mma_commit<CG>(bar(ms.empty[slot]));
+              if (u + 1 == C::VU) {
+                mma_commit<CG>(bar(ms.pv_done));
+                if (i == count) mma_commit<CG>(bar(ms.o_full));
+              }
+            }
+            __syncwarp();
+            step_slot();
           }
           if (!ok) break;
-          mma_commit<CG>(bar(ms.pv_done));
-          if (i == wk.b1) mma_commit<CG>(bar(ms.o_full));
         }
-        nb += wk.b1 - wk.b0;
       }
     }
   } else if (warp < 8) {
@@ -804,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = pt; q < nkeys * nsl * 8; q += kPT) {
             uint4* ptr = reinterpret_cast<uint4*>(dst + q * 16);
             uint4 x = *ptr;
-            const int key = (q / 8) % nkeys;
+            const int key = q / (nsl * 128) * kPage + q / 8 % kPage;  // [page][slab][16][128 B]
             bool bad = false;
             uint32_t* w = &x.x;
 #pragma unroll
@@ -848,7 +874,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             codes[t] = *reinterpret_cast<const uint4*>(src + pb * (kPage * C::kBox) + t * 512 + lane * 16);
             d[t] = sc[(page * kPage + tok0 + t * kTok) * (2 * NS) + (slab0 * 64 + dim) / 32];
           }
-          uint8_t* const slab = dst + sl * nkeys * 128 + page * kPage * 128;
+          // K: [8 tokens][slab][8][128 B], V: [page][slab][16][128 B]
+          const int group = kv ? 1024 : C::kBoxSlabsK * 1024;  // from tokens 0-7 of the page to 8-15
+          uint8_t* const slab = dst + page * kPage * 128 * (kv ? C::kSlabsV : C::kBoxSlabsK) + sl * (kv ? 2048 : 1024);
 #pragma unroll
           for (int t = 0; t < kSteps; ++t) {
             const int tok = tok0 + t * kTok;
@@ -875,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               found |= bad;
             }
             // the two 16-byte pieces in an order that keeps the 128-byte rows of neighbouring slabs on other banks
-            uint8_t* row = slab + tok * 128;
+            uint8_t* row = slab + (tok >> 3) * group + (tok & 7) * 128;
             const uint4 v0 = make_uint4(o[0], o[1], o[2], o[3]), v1 = make_uint4(o[4], o[5], o[6], o[7]);
             *reinterpret_cast<uint4*>(row + (((ch + odd) ^ (tok & 7)) << 4)) = odd ? v1 : v0;
             *reinterpret_cast<uint4*>(row + (((ch + 1 - odd) ^ (tok & 7)) << 4)) = odd ? v0 : v1;
