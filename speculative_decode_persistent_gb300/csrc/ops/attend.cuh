@@ -892,21 +892,26 @@ __global__ void __launch_bounds__(kThreads, 1)
               o[2 * j] = *reinterpret_cast<const uint32_t*>(&a2);
               o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&b2);
             }
-            if (gone || partly) {
-              const int key = page * kPage + tok;
-              const bool none = gone >> page & 1;
-              const bool bad = partly && !none && key < end && (__half_as_ushort(d[t]) & 0x7c00u) == 0x7c00u;
-              if (none || bad || (kv && key >= end)) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = 0;
-              }
-              found |= bad;
-            }
             // the two 16-byte pieces in an order that keeps the 128-byte rows of neighbouring slabs on other banks
             uint8_t* row = slab + (tok >> 3) * group + (tok & 7) * 128;
             const uint4 v0 = make_uint4(o[0], o[1], o[2], o[3]), v1 = make_uint4(o[4], o[5], o[6], o[7]);
             *reinterpret_cast<uint4*>(row + (((ch + odd) ^ (tok & 7)) << 4)) = odd ? v1 : v0;
             *reinterpret_cast<uint4*>(row + (((ch + 1 - odd) ^ (tok & 7)) << 4)) = odd ? v0 : v1;
+          }
+          if (gone || partly) {  // missing pages read as zeros, unseen V values too
+#pragma unroll 1
+            for (int t = 0; t < kSteps; ++t) {
+              const int tok = tok0 + t * kTok, key = page * kPage + tok;
+              const uint32_t scale = __half_as_ushort(sc[key * (2 * NS) + (slab0 * 64 + dim) / 32]);
+              const bool none = gone >> page & 1;
+              const bool bad = partly && !none && key < end && (scale & 0x7c00u) == 0x7c00u;
+              if (none || bad || (kv && key >= end)) {
+                uint8_t* row = slab + (tok >> 3) * group + (tok & 7) * 128;
+                *reinterpret_cast<uint4*>(row + ((ch ^ (tok & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (tok & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+              }
+              found |= bad;
+            }
           }
         }
         fence_async_shared();

@@ -1,5 +1,5 @@
-// Shared by the KV-cache operators: argument checks, the row map, the q8
-// codec and typed loads and stores of eight elements.
+// Shared by the KV-cache operators: argument checks, the row map, and
+// typed loads and stores of eight elements.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -128,39 +128,6 @@ __device__ __forceinline__ void store8(typename Elem<DT>::T* p, const float* x) 
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = t[i];
   }
-}
-
-// ----------------------------------------------------------------- q8 codec
-// binary16 nearest to amax / 127 (ties to even): the rounded single-precision
-// quotient, then the exact comparison of amax with 127 x the midpoints to its
-// neighbours (at most 19 significant bits, so exact).
-__device__ __forceinline__ __half q8_scale(float amax) {
-  const unsigned u = __half_as_ushort(__float2half_rn(amax / 127.0f));
-  const float hf = __half2float(__ushort_as_half(static_cast<unsigned short>(u)));
-  unsigned r = u;
-  if (u < 0x7bffu) {
-    const float pm = 127.0f * (0.5f * (hf + __half2float(__ushort_as_half(static_cast<unsigned short>(u + 1)))));
-    if (amax > pm || (amax == pm && (u & 1u))) r = u + 1;
-  }
-  if (u > 0 && u < 0x7c00u) {
-    const float pm = 127.0f * (0.5f * (hf + __half2float(__ushort_as_half(static_cast<unsigned short>(u - 1)))));
-    if (amax < pm || (amax == pm && (u & 1u))) r = u - 1;
-  }
-  return __ushort_as_half(static_cast<unsigned short>(r));
-}
-
-// round-half-even of x / d clamped to [-127, 127], exactly, given inv = 1/d
-// rounded: |x inv| < 256 is off by less than 2^-14 before it is rounded, so
-// the candidate is at most one step off, and the exact remainder x - q d
-// (q d has at most 19 significant bits) says in which direction.
-__device__ __forceinline__ int q8_code(float x, float d, float inv) {
-  if (d == 0.f) return 0;
-  float q = rintf(x * inv);
-  const float r = fmaf(-q, d, x), h = 0.5f * d;
-  const bool odd = (static_cast<int>(q) & 1) != 0;
-  if (r > h || (r == h && odd)) q += 1.f;
-  else if (r < -h || (r == -h && odd)) q -= 1.f;
-  return static_cast<int>(fminf(fmaxf(q, -127.f), 127.f));
 }
 
 }  // namespace ops

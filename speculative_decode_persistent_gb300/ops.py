@@ -17,10 +17,11 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
-from .mk import MK_KV_F16, MK_KV_Q8, MkError, i32, lib, sz, vp
+from .mk import LIB_PATH, MK_KV_F16, MK_KV_Q8, MkError, i32, lib, sz, vp
 
 PAGE_TOKENS = 16
 MK_OPS_MAX_SEQS = 1024
@@ -59,14 +60,23 @@ for _name, _res, _args in (
     _fn.restype, _fn.argtypes = _res, _args
 EXPORTS = ["mk_kv_write", "mk_kv_read", "mk_attend_work_bytes", "mk_attend"]
 
+# The calls below pass the structs as packed bytes, which costs a few hundred
+# nanoseconds less a field than ctypes structures: a small call is bound by
+# this file, not by the GPU.
+_fast = ctypes.CDLL(LIB_PATH)
+for _name, _n in (("mk_kv_write", 4), ("mk_kv_read", 4), ("mk_attend", 3)):
+    _fn = getattr(_fast, _name)
+    _fn.restype, _fn.argtypes = i32, [vp] * _n + ([i32] if _n == 4 else []) + [vp]
+_kv_write, _kv_read, _attend = _fast.mk_kv_write, _fast.mk_kv_read, _fast.mk_attend
+_POOL, _ROWS, _DENSE, _ARGS = (struct.Struct(f).pack for f in ("@4P4i", "@3P4i", "@Pqq", "@PqqPqqPqqiifiiPQ"))
+assert all(struct.calcsize(f) <= ctypes.sizeof(t) for f, t in (
+    ("@4P4i", mk_kv_pool), ("@3P4i", mk_kv_rows), ("@Pqq", mk_dense), ("@PqqPqqPqqiifiiPQ", mk_attend_args)))
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_HALF = (torch.float16, torch.int16)
+
 
 def _refuse(what: str):
     raise MkError(_INVALID, what)
-
-
-def _check(rc: int, what: str):
-    if rc != 0:
-        raise MkError(rc, what)
 
 
 class KVPool:
@@ -76,30 +86,32 @@ class KVPool:
     or int16 views of its bits), or int8 codes with k_scale, v_scale
     [pages][kv heads][16][head dim / 32] (binary16 likewise)."""
 
+    __slots__ = ("tensors", "device", "q8", "n_pages", "hkv", "dh", "c")
+
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        if k.dim() != 4 or k.shape != v.shape or k.shape[2] != PAGE_TOKENS or k.dtype != v.dtype:
+        shape, dtype, device = k.shape, k.dtype, k.device
+        if len(shape) != 4 or v.shape != shape or shape[2] != PAGE_TOKENS or v.dtype != dtype:
             _refuse("KVPool (k and v are [pages][kv heads][16][head dim] of one type)")
-        half = (torch.float16, torch.int16)
-        self.q8 = k.dtype == torch.int8
-        every = [k, v]
-        if self.q8:
-            want = k.shape[:3] + (k.shape[3] // 32,)
-            for s in (k_scale, v_scale):
-                if s is None or s.dtype not in half or tuple(s.shape) != tuple(want):
-                    _refuse("KVPool (an int8 pool needs binary16 scales [pages][kv heads][16][head dim / 32])")
-                every.append(s)
-        elif k.dtype not in half or k_scale is not None or v_scale is not None:
-            _refuse("KVPool (binary16, or int8 codes with scales)")
-        if not all(t.is_contiguous() for t in every):
+        self.q8 = dtype == torch.int8
+        self.n_pages, self.hkv, _, self.dh = shape
+        if not (k.is_contiguous() and v.is_contiguous()):
             _refuse("KVPool (contiguous tensors)")
-        if any(t.device != k.device for t in every):
+        if v.device != device:
             _refuse("KVPool (one device)")
-        self.tensors, self.device = every, k.device
-        self.n_pages, self.hkv, _, self.dh = k.shape
-        self.c = mk_kv_pool(k.data_ptr(), v.data_ptr(), every[2].data_ptr() if self.q8 else None,
-                            every[3].data_ptr() if self.q8 else None, MK_KV_Q8 if self.q8 else MK_KV_F16,
-                            self.n_pages, self.hkv, self.dh)
-        self.ref = ctypes.byref(self.c)
+        self.device = device
+        if self.q8:
+            want = (self.n_pages, self.hkv, PAGE_TOKENS, self.dh // 32)
+            for s in (k_scale, v_scale):
+                if s is None or s.dtype not in _HALF or s.shape != want or not s.is_contiguous() or s.device != device:
+                    _refuse("KVPool (an int8 pool needs binary16 scales [pages][kv heads][16][head dim / 32])")
+            self.tensors = (k, v, k_scale, v_scale)
+            self.c = _POOL(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), MK_KV_Q8, self.n_pages,
+                           self.hkv, self.dh)
+        else:
+            if dtype not in _HALF or k_scale is not None or v_scale is not None:
+                _refuse("KVPool (binary16, or int8 codes with scales)")
+            self.tensors = (k, v)
+            self.c = _POOL(k.data_ptr(), v.data_ptr(), 0, 0, MK_KV_F16, self.n_pages, self.hkv, self.dh)
 
 
 class KVRows:
@@ -111,71 +123,74 @@ class KVRows:
     that makes its outputs). max_q: the most new rows of one sequence (default
     n_rows), a hint for the choice of a kernel."""
 
+    __slots__ = ("tensors", "device", "n_seqs", "n_rows", "max_q", "_head", "_stride")
+
     def __init__(self, row_start, kv_len, tables, n_rows=None, max_q=None):
-        for t in (row_start, kv_len, tables):
-            if t.dtype != torch.int32 or not t.is_contiguous():
-                _refuse("KVRows (contiguous int32 tensors)")
-        if tables.dim() != 2 or kv_len.dim() != 1 or row_start.dim() != 1:
+        i = torch.int32
+        if row_start.dtype != i or kv_len.dtype != i or tables.dtype != i:
+            _refuse("KVRows (contiguous int32 tensors)")
+        if not (row_start.is_contiguous() and kv_len.is_contiguous() and tables.is_contiguous()):
+            _refuse("KVRows (contiguous int32 tensors)")
+        shape, n = tables.shape, kv_len.shape
+        if len(shape) != 2 or len(n) != 1 or row_start.shape != (n[0] + 1,) or shape[0] != n[0]:
             _refuse("KVRows (row_start [n + 1], kv_len [n], tables [n][pages])")
-        n = kv_len.shape[0]
-        if row_start.shape[0] != n + 1 or tables.shape[0] != n:
-            _refuse("KVRows (row_start [n + 1], kv_len [n], tables [n][pages])")
-        if row_start.device != kv_len.device or tables.device != kv_len.device:
+        device = kv_len.device
+        if row_start.device != device or tables.device != device:
             _refuse("KVRows (one device)")
         if n_rows is not None and n_rows < 0 or max_q is not None and max_q < 0:
             _refuse("KVRows (counts of rows)")
-        self.tensors, self.device = (row_start, kv_len, tables), kv_len.device
-        self.n_seqs, self.n_rows, self.max_q = n, n_rows, max_q
-        self.c = mk_kv_rows(row_start.data_ptr(), kv_len.data_ptr(), tables.data_ptr(), n, 0, tables.shape[1], 0)
-        self.ref = ctypes.byref(self.c)
+        self.tensors, self.device = (row_start, kv_len, tables), device
+        self.n_seqs, self.n_rows, self.max_q = n[0], n_rows, max_q
+        self._head, self._stride = (row_start.data_ptr(), kv_len.data_ptr(), tables.data_ptr(), n[0]), shape[1]
 
     def _at(self, n_rows: int):
         """The C view for dense tensors of n_rows rows."""
-        self.c.n_rows = n_rows
-        self.c.max_q = n_rows if self.max_q is None else min(self.max_q, n_rows)
-        return self.ref
+        return _ROWS(*self._head, n_rows, self._stride, n_rows if self.max_q is None else min(self.max_q, n_rows))
 
 
 def _dense(t, heads: int, dh: int, what: str, out=False):
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dh:
+    """(address, row stride, head stride) of a dense tensor, checked."""
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dh:
         _refuse(f"{what} ([rows][{heads}][{dh}])")
-    if dh > 1 and t.stride(2) != 1:
+    row, head, one = t.stride()
+    if one != 1:
         _refuse(f"{what} (contiguous head dim)")
-    if out and t.shape[0] and not (t.stride(1) >= dh and (t.shape[0] == 1 or t.stride(0) >= (heads - 1) * t.stride(1) + dh)):
+    if out and shape[0] and not (head >= dh and (shape[0] == 1 or row >= (heads - 1) * head + dh)):
         _refuse(f"{what} (rows of an output must not overlap)")
     if t.requires_grad and torch.is_grad_enabled():
         _refuse(f"{what} (no gradient is defined: detach it or use torch.no_grad)")
-    return mk_dense(t.data_ptr(), t.stride(0), t.stride(1))
+    return t.data_ptr(), row, head
 
 
-def _same(pool: KVPool, rows: KVRows, *tensors):
-    n = tensors[0].shape[0]
+def _same(pool: KVPool, rows: KVRows, t, *more):
+    """Rows and device index of dense tensors that belong together."""
+    n, dtype, device = t.shape[0], t.dtype, pool.device
     if rows.n_rows is not None and rows.n_rows != n:
         _refuse("rows of the dense tensors differ from KVRows.n_rows")
-    if any(t.shape[0] != n or t.dtype != tensors[0].dtype for t in tensors):
-        _refuse("dense tensors of one type with one number of rows")
-    if tensors[0].dtype not in DTYPES:
+    for x in more:
+        if x.shape[0] != n or x.dtype != dtype:
+            _refuse("dense tensors of one type with one number of rows")
+    if dtype not in DTYPES:
         _refuse("dense tensors are float32, float16 or bfloat16")
-    if pool.device.type != "cuda" or rows.device != pool.device or any(t.device != pool.device for t in tensors):
+    if device.type != "cuda" or rows.device != device or t.device != device:
         _refuse("pool, rows and dense tensors on one CUDA device")
-    return n
+    for x in more:
+        if x.device != device:
+            _refuse("pool, rows and dense tensors on one CUDA device")
+    return n, device.index
 
 
-class _On:
-    """The tensors' device made current for a call."""
-
-    def __init__(self, device):
-        self.device = device
-
-    def __enter__(self):
-        self.was = torch.cuda.current_device()
-        if self.was != self.device.index:
-            torch.cuda.set_device(self.device)
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.was != self.device.index:
-            torch.cuda.set_device(self.was)
+def _run(device: int, what: str, fn, *args):
+    """fn(*args, stream) with the device current, on its current stream."""
+    was = torch._C._cuda_getDevice()
+    if was == device:
+        rc = fn(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _raw_stream(device))
+    if rc != 0:
+        raise MkError(rc, what)
 
 
 def kv_write(pool: KVPool, rows: KVRows, k, v) -> None:
@@ -183,9 +198,8 @@ def kv_write(pool: KVPool, rows: KVRows, k, v) -> None:
     rounded to binary16 or quantised as the fused step does. Two rows of one
     call must not share a slot of the pool."""
     kd, vd = _dense(k, pool.hkv, pool.dh, "kv_write k"), _dense(v, pool.hkv, pool.dh, "kv_write v")
-    n = _same(pool, rows, k, v)
-    with _On(pool.device) as stream:
-        _check(lib.mk_kv_write(pool.ref, rows._at(n), kd, vd, DTYPES[k.dtype], stream), "mk_kv_write")
+    n, device = _same(pool, rows, k, v)
+    _run(device, "mk_kv_write", _kv_write, pool.c, rows._at(n), _DENSE(*kd), _DENSE(*vd), DTYPES[k.dtype])
 
 
 def kv_read(pool: KVPool, rows: KVRows, dtype=torch.float16, out=None):
@@ -195,13 +209,17 @@ def kv_read(pool: KVPool, rows: KVRows, dtype=torch.float16, out=None):
     if out is None:
         if rows.n_rows is None:
             _refuse("kv_read (KVRows.n_rows or out)")
-        out = tuple(torch.empty((rows.n_rows, pool.hkv, pool.dh), dtype=dtype, device=pool.device) for _ in "kv")
-    k, v = out
-    kd, vd = (_dense(t, pool.hkv, pool.dh, "kv_read out", out=True) for t in (k, v))
-    n = _same(pool, rows, k, v)
-    with _On(pool.device) as stream:
-        _check(lib.mk_kv_read(pool.ref, rows._at(n), kd, vd, DTYPES[k.dtype], stream), "mk_kv_read")
+        shape = (rows.n_rows, pool.hkv, pool.dh)
+        k, v = torch.empty(shape, dtype=dtype, device=pool.device), torch.empty(shape, dtype=dtype, device=pool.device)
+    else:
+        k, v = out
+    kd, vd = _dense(k, pool.hkv, pool.dh, "kv_read out", True), _dense(v, pool.hkv, pool.dh, "kv_read out", True)
+    n, device = _same(pool, rows, k, v)
+    _run(device, "mk_kv_read", _kv_read, pool.c, rows._at(n), _DENSE(*kd), _DENSE(*vd), DTYPES[k.dtype])
     return k, v
+
+
+_work_bytes: dict = {}  # of mk_attend_work_bytes, which goes by the head dim alone
 
 
 def attend(pool: KVPool, rows: KVRows, q, scale=None, window: int = 0, sinks: int = 0, gate=None, out=None):
@@ -215,23 +233,27 @@ def attend(pool: KVPool, rows: KVRows, q, scale=None, window: int = 0, sinks: in
     no sequence are left as they are, undefined when it is made here)."""
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    hq = q.shape[1] if q.dim() == 3 else 0
-    a = mk_attend_args()
-    a.q = _dense(q, hq, pool.dh, "attend q")
-    a.out = _dense(out, hq, pool.dh, "attend out", out=True)
+    hq, dh = q.shape[1] if q.dim() == 3 else 0, pool.dh
+    qd, od = _dense(q, hq, dh, "attend q"), _dense(out, hq, dh, "attend out", True)
     if gate is None:
-        n = _same(pool, rows, q, out)
+        gd = (0, 0, 0)
+        n, device = _same(pool, rows, q, out)
     else:
-        a.gate = _dense(gate, hq, pool.dh, "attend gate")
-        n = _same(pool, rows, q, out, gate)
-    a.hq, a.dtype = hq, DTYPES[q.dtype]
-    a.scale = 1.0 / math.sqrt(pool.dh) if scale is None else scale
-    a.window, a.sinks = window, sinks
-    with _On(pool.device) as stream:
-        ref = rows._at(n)
-        nbytes = lib.mk_attend_work_bytes(pool.ref, ref, hq)
-        # from torch's allocator, so calls on other streams and captured graphs have their own
-        work = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=pool.device)
-        a.work, a.work_bytes = work.data_ptr(), work.numel()
-        _check(lib.mk_attend(pool.ref, ref, ctypes.byref(a), stream), "mk_attend")
+        gd = _dense(gate, hq, dh, "attend gate")
+        n, device = _same(pool, rows, q, out, gate)
+    scale = 1.0 / math.sqrt(dh) if scale is None else float(scale)
+    if not (0.0 < scale < 3.4e38 and 0 <= window < 2 ** 31 and 0 <= sinks < 2 ** 31):
+        _refuse("attend (a finite positive scale, a window and sinks of at least 0)")
+    at = rows._at(n)
+    nbytes = _work_bytes.get(dh)
+    if nbytes is None:
+        nbytes = lib.mk_attend_work_bytes(mk_kv_pool.from_buffer_copy(pool.c),
+                                          mk_kv_rows.from_buffer_copy(at), hq)
+        if nbytes:
+            _work_bytes[dh] = nbytes
+    # from torch's allocator, so calls on other streams and captured graphs have their own
+    work = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=pool.device)
+    args = _ARGS(*qd, *gd, *od, hq, DTYPES[q.dtype], scale, window, sinks, work.data_ptr(),
+                 work.numel())
+    _run(device, "mk_attend", _attend, pool.c, at, args)
     return out
