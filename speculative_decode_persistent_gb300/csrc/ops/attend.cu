@@ -22,8 +22,10 @@ mk_status check_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, int32_t h
   if (st != MK_OK) return st;
   if (hq <= 0 || hq % pool->hkv) return MK_ERR_INVALID;
   if (hq / pool->hkv > 256) return MK_ERR_UNSUPPORTED;
-  // (row, head) pairs are counted with 32 bits
-  return static_cast<int64_t>(rows->n_rows) * hq > 0x7fff0000ll ? MK_ERR_UNSUPPORTED : MK_OK;
+  // (row, head) pairs, and the blocks of all tiles, are counted with 32 bits
+  if (static_cast<int64_t>(rows->n_rows) * hq > 0x7fff0000ll) return MK_ERR_UNSUPPORTED;
+  const double tiles = static_cast<double>(rows->n_rows) * hq / 128 + static_cast<double>(rows->n_seqs) * pool->hkv;
+  return tiles * (rows->table_stride / (kBN / kPage) + 2 + kItemCost) > 2e9 ? MK_ERR_UNSUPPORTED : MK_OK;
 }
 
 constexpr size_t kJoinBytes = (kMaxWorkers * sizeof(JoinInfo) + 255) / 256 * 256;
@@ -113,7 +115,7 @@ extern "C" mk_status mk_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, c
   // would have no rows, and single blocks keep twice as many copies going.
   const int cg = ns % 2 == 0 && static_cast<int64_t>(rows->max_q) * p.G > 128 ? 2 : 1;
   CUtensorMap tk, tv;
-  const int box = q8_box(ns, cg), slabs_k = cg == 2 || ns < 2 ? ns : 2, slabs_v = ns / cg;
+  const int box = q8_box(ns, cg), slabs_k = ns, slabs_v = ns / cg;
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess || !encode_map(&tk, pool->k, *pool, box, 8, slabs_k) ||
       !encode_map(&tv, pool->v, *pool, box, kPage, slabs_v))

@@ -19,11 +19,13 @@
 // reads both halves, so a block fetches and stores half the bytes per product.
 //
 // Work. All (sequence, kv head, tile) items are cut into 128-token blocks of
-// what their rows can see (a window skips the middle); the blocks of all items
-// form one line that is cut evenly among the workers (blocks or pairs). An
-// item cut in two or more leaves unnormalised parts, which attend_join adds
-// in a fixed order: results do not depend on timing. Every worker finds its
-// piece from the lengths on the device, so nothing is planned on the host.
+// what their rows can see (a window skips the middle). The blocks of all items,
+// each item's behind kItemCost units that stand for its start and end (query
+// rows, result), form one line that is cut evenly among the workers (blocks or
+// pairs). An item cut in two or more leaves unnormalised parts, which
+// attend_join adds in a fixed order: results do not depend on timing. Every
+// worker finds its piece from the lengths on the device, so nothing is planned
+// on the host.
 //
 // Operand units in shared memory, 128-byte rows of 64 dims (a slab), swizzled:
 // K as [8 tokens][slab][8 rows], V as [page][slab][16 rows], so that one copy
@@ -56,6 +58,8 @@ namespace ops {
 constexpr int kBN = 128;             // tokens per block: eight pages
 constexpr int kMaxWorkers = 160;     // at least the SM count
 constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kJoinSplit = 8;        // join blocks per cut
+constexpr int kItemCost = 4;         // an item's start and end, in blocks
 
 // A worker's first item, when it began at an earlier worker: what the join needs.
 struct JoinInfo {
@@ -130,51 +134,44 @@ __device__ __forceinline__ uint32_t seen_bits(int p, int base, int window, int s
 // Column of S's 128 in which P of token t (even) lies: each half over its own scores.
 __host__ __device__ constexpr int p_col(int t) { return t / 64 * 64 + t % 64 / 2; }
 
-// A worker's walk through the line of blocks: segments of consecutive blocks
-// of one item. Every role walks it for itself.
+// A worker's walk through the line: segments of consecutive blocks of one
+// item. Every role walks it for itself.
 struct Start {
-  int s, h, mt, blk;
-  int64_t n;  // blocks of this worker
+  int s, h, mt, off, n;  // item, offset into its part of the line, length of the worker's piece
+  SeqView v;
 };
 struct Walk {
   const AttendParams* a;
-  int s, h, mt, blk, n_mt, M, seg;
-  int64_t left;
+  int s, h, mt, off, left, n_mt, M, seg;
   SeqView v;
   Tile t;
   int b0, b1;  // block indices [b0, b1) of the current segment
   __device__ __forceinline__ Walk(const AttendParams& p, const Start& st, int M_)
-      : a(&p), s(st.s), h(st.h), mt(st.mt), blk(st.blk), M(M_), seg(-1), left(st.n) {
-    if (left > 0) {
-      v = seq_view(p.rows, s);
-      n_mt = tiles_of(v, p.G, M);
-    }
+      : a(&p), s(st.s), h(st.h), mt(st.mt), off(st.off), left(st.n), M(M_), seg(-1), v(st.v) {
+    n_mt = left > 0 ? tiles_of(v, p.G, M) : 0;
   }
   __device__ __forceinline__ bool next() {
-    if (seg >= 0) {
-      left -= b1 - b0;
-      if (left <= 0) return false;
-      blk = 0;
-      if (++mt == n_mt) {
-        mt = 0;
-        if (++h == a->pool.hkv) {
-          h = 0;
-          do {
-            if (++s >= a->rows.n_seqs) return false;  // (only if the lengths changed under the kernel)
-            v = seq_view(a->rows, s);
-            n_mt = tiles_of(v, a->G, M);
-          } while (n_mt == 0);
-        }
+    if (left <= 0) return false;
+    if (seg >= 0 && ++mt == n_mt) {
+      mt = 0;
+      if (++h == a->pool.hkv) {
+        h = 0;
+        do {
+          if (++s >= a->rows.n_seqs) return false;  // (only if the lengths changed under the kernel)
+          v = seq_view(a->rows, s);
+          n_mt = tiles_of(v, a->G, M);
+        } while (n_mt == 0);
       }
-    } else if (left <= 0) {
-      return false;
     }
     ++seg;
     t = make_tile(v, a->G, M, mt, a->window, a->sinks);
-    b0 = blk;
-    b1 = static_cast<int>(min(static_cast<int64_t>(t.nblk), blk + left));
-    return true;
+    b0 = max(0, off - kItemCost);
+    b1 = min(t.nblk, max(0, off + left - kItemCost));
+    left -= t.nblk + kItemCost - off;
+    off = 0;
+    return b1 > b0;  // a piece that ends in an item's start leaves it to the next worker
   }
+  __device__ __forceinline__ bool more() const { return left > kItemCost; }  // another segment follows
   __device__ __forceinline__ bool whole() const { return b0 == 0 && b1 == t.nblk; }
   // Table entry of the block's i-th 16 tokens, -1 behind the table; as loaded,
   // so that a load ahead is waited for only where has_page() looks at it.
@@ -192,12 +189,17 @@ template <int NS, bool Q8, int CG>
 struct Cfg {
   static constexpr int DH = NS * 64, M = 128 * CG;
   // units: what one ring slot holds, nkeys tokens x nsl slabs of 64 dims
-  static constexpr int KU = CG == 2 ? 1 : (NS + 1) / 2;  // K: all 128 tokens, two slabs each (pair: 64 tokens, all slabs)
+  // K: 64 tokens, all slabs, in pairs that one product reads across two
+  // neighbouring slots (kPairK: half the copies); of a q8 pool, whose units
+  // should be handed over as soon as they are converted, and of narrow heads
+  // all 128 tokens, two slabs each. Of two blocks each has its 64 tokens.
+  static constexpr bool kPairK = !Q8 && CG == 1 && NS > 2;
+  static constexpr int KU = CG == 2 ? 1 : (NS + 1) / 2;
   static constexpr int VU = CG == 2 ? 1 : NS > 2 ? 2 : 1;  // V: all slabs, split over the tokens (pair: half the slabs)
-  static constexpr int kKeysK = CG == 2 ? 64 : 128, kKeysV = CG == 2 ? 128 : 128 / VU;
+  static constexpr int kKeysK = CG == 2 || kPairK ? 64 : 128, kKeysV = CG == 2 ? 128 : 128 / VU;
   static constexpr int kSlabsV = CG == 2 ? NS / 2 : NS;
-  static __host__ __device__ constexpr int slabs_k(int u) { return CG == 2 ? NS : (NS - 2 * u < 2 ? NS - 2 * u : 2); }
-  static constexpr int kBoxSlabsK = CG == 2 || NS < 2 ? NS : 2;  // slabs a K copy fills (of a last odd one: zeros behind it)
+  static __host__ __device__ constexpr int slabs_k(int u) { return CG == 2 || kPairK ? NS : (NS - 2 * u < 2 ? NS - 2 * u : 2); }
+  static constexpr int kBoxSlabsK = CG == 2 || kPairK || NS < 2 ? NS : 2;  // slabs a K unit has room for
   static constexpr int kUnitK = kKeysK * kBoxSlabsK * 128, kUnitV = kKeysV * kSlabsV * 128;
   static constexpr int kSlot = kUnitK > kUnitV ? kUnitK : kUnitV;
   static constexpr int kQ = NS * 16384;
@@ -207,11 +209,12 @@ struct Cfg {
   // binary16 pool: all room for operand units. q8: units as stored are what is
   // in flight from memory, so two operand units are kept and the rest is for those.
   static constexpr int kFit = kBudget / kSlot;
-  static constexpr int kSlots = Q8 ? 2 : kFit > 8 ? 8 : kFit;
+  static constexpr int kSlots = Q8 ? 2 : kFit > 8 ? 8 : kPairK ? kFit / 2 * 2 : kFit;
   static constexpr int kRawFit = (kBudget - kSlots * kSlot) / kRaw;
   static constexpr int kRawSlots = !Q8 ? 0 : kRawFit > 6 ? 6 : kRawFit;
   static constexpr int kBox = q8_box(NS, CG);
   static constexpr int kSmem = kMisc + kQ + kSlots * kSlot + kRawSlots * kRaw;
+  static_assert(!kPairK || (kSlots % 2 == 0 && kSlot == kUnitK && kUnitK == kUnitV), "pairs of K units lie side by side");
   static_assert(kSlots >= 2 && (!Q8 || kRawSlots >= 4) && kSmem <= 232448, "ring");
   static_assert(!Q8 || (slabs_k(0) * 64 % kBox == 0 && kSlabsV * 64 % kBox == 0), "boxes");
 };
@@ -268,50 +271,50 @@ __device__ __forceinline__ void put_out(const AttendParams& a, int row, int head
 }
 
 // ---------------------------------------------------------------- scheduling
-// Total blocks of the line and this worker's piece of it. scratch: int64
-// [n_seqs + 1]. All threads of the block call it.
+// The line's length and this worker's piece of it. scratch: [n_seqs]. All
+// threads of the block call it. (The line has fewer than 2^31 units: the host
+// refuses longer ones.)
+__device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
+__device__ __forceinline__ int warp_scan(int x, int lane) {
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, k);
+    if (lane >= k) x += y;
+  }
+  return x;
+}
 template <int M>
-__device__ void find_start(const AttendParams& a, int64_t* scratch, Start* out, int worker, bool leader) {
+__device__ void find_start(const AttendParams& a, int* scratch, Start* out, int worker, bool leader) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, nw = blockDim.x / 32;
-  for (int s = warp; s < a.rows.n_seqs; s += nw) {
+  const int n_seqs = a.rows.n_seqs, hkv = a.pool.hkv;
+  for (int s = warp; s < n_seqs; s += nw) {
     const SeqView v = seq_view(a.rows, s);
     const int n = tiles_of(v, a.G, M);
-    int64_t sum = 0;
-    for (int mt = lane; mt < n; mt += 32) sum += make_tile(v, a.G, M, mt, a.window, a.sinks).nblk;
-#pragma unroll
-    for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    int sum = 0;
+    for (int mt = lane; mt < n; mt += 32) sum += make_tile(v, a.G, M, mt, a.window, a.sinks).nblk + kItemCost;
+    sum = warp_sum(sum);
     if (lane == 0) scratch[s] = sum;
   }
   __syncthreads();
   if (warp != 0) return;
-  int64_t total = 0;
-  for (int s0 = 0; s0 < a.rows.n_seqs; s0 += 32) {
-    int64_t x = s0 + lane < a.rows.n_seqs ? scratch[s0 + lane] : 0;
-#pragma unroll
-    for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-    total += x;
-  }
-  total *= a.pool.hkv;
-  const int64_t quota = max(static_cast<int64_t>(1), (total + a.workers - 1) / a.workers);
-  const int64_t g0 = worker * quota, n = min(quota, total - g0);
+  int total = 0;
+  for (int s0 = 0; s0 < n_seqs; s0 += 32) total += warp_sum(s0 + lane < n_seqs ? scratch[s0 + lane] : 0);
+  total *= hkv;
+  const int quota = max(1, total / a.workers + (total % a.workers > 0));
+  const int64_t g = static_cast<int64_t>(worker) * quota;
+  const int n = g < total ? min(quota, total - static_cast<int>(g)) : 0, g0 = static_cast<int>(g);
   if (leader && lane == 0) a.join[worker].w0 = -1;
   if (lane == 0) out->n = n;
   if (n <= 0) return;
-  // the sequence whose blocks hold g0, then the head, then the tile
-  int64_t at = 0, cost = 0;
-  int s = 0;
+  // the sequence whose part of the line holds g0, then the head, then the tile
+  int at = 0, cost = 0, s = 0;
   for (;; s += 32) {  // (g0 < total, so one of them holds it)
-    cost = s + lane < a.rows.n_seqs ? scratch[s + lane] : 0;
-    int64_t inc = cost * a.pool.hkv;
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, inc, k);
-      if (lane >= k) inc += y;
-    }
+    cost = s + lane < n_seqs ? scratch[s + lane] : 0;
+    const int inc = warp_scan(cost * hkv, lane);
     const uint32_t hit = __ballot_sync(0xffffffffu, g0 < at + inc);
-    const int l = hit ? __ffs(hit) - 1 : 31;
     if (hit) {
-      at += __shfl_sync(0xffffffffu, inc - cost * a.pool.hkv, l);
+      const int l = __ffs(hit) - 1;
+      at += __shfl_sync(0xffffffffu, inc - cost * hkv, l);
       cost = __shfl_sync(0xffffffffu, cost, l);
       s += l;
       break;
@@ -319,43 +322,40 @@ __device__ void find_start(const AttendParams& a, int64_t* scratch, Start* out, 
     at += __shfl_sync(0xffffffffu, inc, 31);
   }
   const SeqView v = seq_view(a.rows, s);
-  const int h = static_cast<int>((g0 - at) / cost);
+  const int h = (g0 - at) / cost;
   at += h * cost;
   const int n_mt = tiles_of(v, a.G, M);
-  int mt = 0;
+  int mt = 0, nblk = 0;
   for (;; mt += 32) {
     if (mt >= n_mt) {  // (only if the lengths changed under the kernel)
       if (lane == 0) out->n = 0;
       return;
     }
-    const int nb = mt + lane < n_mt ? make_tile(v, a.G, M, mt + lane, a.window, a.sinks).nblk : 0;
-    int64_t inc = nb;
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, inc, k);
-      if (lane >= k) inc += y;
-    }
+    const int nb = mt + lane < n_mt ? make_tile(v, a.G, M, mt + lane, a.window, a.sinks).nblk + kItemCost : 0;
+    const int inc = warp_scan(nb, lane);
     const uint32_t hit = __ballot_sync(0xffffffffu, g0 < at + inc && nb > 0);
     if (hit) {
       const int l = __ffs(hit) - 1;
       at += __shfl_sync(0xffffffffu, inc - nb, l);
+      nblk = __shfl_sync(0xffffffffu, nb, l) - kItemCost;
       mt += l;
       break;
     }
     at += __shfl_sync(0xffffffffu, inc, 31);
   }
   if (lane == 0) {
-    *out = Start{s, h, mt, static_cast<int>(g0 - at), n};
-    if (leader && g0 > at) {
-      const Tile t = make_tile(v, a.G, M, mt, a.window, a.sinks);
+    *out = Start{s, h, mt, g0 - at, n, v};
+    const int first = at + kItemCost;  // the item's first block
+    if (leader && g0 > first) {
       JoinInfo j;
       j.s = s;
       j.h = h;
       j.mt = mt;
-      j.w0 = static_cast<int>(at / quota);
-      j.w1 = static_cast<int>((at + t.nblk - 1) / quota);
-      j.slot0 = 2 * j.w0 + (at == j.w0 * quota ? 0 : 1);
-      j.rows = t.rows;
+      j.w0 = first / quota;
+      j.w1 = (first + nblk - 1) / quota;
+      // the first worker's segment is its first one when its piece begins in this item
+      j.slot0 = 2 * j.w0 + (j.w0 * quota >= at ? 0 : 1);
+      j.rows = min(M, v.q_len * a.G - mt * M);
       j.pad = 0;
       a.join[worker] = j;
     }
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kWarpMma) tmem_alloc<CG>(smem_u32(&ms.tmem), 512);
-  find_start<M>(a, reinterpret_cast<int64_t*>(ring), &ms.start, worker, rank == 0);
+  find_start<M>(a, reinterpret_cast<int*>(ring), &ms.start, worker, rank == 0);
   tc_fence_before();
   fence_async_shared();  // the scratch lay where tensor copies go
   __syncthreads();
@@ -479,8 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // unit u of K (kv = 0) or V of block b, whose page ids the lanes 0..7 hold
     auto unit = [&](int kv, int u, int pg) {
       const int nkeys = kv ? C::kKeysV : C::kKeysK, nsl = kv ? C::kSlabsV : C::slabs_k(u);
-      const int key0 = CG == 2 ? (kv ? 0 : 64 * rank) : (kv ? u * C::kKeysV : 0);
-      const int slab0 = CG == 2 ? (kv ? rank * C::kSlabsV : 0) : (kv ? 0 : 2 * u);
+      const int key0 = CG == 2 ? (kv ? 0 : 64 * rank) : kv ? u * C::kKeysV : C::kPairK ? u * 64 : 0;
+      const int slab0 = CG == 2 ? (kv ? rank * C::kSlabsV : 0) : kv || C::kPairK ? 0 : 2 * u;
       const int np = nkeys / kPage, p0 = key0 / kPage;
       const CUtensorMap* map = kv ? &tv : &tk;
       const int none = a.pool.n_pages * a.pool.hkv * kPage;  // a row behind the pool reads as zeros
@@ -569,21 +569,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t d = tm + 256 + (blk & 1) * kBN;
 #pragma unroll
         for (int u = 0; u < C::KU; ++u) {
+          const int first = slot;
           if (!wait(ms.ready[slot], phase)) return false;
+          if (C::kPairK) {
+            step_slot();
+            if (!wait(ms.ready[slot], phase)) return false;
+          }
           tc_fence_after();
-          const uint64_t da = smem_desc(qa + (CG == 2 ? 0 : 2 * u) * 16384, 16, 1024);
-          const uint64_t db = smem_desc(ra + slot * C::kSlot, 16, C::kBoxSlabsK * 1024);
+          const uint64_t da = smem_desc(qa + (CG == 2 || C::kPairK ? 0 : 2 * u) * 16384, 16, 1024);
+          const uint64_t db = smem_desc(ra + first * C::kSlot, 16, C::kBoxSlabsK * 1024);
           if (elect_one()) {
 #pragma unroll
             for (int sl = 0; sl < C::slabs_k(u); ++sl)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 mma_ss<CG>(d, da + sl * 1024 + k * 2, db + sl * 64 + k * 2, kIdS, u + sl + k > 0);
-            mma_commit<CG>(bar(ms.empty[slot]));
-            if (u + 1 == C::KU) mma_commit<CG>(bar(ms.s_full[blk & 1]));
+            mma_commit<CG>(bar(ms.empty[first]));
+            if (C::kPairK) mma_commit<CG>(bar(ms.empty[slot]));
+            if (u + 1 == C::KU || C::kPairK) mma_commit<CG>(bar(ms.s_full[blk & 1]));
           }
           __syncwarp();
           step_slot();
+          if (C::kPairK) break;  // (both units at once)
         }
         ++blk;
         return true;
@@ -998,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_async_shared();
       __syncwarp();
       if (lane == 0) lead_arrive(ms.q_ready);
-      if (wk.left > wk.b1 - wk.b0) {  // the next tile's rows on their way to L2
+      if (wk.more()) {  // the next tile's rows on their way to L2
         const bool wrap = wk.mt + 1 == wk.n_mt;
         const int h = wk.h + wrap, R0 = (wrap ? 0 : wk.mt + 1) * M + rank * 128;
         const int left_rows = h < a.pool.hkv ? min(128, wk.v.q_len * a.G - R0) : 0;
@@ -1080,7 +1087,7 @@ cudaError_t launch_attend(AttendParams a, const CUtensorMap& tk, const CUtensorM
   cudaLaunchAttribute ja[1];
   ja[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   ja[0].val.programmaticStreamSerializationAllowed = 1;
-  jc.gridDim = dim3(a.workers, 4);
+  jc.gridDim = dim3(a.workers, kJoinSplit);
   jc.blockDim = dim3(256);
   jc.stream = stream;
   jc.attrs = ja;
