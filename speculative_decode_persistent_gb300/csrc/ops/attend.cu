@@ -25,7 +25,7 @@ mk_status check_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, int32_t h
   // (row, head) pairs, and the blocks of all tiles, are counted with 32 bits
   if (static_cast<int64_t>(rows->n_rows) * hq > 0x7fff0000ll) return MK_ERR_UNSUPPORTED;
   const double tiles = static_cast<double>(rows->n_rows) * hq / 128 + static_cast<double>(rows->n_seqs) * pool->hkv;
-  return tiles * (rows->table_stride / (kBN / kPage) + 2 + kItemCost) > 2e9 ? MK_ERR_UNSUPPORTED : MK_OK;
+  return tiles * (rows->table_stride / (kBN / kPage) + 2 + item_cost(256)) > 2e9 ? MK_ERR_UNSUPPORTED : MK_OK;
 }
 
 constexpr size_t kJoinBytes = (kMaxWorkers * sizeof(JoinInfo) + 255) / 256 * 256;
