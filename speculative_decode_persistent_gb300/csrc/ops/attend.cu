@@ -117,7 +117,7 @@ extern "C" mk_status mk_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, c
   CUtensorMap tk, tv;
   const int box = q8_box(ns, cg), slabs_k = ns, slabs_v = ns / cg;
   int device = 0;
-  if (cudaGetDevice(&device) != cudaSuccess || !encode_map(&tk, pool->k, *pool, box, 8, slabs_k) ||
+  if (cudaGetDevice(&device) != cudaSuccess || !encode_map(&tk, pool->k, *pool, box, slabs_k == 1 ? kPage : 8, slabs_k) ||
       !encode_map(&tv, pool->v, *pool, box, kPage, slabs_v))
     return MK_ERR_CUDA;
   const cudaError_t e = (q8 ? launch_attend_q8 : launch_attend_f16)(ns, cg, p, tk, tv, device, static_cast<cudaStream_t>(stream));

@@ -48,6 +48,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "ops_internal.cuh"
 #include "sm103.cuh"
@@ -491,27 +492,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n = 0;       // units issued
     bool ok = true;
     // unit u of K (kv = 0) or V of block b, whose page ids the lanes 0..7 hold
-    auto unit = [&](int kv, int u, int pg) {
-      const int nkeys = kv ? C::kKeysV : C::kKeysK, nsl = kv ? C::kSlabsV : C::slabs_k(u);
-      const int key0 = CG == 2 ? (kv ? 0 : 64 * rank) : kv ? u * C::kKeysV : C::kPairK ? u * 64 : 0;
+    auto unit = [&](auto kvc, auto uc, int pg) {
+      constexpr int kv = decltype(kvc)::value, u = decltype(uc)::value;
+      constexpr int nkeys = kv ? C::kKeysV : C::kKeysK, np = nkeys / kPage;
+      const int p0 = CG == 2 ? (kv ? 0 : 4 * rank) : (kv ? u * C::kKeysV : C::kPairK ? u * 64 : 0) / kPage;
       const int slab0 = CG == 2 ? (kv ? rank * C::kSlabsV : 0) : kv || C::kPairK ? 0 : 2 * u;
-      const int np = nkeys / kPage, p0 = key0 / kPage;
-      const CUtensorMap* map = kv ? &tv : &tk;
       const int none = a.pool.n_pages * a.pool.hkv * kPage;  // a row behind the pool reads as zeros
-      // A lane issues each copy, with the page id of the lane that holds it
-      // (75 cycles a copy; one lane for all of them: 125).
+      // the pages' rows first, then one lane's copies back to back
+      int y[np];
+#pragma unroll
+      for (int i = 0; i < np; ++i) {
+        const int page = __shfl_sync(0xffffffffu, pg, (p0 + i) & 7);
+        y[i] = wk.has_page(page) ? (page * a.pool.hkv + wk.h) * kPage : none;
+      }
       if constexpr (!Q8) {
-        // K: boxes of 8 tokens x the unit's slabs, V: of a page x the unit's slabs
+        // K: boxes of 8 tokens x the unit's slabs (of a page where that is one), V: of a page x the unit's slabs
         const int slot = n % C::kSlots;
         if (!wait(ms.empty[slot], ((n / C::kSlots) & 1) ^ 1)) return false;
         const uint32_t fb = bar(ms.full[slot]), dst = smem_u32(ring + slot * C::kSlot);
-        const int bytes = kv ? kPage * 128 * C::kSlabsV : 8 * 128 * C::kBoxSlabsK, copies = kv ? np : 2 * np;
-        if (lane == 0) bar_expect(fb, copies * bytes);
-        const int page = __shfl_sync(0xffffffffu, pg, (p0 + (kv ? lane : lane >> 1)) & 7);
+        if (elect_one()) {
+          constexpr uint32_t kPageBytes = kPage * 128 * (kv ? C::kSlabsV : C::kBoxSlabsK);
+          constexpr bool kWhole = kv || C::kBoxSlabsK == 1;  // a page's copy in one
+          bar_expect(fb, np * kPageBytes);
+#pragma unroll
+          for (int i = 0; i < np; ++i) {
+            tma_3d(dst + i * kPageBytes, kv ? &tv : &tk, 0, y[i], slab0, fb);
+            if (!kWhole) tma_3d(dst + i * kPageBytes + kPageBytes / 2, &tk, 0, y[i] + 8, slab0, fb);
+          }
+        }
         __syncwarp();
-        if (lane < copies)
-          tma_3d(dst + lane * bytes, map, 0,
-                 (!wk.has_page(page) ? none : (page * a.pool.hkv + wk.h) * kPage) + (kv ? 0 : (lane & 1) * 8), slab0, fb);
       } else {
         const int slot = n % C::kRawSlots;
         if (!wait(ms.raw_empty[slot], ((n / C::kRawSlots) & 1) ^ 1)) return false;
@@ -519,34 +528,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t mine = (gone >> p0) & ((1u << np) - 1);
         constexpr int kScaleBytes = kPage * NS * 4;
         const uint32_t fb = bar(ms.raw_full[slot]), dst = smem_u32(raw + slot * C::kRaw);
-        if (lane == 0) {
+        constexpr int nsl = kv ? C::kSlabsV : C::slabs_k(u), nbx = nsl * 64 / C::kBox;
+        if (elect_one()) {
+          const uint8_t* scales = static_cast<const uint8_t*>(kv ? a.pool.v_scale : a.pool.k_scale);
           ms.raw_pages[slot] = static_cast<int>(mine);
           bar_expect(fb, nkeys * nsl * 64 + (np - __popc(mine)) * kScaleBytes);
+#pragma unroll
+          for (int i = 0; i < np; ++i) {
+#pragma unroll
+            for (int bx = 0; bx < nbx; ++bx)
+              tma_2d(dst + (i * nbx + bx) * kPage * C::kBox, kv ? &tv : &tk, slab0 * 64 + bx * C::kBox, y[i], fb);
+            if (y[i] != none)
+              bulk_copy(dst + C::kSlot / 2 + i * kScaleBytes, scales + static_cast<int64_t>(y[i]) * (NS * 4), kScaleBytes, fb);
+          }
         }
-        const int nbx = nsl * 64 / C::kBox, i = lane / nbx;
-        const int page = __shfl_sync(0xffffffffu, pg, (p0 + i) & 7), page_s = __shfl_sync(0xffffffffu, pg, (p0 + lane) & 7);
         __syncwarp();
-        if (lane < np * nbx)
-          tma_2d(dst + lane * kPage * C::kBox, map, slab0 * 64 + (lane - i * nbx) * C::kBox,
-                 !wk.has_page(page) ? none : (page * a.pool.hkv + wk.h) * kPage, fb);
-        if (lane < np && wk.has_page(page_s))
-          bulk_copy(dst + C::kSlot / 2 + lane * kScaleBytes,
-                    static_cast<const uint8_t*>(kv ? a.pool.v_scale : a.pool.k_scale) +
-                        (static_cast<int64_t>(page_s) * a.pool.hkv + wk.h) * kScaleBytes,
-                    kScaleBytes, fb);
       }
       ++n;
       return true;
+    };
+    auto units = [&](auto kvc, int pg) {
+      bool good = unit(kvc, std::integral_constant<int, 0>(), pg);
+      if constexpr ((decltype(kvc)::value ? C::VU : C::KU) > 1) good = good && unit(kvc, std::integral_constant<int, 1>(), pg);
+      return good;
     };
     while (ok && __any_sync(0xffffffffu, wk.next())) {
       const int b0 = __shfl_sync(0xffffffffu, wk.b0, 0), b1 = __shfl_sync(0xffffffffu, wk.b1, 0);
       int pg = lane < 8 ? wk.entry(wk.t.block(b0), lane) : -1, pg_v = -1;
       for (int i = b0; ok && i <= b1; ++i) {
         const int pg_next = i + 1 < b1 && lane < 8 ? wk.entry(wk.t.block(i + 1), lane) : -1;
-        if (i < b1)
-          for (int u = 0; ok && u < C::KU; ++u) ok = unit(0, u, pg);
-        if (i > b0)
-          for (int u = 0; ok && u < C::VU; ++u) ok = unit(1, u, pg_v);
+        if (i < b1) ok = units(std::integral_constant<int, 0>(), pg);
+        if (ok && i > b0) ok = units(std::integral_constant<int, 1>(), pg_v);
         pg_v = pg;
         pg = pg_next;
       }
