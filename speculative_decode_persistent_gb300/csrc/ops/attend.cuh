@@ -210,16 +210,17 @@ struct Cfg {
   static constexpr int kMisc = 3072;
   static constexpr int kRaw = kSlot / 2 + 128 * NS * 4;  // q8 codes, then 2 NS scales per token
   static constexpr int kBudget = 232448 - kMisc - kQ;
-  // binary16 pool: all room for operand units. q8: units as stored are what is
-  // in flight from memory, so two operand units are kept and the rest is for those.
+  // binary16 pool: all room for operand units. q8: a block alone keeps two and
+  // gives the rest to units as stored, which are what is in flight from memory;
+  // a pair, bound by its products, keeps three.
   static constexpr int kFit = kBudget / kSlot;
-  static constexpr int kSlots = Q8 ? 2 : kFit > 8 ? 8 : kPairK ? kFit / 2 * 2 : kFit;
+  static constexpr int kSlots = Q8 ? CG + 1 : kFit > 8 ? 8 : kPairK ? kFit / 2 * 2 : kFit;
   static constexpr int kRawFit = (kBudget - kSlots * kSlot) / kRaw;
   static constexpr int kRawSlots = !Q8 ? 0 : kRawFit > 6 ? 6 : kRawFit;
   static constexpr int kBox = q8_box(NS, CG);
   static constexpr int kSmem = kMisc + kQ + kSlots * kSlot + kRawSlots * kRaw;
   static_assert(!kPairK || (kSlots % 2 == 0 && kSlot == kUnitK && kUnitK == kUnitV), "pairs of K units lie side by side");
-  static_assert(kSlots >= 2 && (!Q8 || kRawSlots >= 4) && kSmem <= 232448, "ring");
+  static_assert(kSlots >= 2 && (!Q8 || kRawSlots >= 3) && kSmem <= 232448, "ring");
   static_assert(!Q8 || (slabs_k(0) * 64 % kBox == 0 && kSlabsV * 64 % kBox == 0), "boxes");
 };
 
@@ -899,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (; pb < boxes; pb += kPrep) {
           const int page = (pb * inv) >> 8, dim = (pb - page * nbx) * C::kBox + cc * 16;
-          const int sl = dim / 64, ch = (dim % 64) / 8, odd = sl & 1;
+          const int sl = dim / 64, ch = (dim % 64) / 8;
           uint4 codes[kSteps];
           __half d[kSteps];
 #pragma unroll
@@ -925,11 +926,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               o[2 * j] = *reinterpret_cast<const uint32_t*>(&a2);
               o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&b2);
             }
-            // the two 16-byte pieces in an order that keeps the 128-byte rows of neighbouring slabs on other banks
+            // (the rows of neighbouring slabs share banks: exchanging the two pieces of every other lane avoids that
+            // and costs more than it saves, 74 against 70 us for 4 x 3 rows over 23K tokens)
             uint8_t* row = slab + (tok >> 3) * group + (tok & 7) * 128;
-            const uint4 v0 = make_uint4(o[0], o[1], o[2], o[3]), v1 = make_uint4(o[4], o[5], o[6], o[7]);
-            *reinterpret_cast<uint4*>(row + (((ch + odd) ^ (tok & 7)) << 4)) = odd ? v1 : v0;
-            *reinterpret_cast<uint4*>(row + (((ch + 1 - odd) ^ (tok & 7)) << 4)) = odd ? v0 : v1;
+            *reinterpret_cast<uint4*>(row + ((ch ^ (tok & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (tok & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
           }
           if (gone || partly) {  // missing pages read as zeros, unseen V values too
 #pragma unroll 1
