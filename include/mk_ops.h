@@ -75,7 +75,8 @@ typedef struct mk_dense {
 /*
  * Store rows of K and V ([n_rows][hkv][dh], both of type dtype) at their
  * positions: binary16 round to nearest even, or the q8 codec of mk.h
- * (mk_debug_q8_encode). Two rows of one call must not share a slot (a page
+ * (mk_debug_q8_encode; an infinite value makes its block's scale infinite, so
+ * the block reads as NaN; a NaN beside numbers becomes code -127). Two rows of one call must not share a slot (a page
  * that two sequences of the call both write): which of them stays is open.
  * Errors: MK_ERR_INVALID, MK_ERR_UNSUPPORTED (dh), MK_ERR_CUDA.
  */

@@ -67,7 +67,7 @@ __host__ __device__ constexpr int item_cost(int m) { return m / 32; }
 
 // A worker's first item, when it began at an earlier worker: what the join needs.
 struct JoinInfo {
-  int s, h, mt, w0, w1, slot0, rows, pad;  // w0 < 0: nothing to join here
+  int r0, h, mt, w0, w1, slot0, rows, pad;  // w0 < 0: nothing to join here; r0: the sequence's first row
 };
 
 struct AttendParams {
@@ -231,6 +231,14 @@ constexpr int kWarpCopy = 8, kWarpMma = 9, kWarpPrep = 10;
 constexpr int kPrep = 6;  // preparing warps
 constexpr int kThreads = 32 * (kWarpPrep + kPrep);
 
+// A segment as one softmax warp found it, for all eight: they meet at named
+// barriers and must agree on its blocks even if lengths change under the kernel.
+struct Segment {
+  int s, h, mt, b0, b1, more;
+  SeqView v;
+  Tile t;
+};
+
 struct Misc {
   uint64_t ready[8], full[8], empty[8], raw_full[6], raw_empty[6];
   uint64_t s_full[2], p_ready[2], pv_done, o_full, q_ready, q_free;
@@ -239,7 +247,8 @@ struct Misc {
   Start start;
   int flag[4];           // segment + 1 in which non-finite V values were cleared
   int raw_pages[6];      // bit i: page i of a raw unit is missing
-  int8_t qe[4][128];     // per row: the power of two its query was divided by
+  Segment segment[2];    // by segment parity
+  int8_t qe[3][128];     // per row, by segment modulo 3 (scores run two blocks ahead of their softmax): the power of two its query was divided by
   float swap[2][2][128];  // [block parity][half]: the halves' maxima, at the end their sums
 };
 static_assert(sizeof(Misc) <= 3072, "misc area");
@@ -313,7 +322,11 @@ __device__ void find_start(const AttendParams& a, int* scratch, Start* out, int 
   if (n <= 0) return;
   // the sequence whose part of the line holds g0, then the head, then the tile
   int at = 0, cost = 0, s = 0;
-  for (;; s += 32) {  // (g0 < total, so one of them holds it)
+  for (;; s += 32) {
+    if (s >= n_seqs) {  // (only for rows that belong to several sequences, whose sum left 32 bits)
+      if (lane == 0) out->n = 0;
+      return;
+    }
     cost = s + lane < n_seqs ? scratch[s + lane] : 0;
     const int inc = warp_scan(cost * hkv, lane);
     const uint32_t hit = __ballot_sync(0xffffffffu, g0 < at + inc);
@@ -353,7 +366,7 @@ __device__ void find_start(const AttendParams& a, int* scratch, Start* out, int 
     const int first = at + item_cost(M);  // the item's first block
     if (leader && g0 > first) {
       JoinInfo j;
-      j.s = s;
+      j.r0 = v.r0;
       j.h = h;
       j.mt = mt;
       j.w0 = first / quota;
@@ -384,7 +397,6 @@ __global__ void __launch_bounds__(256) attend_join(const AttendParams a) {
   const int share = j.rows <= cuts * static_cast<int>(gridDim.y) ? 8 : 1;  // warps a row: as many as leave no row waiting
   const int first = ((static_cast<int>(blockIdx.x) - j.w0 - 1) * gridDim.y + blockIdx.y) * (8 / share);
   if (first >= j.rows) return;
-  const SeqView v = seq_view(a.rows, j.s);
   for (int r0 = first; r0 < j.rows; r0 += cuts * gridDim.y * (8 / share)) {
     const int r = share == 1 ? r0 + warp : r0;
     if (r < j.rows) {
@@ -425,7 +437,7 @@ __global__ void __launch_bounds__(256) attend_join(const AttendParams a) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = l == 0.f ? 0.f : x[i] * inv;
-      const int R = j.mt * M + r, tok = R / a.G, row = v.r0 + tok, head = j.h * a.G + R - tok * a.G;
+      const int R = j.mt * M + r, tok = R / a.G, row = j.r0 + tok, head = j.h * a.G + R - tok * a.G;
       put_out<8>(a, row, head, lane * 8, x);
     }
     if (share == 1) __syncwarp(); else __syncthreads();
@@ -674,7 +686,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(quad) << 21;  // TMEM lane field
     int nb = 0;
     bool ok = true;
-    while (wk.next()) {
+    for (int seg = 0;; ++seg) {
+      Segment& g = ms.segment[seg & 1];
+      if (warp == 0) {
+        const bool more = wk.next();
+        if (lane == 0) g = Segment{wk.s, wk.h, wk.mt, wk.b0, wk.b1, more, wk.v, wk.t};
+      }
+      named_sync(5, 256);
+      if (!g.more) break;
+      wk.seg = seg;
+      wk.s = g.s;
+      wk.h = g.h;
+      wk.mt = g.mt;
+      wk.b0 = g.b0;
+      wk.b1 = g.b1;
+      wk.v = g.v;
+      wk.t = g.t;
       const int r = rank * 128 + wr, r_warp = rank * 128 + quad * 32;
       const bool valid = r < wk.t.rows, warp_valid = r_warp < wk.t.rows;
       const int base_p = wk.v.kv_len - wk.v.q_len, last = wk.t.rows - 1;
@@ -692,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (warp_valid) {
           if (i == wk.b0 && valid)  // scale x log2(e) x 2^e, kept normal and finite so that -inf x c is -inf
-            c = fminf(fmaxf(a.c * __uint_as_float(static_cast<uint32_t>(127 + ms.qe[wk.seg & 3][wr]) << 23), 1.2e-38f), 3e38f);
+            c = fminf(fmaxf(a.c * __uint_as_float(static_cast<uint32_t>(127 + ms.qe[wk.seg % 3][wr]) << 23), 1.2e-38f), 3e38f);
           const uint32_t sa = tm + lanes + 256 + (nb & 1) * kBN;
           uint32_t x[32], y[32];
           uint32_t sx = 0xffffffffu, sy = 0xffffffffu;
@@ -1025,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (r < rows && ch < 8 * NS)
             *reinterpret_cast<uint4*>(sq + (ch / 8) * 16384 + r * 128 + (((ch % 8) ^ (r & 7)) << 4)) =
                 make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
-          if (ch == 0 && r < rows) ms.qe[wk.seg & 3][r] = static_cast<int8_t>(e);
+          if (ch == 0 && r < rows) ms.qe[wk.seg % 3][r] = static_cast<int8_t>(e);
         }
       }
       if (!ok) break;

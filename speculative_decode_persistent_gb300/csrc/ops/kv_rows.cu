@@ -79,9 +79,9 @@ __global__ void __launch_bounds__(kBlock, 5) kv_write_kernel(const RowsArgs a) {
       if (t >= 0) store8<MK_F16, true>(static_cast<__half*>(pool) + e, x[i]);
       continue;
     }
-    float m = 0.f;
+    float m = fabsf(x[i][0]);  // (a block of NaN alone has a NaN scale)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[i][j]));
+    for (int j = 1; j < 8; ++j) m = fmaxf(m, fabsf(x[i][j]));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));  // four lanes hold a block of 32
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const float d = q8_scale(m);

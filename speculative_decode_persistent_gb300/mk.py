@@ -377,6 +377,9 @@ class Engine:
             raise MkError(-1, "seq_load (k, v [kv layers][tokens][kv heads][head dim])")
         if not 0 <= seq < self.max_seqs:
             raise MkError(-1, "seq_load (sequence)")
+        for x, view in zip((S, conv), self.state_views()):
+            if x is not None and view is not None and tuple(np.shape(x)) != tuple(view.shape[2:]):
+                raise MkError(-1, "seq_load (shape of the recurrent state)")
         used = set()
         for s in range(self.max_seqs):
             if s != seq:
@@ -413,7 +416,14 @@ class Engine:
             rows = self.seq_rows([seq], [n])
             for i in range(n_kv):
                 ops.kv_read(self.kv_pool(i), rows, out=(k[i], v[i]))
+            self._after_current()
         return k, v
+
+    def _after_current(self):
+        """Later steps come after what the current stream still reads from the pool."""
+        current = self.torch.cuda.current_stream(self.device)
+        if current != self.stream:
+            self.stream.wait_stream(current)
 
     def attend(self, layer: int, q, seqs, new_rows, window: int = 0, sinks: int = 0, gate=None, out=None):
         """Attention of the last new_rows[i] cached tokens of each seqs[i]
@@ -421,8 +431,10 @@ class Engine:
         from . import ops
         if q.dim() != 3 or q.shape[1] != self.layout.fa_hq:
             raise MkError(-1, "attend (q [rows][query heads][head dim])")
-        return ops.attend(self.kv_pool(layer), self.seq_rows(seqs, new_rows), q, window=window, sinks=sinks, gate=gate,
-                          out=out)
+        out = ops.attend(self.kv_pool(layer), self.seq_rows(seqs, new_rows), q, window=window, sinks=sinks, gate=gate,
+                         out=out)
+        self._after_current()
+        return out
 
     # ----------------------------------------------------------------- step
     @staticmethod

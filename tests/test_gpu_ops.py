@@ -491,9 +491,90 @@ def test_engine_refusals(ops):
     eng.seq_load(0, z(40), z(40))
     for status, fn in ((-2, lambda: eng.seq_load(1, z(20), z(20))), (-1, lambda: eng.seq_load(8, z(1), z(1))),
                        (-1, lambda: eng.seq_load(1, z(1)[0], z(1)[0])), (-1, lambda: eng.kv_pool(1)),
+                       (-1, lambda: eng.seq_load(1, z(1), z(1), S=np.zeros((3, 4, 64, 63), np.float32))),
                        (-1, lambda: eng.seq_rows([0], [41])), (-1, lambda: eng.attend(0, z(1)[0], [0], [1]))):
         with pytest.raises(mk.MkError) as e:
             fn()
         assert e.value.status == status
     assert eng.seq_get(0)["length"] == 40
     eng.close()
+
+
+# -------------------------------------------- many blocks and items a worker
+LONG = [([(5, 30000)], 12, 2, 256), ([(600, 9000), (1, 3000), (33, 33)], 12, 2, 128), ([(700, 20000)], 4, 1, 64),
+        ([(300, 12000), (300, 300)], 6, 2, 192), ([(2000, 2000)], 6, 1, 256), ([(1, 1500)] * 200, 8, 4, 128),
+        ([(40, 45)] * 300, 6, 3, 256)]
+
+
+@pytest.mark.parametrize("kv,dtype", [("f16", "f16"), ("q8", "f16"), ("f16", "bf16")])
+@pytest.mark.parametrize("seqs,hq,hkv,dh", LONG)
+def test_attend_long(ops, seqs, hq, hkv, dh, kv, dtype):
+    """Every worker takes many blocks, of one item and of many; run again and again the result is the same."""
+    c = Case(seqs, hq, hkv, dh, kv, dtype, seed=30, pad_rows=0)
+    out = check_attend(ops, c)
+    pool, rows = c.ops()
+    for _ in range(10):
+        assert torch.equal(ops.attend(pool, rows, c.q), out)
+
+
+@pytest.mark.parametrize("kv", ["f16", "q8"])
+def test_attend_long_window(ops, kv):
+    check_attend(ops, Case([(500, 20000), (3, 900), (1, 15000)], 12, 2, 256, kv, "bf16", seed=31), 1500, 40, gate=True)
+
+
+def test_lengths_and_tables_of_any_value(ops):
+    """Rows that run backwards, lengths and page ids out of range: nothing outside the buffers is
+    touched, the call ends, and the next one is right."""
+    c = Case([(9, 300), (70, 400), (1, 50)], 6, 2, 128, "q8", "f16", seed=32)
+    pool, rows = c.ops()
+    want = ops.attend(pool, rows, c.q)
+    n = c.n_rows
+    big = 2 ** 31 - 1
+    for start in ([0, 9, 3, 80], [50, 20, 10, 0], [-5, 1000, 9, 70], [big, 0, -big, big]):
+        for lens in ([300, -4, big], [-big, 0, 17]):
+            t = c.tables.clone()
+            t[0, ::2], t[1, 1::3] = big, -big
+            r = ops.KVRows(torch.tensor(start, dtype=torch.int32, device="cuda"), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                           t, n, 70)
+            out = torch.zeros((n + 4, 6, 128), dtype=torch.float16, device="cuda")
+            ops.attend(pool, r, c.q, out=out[2:n + 2], window=30, sinks=2)
+            k = torch.zeros((n + 4, 2, 128), dtype=torch.float16, device="cuda")
+            ops.kv_read(pool, r, out=(k[2:n + 2], k.clone()[2:n + 2]))
+            torch.cuda.synchronize()
+            assert not out[:2].any() and not out[n + 2:].any() and not k[:2].any() and not k[n + 2:].any()
+    assert torch.equal(ops.attend(pool, rows, c.q)[:c.rows_used], want[:c.rows_used])
+
+
+def test_write_q8_infinities_and_nan_as_the_step_stores_them(ops):
+    from speculative_decode_persistent_gb300 import mk
+    x = torch.randn((64, 32), device="cuda")
+    x[1, 3], x[2, 4], x[3, 5], x[4] = math.inf, -math.inf, math.nan, math.nan
+    x[5] *= 8.3e6 / float(x[5].abs().max())        # a scale near binary16's largest value
+    x[6] *= 9e6 / float(x[6].abs().max())          # and past it
+    x[7] = 1e-9
+    c = Case([(32, 32)], hkv=1, dh=64, kv="q8", dtype="f32", pad_rows=0)
+    c.new_k.copy_(x.view(32, 1, 64))
+    ops.kv_write(*c.ops(), c.new_k, c.new_k)
+    q, d = mk.q8_encode(x)
+    page = c.tables[0].long().repeat_interleave(16)[:32]
+    slot = torch.arange(32, device="cuda") % 16
+    assert torch.equal(c.pool["k"][page, 0, slot].reshape(64, 32), q)
+    assert torch.equal(bits(c.pool["k_scale"][page, 0, slot]).reshape(64), d)
+
+
+def test_first_call_inside_a_capture(tmp_path):
+    """A process whose first calls are captured, and replayed."""
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = (
+        "import sys, torch; sys.path[:0] = [%r, %r]\n" % (root, os.path.join(root, "tests")) +
+        "from ops_helpers import Case, assert_within\n"
+        "from speculative_decode_persistent_gb300 import ops\n"
+        "c = Case([(3, 700), (150, 200)], 6, 2, 128, 'q8', 'f16', seed=3)\n"
+        "pool, rows = c.ops(); g = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(g):\n"
+        "    out = ops.attend(pool, rows, c.q); k, v = ops.kv_read(pool, rows)\n"
+        "g.replay(); torch.cuda.synchronize()\n"
+        "assert_within(out[:153], *c.attend_ref()); assert torch.equal(k[:3], c.gather(0, 'k')[0][-3:].half()); print('same')\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
