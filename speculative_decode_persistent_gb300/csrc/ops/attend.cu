@@ -103,6 +103,8 @@ extern "C" mk_status mk_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, c
   p.c = std::fmin(std::fmax(a->scale * 1.44269504088896341f, 1.2e-38f), 3e38f);
   p.vq = dense_vec(a->q, a->dtype);
   p.vo = dense_vec(a->out, a->dtype);
+  if (p.vo && reinterpret_cast<uintptr_t>(a->out.data) % 32 == 0 && a->out.row_stride % 16 == 0 && a->out.head_stride % 16 == 0)
+    p.vo = 2;
   p.vg = dense_vec(a->gate, a->dtype);
   uint8_t* w = static_cast<uint8_t*>(a->work);
   p.join = reinterpret_cast<JoinInfo*>(w);

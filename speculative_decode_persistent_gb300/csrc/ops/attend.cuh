@@ -76,7 +76,7 @@ struct AttendParams {
   mk_dense q, gate, out;
   int hq, G, g_inv, dtype, window, sinks, workers;  // g_inv = 2^20 / G + 1: x / G = x g_inv >> 20 for x < 2^20 / G
   float c;         // scale x log2(e)
-  int vq, vo, vg;  // 16-byte access to q, out, gate
+  int vq, vo, vg;  // 16-byte access to q, out, gate (out: 2 with 32 bytes)
   JoinInfo* join;  // [kMaxWorkers]
   float2* ml;      // [2 workers][128 CG] reference and sum of a part
   float* part;     // [2 workers][128 CG][dh] unnormalised output
@@ -253,17 +253,17 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= 3072, "misc area");
 
-// Output of eight or more neighbouring dims: gate, rounding, store.
+// Output of eight or more neighbouring dims: gate, rounding, store. Sixteen of
+// them go out as one 32-byte sector where the alignment allows: a warp's rows
+// lie far apart, and half-filled sectors took twice as long.
 template <int N>
-__device__ __forceinline__ void put_out(const AttendParams& a, int row, int head, int d0, const float* x) {
+__device__ __forceinline__ void put_out(const AttendParams& a, int row, int head, int d0, float* x) {
   const int64_t oo = row * a.out.row_stride + head * a.out.head_stride + d0;
-  const int64_t go = row * a.gate.row_stride + head * a.gate.head_stride + d0;
+  if (a.gate.data) {
+    const int64_t go = row * a.gate.row_stride + head * a.gate.head_stride + d0;
 #pragma unroll
-  for (int i = 0; i < N; i += 8) {
-    float y[8], g[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = x[i + k];
-    if (a.gate.data) {
+    for (int i = 0; i < N; i += 8) {
+      float g[8];
       if (a.dtype == MK_F16) {
         const __half* gp = static_cast<const __half*>(a.gate.data) + go + i;
         if (a.vg) load8<MK_F16, true>(gp, g); else load8<MK_F16, false>(gp, g);
@@ -272,14 +272,27 @@ __device__ __forceinline__ void put_out(const AttendParams& a, int row, int head
         if (a.vg) load8<MK_BF16, true>(gp, g); else load8<MK_BF16, false>(gp, g);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = __fdividef(y[k], 1.f + __expf(-g[k]));
+      for (int k = 0; k < 8; ++k) x[i + k] = __fdividef(x[i + k], 1.f + __expf(-g[k]));
     }
-    if (a.dtype == MK_F16) {
-      __half* op = static_cast<__half*>(a.out.data) + oo + i;
-      if (a.vo) store8<MK_F16, true>(op, y); else store8<MK_F16, false>(op, y);
-    } else {
-      __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out.data) + oo + i;
-      if (a.vo) store8<MK_BF16, true>(op, y); else store8<MK_BF16, false>(op, y);
+  }
+  uint16_t* op = static_cast<uint16_t*>(a.out.data) + oo;
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N; i += 2) w[i / 2] = a.dtype == MK_F16 ? pack_half2(x[i], x[i + 1]) : pack_bf162(x[i], x[i + 1]);
+  if (N >= 16 && a.vo == 2) {
+#pragma unroll
+    for (int i = 0; i + 8 <= N / 2; i += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(op + 2 * i), "r"(w[i]), "r"(w[i + 1]),
+                   "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
+                   : "memory");
+  } else if (a.vo) {
+#pragma unroll
+    for (int i = 0; i < N / 2; i += 4) *reinterpret_cast<uint4*>(op + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      op[2 * i] = static_cast<uint16_t>(w[i]);
+      op[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
     }
   }
 }
@@ -852,9 +865,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (valid && !whole) {
-          float4* dst = reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(slot) * M + r) * DH + 32 * k);
+          float* dst = a.part + (static_cast<int64_t>(slot) * M + r) * DH + 32 * k;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dst[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+          for (int j = 0; j < 32; j += 8)
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + j), "f"(y[j]), "f"(y[j + 1]),
+                         "f"(y[j + 2]), "f"(y[j + 3]), "f"(y[j + 4]), "f"(y[j + 5]), "f"(y[j + 6]), "f"(y[j + 7])
+                         : "memory");
         } else if (valid) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) y[j] = !ok ? NAN : l == 0.f ? 0.f : y[j] * inv;
@@ -1033,17 +1049,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           int e = 0;
           if (a.dtype == MK_BF16) {
             // the row times a power of two that brings its largest value to [1, 2): exact, and within binary16's range
-            float x[8], mx = 0.f;
+            // (magnitudes compared as integers; a row's lanes in one reduction)
+            float x[8];
+            uint32_t top2 = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               x[2 * j] = __uint_as_float(o[t][j] << 16);
               x[2 * j + 1] = __uint_as_float(o[t][j] & 0xffff0000u);
-              mx = fmaxf(mx, fmaxf(fabsf(x[2 * j]), fabsf(x[2 * j + 1])));
+              top2 = __vmaxu2(top2, o[t][j] & 0x7fff7fffu);
             }
-#pragma unroll
-            for (int k = kLPR / 2; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-            e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-            if (e > 127 || mx == 0.f) e = 0;  // infinities stay, zero rows too
+            const uint32_t group = kLPR == 32 ? 0xffffffffu : ((1u << kLPR % 32) - 1) << (sub * kLPR);
+            const uint32_t mx = __reduce_max_sync(group, max(top2 & 0xffffu, top2 >> 16));
+            e = static_cast<int>(mx >> 7) - 127;
+            if (e > 127 || mx == 0) e = 0;  // infinities stay, zero rows too
             e = max(-100, min(100, e));
             const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
@@ -1059,6 +1077,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_async_shared();
       __syncwarp();
       if (lane == 0) lead_arrive(ms.q_ready);
+      if (a.gate.data) {  // the gate's rows on their way to L2
+        for (int k = pt; k < rows * NS; k += kPT) {
+          const RowOf at = row_of(wk.t, rank * 128 + k / NS, a.G, a.g_inv);
+          const uint16_t* line = static_cast<const uint16_t*>(a.gate.data) + (wk.v.r0 + at.tok) * a.gate.row_stride +
+                                 (wk.h * a.G + at.head) * a.gate.head_stride + k % NS * 64;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+        }
+      }
       if (wk.more()) {  // the next tile's rows on their way to L2
         const bool wrap = wk.mt + 1 == wk.n_mt;
         const int h = wk.h + wrap, R0 = (wrap ? 0 : wk.mt + 1) * M + rank * 128;
