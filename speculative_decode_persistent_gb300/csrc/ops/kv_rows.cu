@@ -115,8 +115,10 @@ __global__ void __launch_bounds__(kBlock) kv_read_kernel(const RowsArgs a) {
         const uint2 c = __ldg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(pool) + e));
         const float d = __half2float(static_cast<const __half*>(i < 2 ? a.pool.k_scale : a.pool.v_scale)[e / 32]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          x[i][j] = d * static_cast<float>(static_cast<int8_t>((j < 4 ? c.x : c.y) >> (8 * (j & 3))));
+        for (int j = 0; j < 8; ++j) {  // 2^23 + (code + 128) by a byte move: integer conversions run at a quarter of the rate
+          const uint32_t w = (j < 4 ? c.x : c.y) ^ 0x80808080u;
+          x[i][j] = d * (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 | (j & 3))) - 8388736.0f);
+        }
       }
     }
   }
