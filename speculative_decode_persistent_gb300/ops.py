@@ -206,15 +206,18 @@ def kv_read(pool: KVPool, rows: KVRows, dtype=torch.float16, out=None):
     """The rows' cached values as dense (k, v) of type dtype, or into out =
     (k, v). Rows of no sequence are left as they are (undefined when the
     tensors are made here)."""
+    hkv, dh = pool.hkv, pool.dh
     if out is None:
         if rows.n_rows is None:
             _refuse("kv_read (KVRows.n_rows or out)")
-        shape = (rows.n_rows, pool.hkv, pool.dh)
+        shape = (rows.n_rows, hkv, dh)
         k, v = torch.empty(shape, dtype=dtype, device=pool.device), torch.empty(shape, dtype=dtype, device=pool.device)
+        kd, vd = (k.data_ptr(), hkv * dh, dh), (v.data_ptr(), hkv * dh, dh)
+        n, device = _same(pool, rows, k)
     else:
         k, v = out
-    kd, vd = _dense(k, pool.hkv, pool.dh, "kv_read out", True), _dense(v, pool.hkv, pool.dh, "kv_read out", True)
-    n, device = _same(pool, rows, k, v)
+        kd, vd = _dense(k, hkv, dh, "kv_read out", True), _dense(v, hkv, dh, "kv_read out", True)
+        n, device = _same(pool, rows, k, v)
     _run(device, "mk_kv_read", _kv_read, pool.c, rows._at(n), _DENSE(*kd), _DENSE(*vd), DTYPES[k.dtype])
     return k, v
 
@@ -231,16 +234,18 @@ def attend(pool: KVPool, rows: KVRows, q, scale=None, window: int = 0, sinks: in
     is multiplied by sigmoid(gate). A row that sees no token gives 0. Returns
     out, like q (made here unless given; it may be q or gate itself; rows of
     no sequence are left as they are, undefined when it is made here)."""
+    shape, dtype, dh = q.shape, q.dtype, pool.dh
+    hq = shape[1] if len(shape) == 3 else 0
+    qd = _dense(q, hq, dh, "attend q")
+    gd = (0, 0, 0) if gate is None else _dense(gate, hq, dh, "attend gate")
+    more = () if gate is None else (gate,)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    hq, dh = q.shape[1] if q.dim() == 3 else 0, pool.dh
-    qd, od = _dense(q, hq, dh, "attend q"), _dense(out, hq, dh, "attend out", True)
-    if gate is None:
-        gd = (0, 0, 0)
-        n, device = _same(pool, rows, q, out)
+        n, device = _same(pool, rows, q, *more)
+        out = torch.empty(shape, dtype=dtype, device=pool.device)
+        od = (out.data_ptr(), hq * dh, dh)
     else:
-        gd = _dense(gate, hq, dh, "attend gate")
-        n, device = _same(pool, rows, q, out, gate)
+        od = _dense(out, hq, dh, "attend out", True)
+        n, device = _same(pool, rows, q, out, *more)
     scale = 1.0 / math.sqrt(dh) if scale is None else float(scale)
     if not (0.0 < scale < 3.4e38 and 0 <= window < 2 ** 31 and 0 <= sinks < 2 ** 31):
         _refuse("attend (a finite positive scale, a window and sinks of at least 0)")
@@ -253,7 +258,7 @@ def attend(pool: KVPool, rows: KVRows, q, scale=None, window: int = 0, sinks: in
             _work_bytes[dh] = nbytes
     # from torch's allocator, so calls on other streams and captured graphs have their own
     work = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=pool.device)
-    args = _ARGS(*qd, *gd, *od, hq, DTYPES[q.dtype], scale, window, sinks, work.data_ptr(),
+    args = _ARGS(*qd, *gd, *od, hq, DTYPES[dtype], scale, window, sinks, work.data_ptr(),
                  work.numel())
     _run(device, "mk_attend", _attend, pool.c, at, args)
     return out
