@@ -77,7 +77,7 @@ typedef struct mk_dense {
  * positions: binary16 round to nearest even, or the q8 codec of mk.h
  * (mk_debug_q8_encode; an infinite value makes its block's scale infinite, so
  * the block reads as NaN; a NaN beside numbers becomes code -127). Two rows of one call must not share a slot (a page
- * that two sequences of the call both write): which of them stays is open.
+ * that two sequences of the call both write): what it then holds is open.
  * Errors: MK_ERR_INVALID, MK_ERR_UNSUPPORTED (dh), MK_ERR_CUDA.
  */
 mk_status mk_kv_write(const mk_kv_pool* pool, const mk_kv_rows* rows, const mk_dense* k, const mk_dense* v,

@@ -320,13 +320,30 @@ template <int M>
 __device__ void find_start(const AttendParams& a, int* scratch, Start* out, int worker, bool leader) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, nw = blockDim.x / 32;
   const int n_seqs = a.rows.n_seqs, hkv = a.pool.hkv;
-  for (int s = warp; s < n_seqs; s += nw) {
+  // a thread adds up a sequence of few tiles (hundreds of decoding sequences
+  // at once), a warp one of many
+  constexpr int kFew = 4;
+  bool many = false;
+  for (int s = threadIdx.x; s < n_seqs; s += blockDim.x) {
     const SeqView v = seq_view(a.rows, s);
     const int n = tiles_of(v, a.G, M);
-    int sum = 0;
-    for (int mt = lane; mt < n; mt += 32) sum += make_tile(v, a.G, M, mt, a.window, a.sinks).nblk + item_cost(M);
-    sum = warp_sum(sum);
-    if (lane == 0) scratch[s] = sum;
+    int sum = n <= kFew ? 0 : -1;
+    for (int mt = 0; mt < min(n, kFew) && sum >= 0; ++mt)
+      sum += make_tile(v, a.G, M, mt, a.window, a.sinks).nblk + item_cost(M);
+    scratch[s] = sum;
+    many |= sum < 0;
+  }
+  if (__syncthreads_or(many)) {
+    for (int s = warp; s < n_seqs; s += nw) {
+      if (scratch[s] >= 0) continue;
+      const SeqView v = seq_view(a.rows, s);
+      const int n = tiles_of(v, a.G, M);
+      int sum = 0;
+      for (int mt = lane; mt < n; mt += 32) sum += make_tile(v, a.G, M, mt, a.window, a.sinks).nblk + item_cost(M);
+      sum = warp_sum(sum);
+      __syncwarp();
+      if (lane == 0) scratch[s] = sum;
+    }
   }
   __syncthreads();
   if (warp != 0) return;

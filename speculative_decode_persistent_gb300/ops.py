@@ -120,8 +120,8 @@ class KVRows:
     kv_len[s] tokens, whose positions 16i .. 16i+15 lie on page tables[s][i]
     (-1: no page). They are read when the work runs. n_rows: rows of the
     dense tensors (default: the tensor's of the call, needed for a kv_read
-    that makes its outputs). max_q: the most new rows of one sequence (default
-    n_rows), a hint for the choice of a kernel."""
+    that makes its outputs). max_q: the most new rows of one sequence (default:
+    their mean), a hint for the choice of a kernel."""
 
     __slots__ = ("tensors", "device", "n_seqs", "n_rows", "max_q", "_head", "_stride")
 
@@ -145,7 +145,8 @@ class KVRows:
 
     def _at(self, n_rows: int):
         """The C view for dense tensors of n_rows rows."""
-        return _ROWS(*self._head, n_rows, self._stride, n_rows if self.max_q is None else min(self.max_q, n_rows))
+        mean = -(-n_rows // max(self.n_seqs, 1))
+        return _ROWS(*self._head, n_rows, self._stride, mean if self.max_q is None else min(self.max_q, n_rows))
 
 
 def _dense(t, heads: int, dh: int, what: str, out=False):

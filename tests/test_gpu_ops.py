@@ -578,3 +578,38 @@ def test_first_call_inside_a_capture(tmp_path):
         "assert_within(out[:153], *c.attend_ref()); assert torch.equal(k[:3], c.gather(0, 'k')[0][-3:].half()); print('same')\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("kv", ["f16", "q8"])
+def test_sequences_that_share_pages(ops, kv):
+    """A common prefix on the same pages, and one sequence twice."""
+    c = Case([(4, 200), (150, 330), (1, 96)], 6, 2, 256, kv, "f16", seed=33)
+    c.tables[0, :6], c.tables[2, :6] = c.tables[1, :6], c.tables[1, :6]
+    out = check_attend(ops, c)
+    pool, rows = c.ops()
+    twice = ops.KVRows(torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda"), c.kv_len[:1].repeat(2), c.tables[:1].repeat(2, 1), 8)
+    got = ops.attend(pool, twice, c.q[:4].repeat(2, 1, 1))
+    assert torch.equal(got[:4], got[4:])
+    assert float((got[:4].double() - out[:4].double()).abs().max()) < 2e-3  # (cut elsewhere)
+    k, v = ops.kv_read(pool, rows, torch.float32)
+    for i, (n, T) in enumerate(c.seqs):
+        r = int(c.start[i])
+        assert torch.equal(k[r:r + n], c.gather(i, "k")[0][T - n:].float())
+
+
+def test_engine_loads_nothing_and_goes_on(ops):
+    """An empty context is an empty sequence: the same tokens as after seq_new."""
+    from gen import configs
+    from gen.synth import make_weights
+    from speculative_decode_persistent_gb300 import mk
+    eng = mk.Engine(configs.TINY, make_weights(configs.TINY, 0), 0, 16)
+    z = torch.zeros((1, 0, 1, 64), device="cuda", dtype=torch.float16)
+    eng.seq_load(0, z, z)
+    eng.seq_new(1)
+    got = [list(eng.step([5, 6, 7], [0, 1, 2], [s] * 3, [1, 1, 2])[0]) for s in (0, 1)]
+    assert got[0] == got[1] and eng.seq_get(0)["length"] == 3
+    k, v = eng.seq_kv(0)
+    k1, v1 = eng.seq_kv(1)
+    # (split sums are added in any order: a rounding apart)
+    assert torch.allclose(k.float(), k1.float(), atol=1e-3) and torch.allclose(v.float(), v1.float(), atol=1e-3)
+    eng.close()
