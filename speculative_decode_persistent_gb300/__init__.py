@@ -1,7 +1,8 @@
 """GB300-native fused speculative-decode verify step (sm_103a).
 
 The CUDA library libmk.so (C ABI in include/mk.h) runs the whole verify cycle
-in one persistent cooperative kernel; `mk` is its ctypes binding.
+in one persistent cooperative kernel; `mk` is its ctypes binding. `ops` has the
+operators on the paged KV cache outside the step (include/mk_ops.h).
 """
 from . import build  # noqa: F401
 

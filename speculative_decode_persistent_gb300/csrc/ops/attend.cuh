@@ -213,7 +213,7 @@ struct Cfg {
   static constexpr int kUnitK = kKeysK * kBoxSlabsK * 128, kUnitV = kKeysV * kSlabsV * 128;
   static constexpr int kSlot = kUnitK > kUnitV ? kUnitK : kUnitV;
   static constexpr int kQ = NS * 16384;
-  static constexpr int kMisc = 3072;
+  static constexpr int kMisc = 3040;
   static constexpr int kRaw = kSlot / 2 + 128 * NS * 4;  // q8 codes, then 2 NS scales per token
   static constexpr int kBudget = 232448 - kMisc - kQ;
   // binary16 pool: all room for operand units. q8: a block alone keeps two and
@@ -257,7 +257,7 @@ struct Misc {
   int8_t qe[3][128];     // per row, by segment modulo 3 (scores run two blocks ahead of their softmax): the power of two its query was divided by
   float swap[2][2][128];  // [block parity][half]: the halves' maxima, at the end their sums
 };
-static_assert(sizeof(Misc) <= 3072, "misc area");
+static_assert(sizeof(Misc) <= 3040, "misc area");
 
 // Output of eight or more neighbouring dims: gate, rounding, store. Sixteen of
 // them go out as one 32-byte sector where the alignment allows: a warp's rows
