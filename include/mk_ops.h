@@ -106,8 +106,9 @@ mk_status mk_kv_read(const mk_kv_pool* pool, const mk_kv_rows* rows, const mk_de
  * be q or gate itself; it must not overlap them otherwise.
  * A wait inside the kernel that gives up after two seconds (which takes a
  * fault elsewhere, or lengths that change while it runs) makes the rows it was
- * for NaN; the call's status was returned before. An infinite V value that a
- * row sees with a weight below 2^-24 of its largest gives NaN.
+ * for NaN; the call's status was returned before. A weight below 2^-36 of the
+ * row's largest counts in the sum but adds nothing (an infinite V value that is
+ * seen with one gives NaN); from 2^-25 on it has all of binary16's bits.
  * work: mk_attend_work_bytes() bytes, 256-byte aligned, contents free; calls that may
  * overlap on the GPU need a buffer each (two captured graphs too).
  * Errors: MK_ERR_INVALID (also: scale not finite and positive, negative
