@@ -1078,7 +1078,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (r0 >= rows) break;  // whole warps
           int e = 0;
           if (a.dtype == MK_BF16) {
-            // the row times a power of two that brings its largest value to [1, 2): exact, and within binary16's range
+            // the row times a power of two that brings its largest value to [2^14, 2^15): exact for what is at least
+            // 2^-31 of it, to 2^-25 for the rest (2^-39 of the largest); infinite and NaN values stay
             // (magnitudes compared as integers; a row's lanes in one reduction)
             float x[8];
             uint32_t top2 = 0;
@@ -1090,9 +1091,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const uint32_t group = kLPR == 32 ? 0xffffffffu : ((1u << kLPR % 32) - 1) << (sub * kLPR);
             const uint32_t mx = __reduce_max_sync(group, max(top2 & 0xffffu, top2 >> 16));
-            e = static_cast<int>(mx >> 7) - 127;
-            if (e > 127 || mx == 0) e = 0;  // infinities stay, zero rows too
-            e = max(-100, min(100, e));
+            e = max(static_cast<int>(mx >> 7) - (127 + 14), -126);  // at most 114; 2^e and 2^-e are normal
             const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[t][j] = pack_half2(x[2 * j] * f, x[2 * j + 1] * f);

@@ -1,5 +1,6 @@
 """Attention over values at the ends of the types' ranges, against the 64-bit reference of
-tests/ops_helpers.py: weights far below a row's largest."""
+tests/ops_helpers.py: weights far below a row's largest; bf16
+queries of every magnitude the type has."""
 import math
 import os
 import sys
@@ -19,6 +20,11 @@ def ops(request):
         pytest.skip("no CUDA device")
     from speculative_decode_persistent_gb300 import ops as o
     return o
+
+
+def attend(ops, c, **kw):
+    pool, rows = c.ops()
+    return ops.attend(pool, rows, c.q, **kw)[:c.rows_used]
 
 
 # ------------------------------------------------- weights far below the largest
@@ -72,3 +78,53 @@ def test_a_dominant_token_without_a_value(ops, n, hq, dh, at, copies, gap, dtype
         step = torch.finfo(c.dtype).eps / 2
         bound = err + (want.abs() + err) * step + (2.0 ** -25 if dtype == "f16" else 0.0)
         assert_within(got[:, i], want.expand(copies, hq, dh), bound.expand(copies, hq, dh))
+
+
+# ------------------------------------------------------------- bf16 queries
+@pytest.mark.parametrize("e", [-126, -120, -105, 90, 116, 122])
+@pytest.mark.parametrize("n,dh,hq,hkv", [(9, 128, 4, 2), (1, 64, 2, 1), (60, 256, 6, 1)])
+def test_bf16_queries_to_the_ends_of_the_type(ops, n, dh, hq, hkv, e):
+    """Queries about 2^e; the score scale undoes it, so the scores are of ordinary size."""
+    c = Case([(n, 200)], hq, hkv, dh, "f16", "bf16", seed=47)
+    c.q.copy_((c.q.double() * 2.0 ** e).to(torch.bfloat16))
+    assert bool(torch.isfinite(c.q).all())
+    s = 2.0 ** -e / math.sqrt(dh)
+    assert_within(attend(ops, c, scale=s), *c.attend_ref(scale=s))
+
+
+@pytest.mark.parametrize("kv", ["f16", "q8"])
+@pytest.mark.parametrize("small", [2.0 ** -12, 2.0 ** -16, 2.0 ** -18, 2.0 ** -20, 2.0 ** -22])
+@pytest.mark.parametrize("n,dh,hq", [(1, 128, 2), (80, 256, 6), (5, 64, 4)])
+def test_bf16_queries_of_wide_spread(ops, n, dh, hq, small, kv):
+    """One dim of a query is far larger than the others, where K is large: all of them count in the scores."""
+    c = Case([(n, 300)], hq, 1, dh, kv, "bf16", seed=48)
+    big = 4.0 * 2.0 ** -12 / small
+    c.q[..., 1:] = (c.q[..., 1:].float() * small).to(torch.bfloat16)
+    if kv == "f16":
+        c.pool["k"][..., 1:] *= big
+        c.pool["k"][..., 0] *= 2.0 ** -10
+        c.value["k"] = c.pool["k"].double()
+    else:  # a power of two on every scale but the first block's
+        c.pool["k_scale"][..., 1:] *= big
+        c.pool["k"][..., 0] = 1
+        c.value["k"] = (c.pool["k"].double().unflatten(-1, (-1, 32)) * c.pool["k_scale"].double()[..., None]).flatten(-2)
+    s = 2.0 ** 9 / math.sqrt(dh)
+    assert_within(attend(ops, c, scale=s), *c.attend_ref(scale=s))
+
+
+def test_bf16_queries_with_infinities(ops):
+    """An infinite query makes the scores infinite by the signs of K: of tokens with -inf scores alone the
+    row gives 0; any +inf gives NaN."""
+    c = Case([(4, 40)], 2, 1, 64, "f16", "bf16", seed=49)
+    c.pool["k"][..., 0] = -c.pool["k"][..., 0].abs() - 1
+    c.value["k"] = c.pool["k"].double()
+    c.q[1, 0, 0] = math.inf
+    c.q[1, 0, 1:] = 2.0 ** 100  # far past binary16: the row's infinity must stay its only one
+    c.q[2, 1, 0] = -math.inf
+    c.q[3, 0, 5] = math.nan
+    got = attend(ops, c)
+    assert not got[1, 0].any()
+    assert bool(torch.isnan(got[2, 1]).all()) and bool(torch.isnan(got[3, 0]).all())
+    want, bound = c.attend_ref()
+    for i, h in ((0, 0), (0, 1), (1, 1), (2, 0), (3, 1)):
+        assert_within(got[i, h], want[i, h], bound[i, h])
