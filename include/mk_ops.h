@@ -102,7 +102,11 @@ mk_status mk_kv_read(const mk_kv_pool* pool, const mk_kv_rows* rows, const mk_de
  * no effect. Rounding: scores, softmax statistics and sums are fp32; the
  * products' operands are binary16 (bf16 queries are scaled by a power of two
  * per row, exact but for elements below 2^-31 of the row's largest, which are
- * rounded to 2^-39 of it; q8 values and the probabilities are rounded).
+ * rounded to 2^-39 of it; q8 values and the probabilities are rounded). A q8
+ * token with a scale of 512 or more, whose values may pass binary16's largest,
+ * enters as 2^-8 of itself: its small values are rounded to 2^-17, the limits of
+ * small weights below are 2^8 coarser beside it, and the blocks that meet one
+ * take their work twice.
  * q, gate, out: [n_rows][hq][dh] of type dtype (MK_F16 or MK_BF16). out may
  * be q or gate itself; it must not overlap them otherwise.
  * A wait inside the kernel that gives up after two seconds (which takes a

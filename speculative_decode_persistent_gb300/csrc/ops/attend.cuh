@@ -45,6 +45,16 @@
 // in shared memory before the product, and rows that do see one add it when
 // they write their result (a rare path). Missing pages arrive as zeros.
 //
+// Large q8 values. A q8 block holds up to 127 x 65504, its operands are binary16.
+// The softmax warps note the first segment with a scale of 512 or more; from it
+// on a worker writes no result, and takes its segments again with code that lets
+// the values of such tokens enter the products as 2^-8 of themselves. There the
+// preparing and the softmax warps find the tokens by their scales, each for itself:
+// the factor of a K token goes into its scores, that of a V token into its weight's
+// exponent (also in the running maximum, so that the weight stays a binary16
+// number) and out of the sum of the weights. (That code in the only pass: 69 -> 83 us
+// for 4 x 3 rows, 202 -> 252 us for 512 rows over 20K tokens.)
+//
 // Bound and measured (24 query heads, 4 kv heads of 256). Many rows: the
 // products; 2,048 rows over 20,512 fp16 tokens in 565 us, 1,736 TFLOP/s, over
 // q8 tokens in 687 us, where converting the codes takes as long. Few rows: the
@@ -57,6 +67,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <climits>
 #include <type_traits>
 
 #include "ops_internal.cuh"
@@ -146,6 +157,35 @@ __device__ __forceinline__ uint32_t seen_bits(int p, int base, int window, int s
   uint32_t m = low_bits(p - base + 1);
   if (window > 0) m &= ~low_bits(p - window + 1 - base) | low_bits(sinks - base);
   return m;
+}
+
+// A q8 token is large when one of its 2 NS scales is 512 or more (infinite and NaN ones too): 128 times it, the
+// largest code, is not a binary16 number. Scales are compared as integers, two at a time, so a sign counts as large.
+template <int NS>
+__device__ __forceinline__ void token_scales(const uint8_t* scales, uint32_t (&w)[NS]) {
+  if constexpr (NS == 4) {
+    const uint4 x = *reinterpret_cast<const uint4*>(scales);
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+  } else if constexpr (NS == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(scales);
+    w[0] = x.x; w[1] = x.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) w[i] = reinterpret_cast<const uint32_t*>(scales)[i];
+  }
+}
+template <int N>
+__device__ __forceinline__ bool any_large(const uint32_t (&w)[N]) {
+  uint32_t top = w[0];
+#pragma unroll
+  for (int i = 1; i < N; i += 2) top = __vimax3_u16x2(top, w[i], w[i + 1 < N ? i + 1 : i]);
+  return max(top >> 16, top & 0xffffu) >= 0x6000u;
+}
+template <int NS>
+__device__ __forceinline__ bool large_token(const uint8_t* scales) {
+  uint32_t w[NS];
+  token_scales<NS>(scales, w);
+  return any_large(w);
 }
 
 // Column of S's 128 in which P of token t (even) lies: each half over its own scores.
@@ -258,6 +298,8 @@ struct Misc {
   uint32_t tmem;
   int dead;
   Start start;
+  int large;             // first segment with large q8 values, INT_MAX: none; the same in both blocks of a pair
+  int taken, units, blocks;  // segments, units and blocks of the first pass
   int flag[4];           // segment + 1 in which non-finite V values were cleared
   int raw_pages[6];      // bit i: page i of a raw unit is missing
   Segment segment[2];    // by segment parity
@@ -487,13 +529,12 @@ __global__ void __launch_bounds__(256) attend_join(const AttendParams a) {
   }
 }
 
-template <int NS, bool Q8, int CG>
-__global__ void __launch_bounds__(kThreads, 1)
-    attend_kernel(const __grid_constant__ AttendParams a, const __grid_constant__ CUtensorMap tk,
-                  const __grid_constant__ CUtensorMap tv) {
+// The worker's segments, every warp its part. LARGE: once more, from segment `first` on, with large q8 values.
+template <int NS, bool Q8, int CG, bool LARGE>
+__device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtensorMap& tk, const CUtensorMap& tv, uint8_t* smem,
+                                            uint32_t tm) {
   using C = Cfg<NS, Q8, CG>;
   constexpr int M = C::M, DH = C::DH;
-  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const sq = smem;                          // Q [NS][128 rows][128 B], swizzled
   uint8_t* const ring = sq + C::kQ;                  // operand units
   uint8_t* const raw = ring + C::kSlots * C::kSlot;  // q8 units as stored
@@ -510,43 +551,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (CG == 1) bar_arrive(smem_u32(&b)); else bar_arrive_cluster(peer_addr(smem_u32(&b), 0));
   };
 
-  if (tid == 0) {
-    for (int i = 0; i < C::kSlots; ++i) {
-      bar_init(bar(ms.full[i]), 1);
-      bar_init(bar(ms.ready[i]), CG * kPrep);
-      bar_init(bar(ms.empty[i]), 1);
-    }
-    for (int i = 0; i < C::kRawSlots; ++i) {
-      bar_init(bar(ms.raw_full[i]), 1);
-      bar_init(bar(ms.raw_empty[i]), kPrep);
-    }
-    for (int i = 0; i < 2; ++i) {
-      bar_init(bar(ms.s_full[i]), 1);
-      bar_init(bar(ms.p_ready[i]), 8 * CG);
-    }
-    bar_init(bar(ms.pv_done), 1);
-    bar_init(bar(ms.o_full), 1);
-    bar_init(bar(ms.q_ready), CG * kPrep);
-    bar_init(bar(ms.q_free), 1);
-    ms.dead = (smem_u32(smem) & 1023u) != 0;  // (the swizzled tiles need the alignment)
-    for (int i = 0; i < 4; ++i) ms.flag[i] = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  if (warp == kWarpMma) tmem_alloc<CG>(smem_u32(&ms.tmem), 512);
-  find_start<M>(a, reinterpret_cast<int*>(ring), &ms.start, worker, rank == 0);
-  tc_fence_before();
-  fence_async_shared();  // the scratch lay where tensor copies go
-  __syncthreads();
-  if (CG == 2) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  tc_fence_after();
-  const uint32_t tm = ms.tmem;
-  asm volatile("griddepcontrol.launch_dependents;");
   Walk wk(a, ms.start, M);
+  // barriers and buffers go by the number of segments taken so far: seg + shift
+  const int first = LARGE ? ms.large : 0, shift = LARGE ? ms.taken - first : 0;
+  const int units0 = LARGE ? ms.units : 0, blocks0 = LARGE ? ms.blocks : 0;
+  const bool ok0 = !LARGE || !*dead;  // (after a wait that gave up: NaN for the rows that are left)
+  auto take = [&] {
+    if constexpr (LARGE) {
+      while (wk.seg + 1 < first)
+        if (!wk.next()) return false;
+    }
+    return wk.next();
+  };
 
   if (warp == kWarpCopy) {
     // ------------------------------------------------------------ page copies
-    int n = 0;       // units issued
-    bool ok = true;
+    int n = units0;  // units issued
+    bool ok = ok0;
     // unit u of K (kv = 0) or V of block b, whose page ids the lanes 0..7 hold
     auto unit = [&](auto kvc, auto uc, int pg) {
       constexpr int kv = decltype(kvc)::value, u = decltype(uc)::value;
@@ -608,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr ((decltype(kvc)::value ? C::VU : C::KU) > 1) good = good && unit(kvc, std::integral_constant<int, 1>(), pg);
       return good;
     };
-    while (ok && __any_sync(0xffffffffu, wk.next())) {
+    while (ok && __any_sync(0xffffffffu, take())) {
       const int b0 = __shfl_sync(0xffffffffu, wk.b0, 0), b1 = __shfl_sync(0xffffffffu, wk.b1, 0);
       int pg = lane < 8 ? wk.entry(wk.t.block(b0), lane) : -1, pg_v = -1;
       for (int i = b0; ok && i <= b1; ++i) {
@@ -639,8 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0) {
       constexpr uint32_t kIdS = instr_desc(M, kBN, 0), kIdO = instr_desc(M, DH, 1);
       const uint32_t qa = smem_u32(sq), ra = smem_u32(ring);
-      int slot = 0, phase = 0, blk = 0;  // ring position, block whose scores come next
-      bool ok = true;
+      int slot = units0 % C::kSlots, phase = (units0 / C::kSlots) & 1, blk = blocks0;  // ring position, block whose scores come next
+      bool ok = ok0;
       auto step_slot = [&] {
         if (++slot == C::kSlots) {
           slot = 0;
@@ -677,9 +698,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++blk;
         return true;
       };
-      while (ok && __any_sync(0xffffffffu, wk.next())) {
+      while (ok && __any_sync(0xffffffffu, take())) {
         const int count = __shfl_sync(0xffffffffu, wk.b1 - wk.b0, 0);
-        ok = wait(ms.q_ready, wk.seg & 1);
+        ok = wait(ms.q_ready, (wk.seg + shift) & 1);
         if (!ok) break;
         tc_fence_after();
         for (int i = 0; i <= count; ++i) {
@@ -727,12 +748,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp >> 2, quad = warp & 3;
     const int wr = quad * 32 + lane;  // row of this block's half of the tile
     const uint32_t lanes = static_cast<uint32_t>(quad) << 21;  // TMEM lane field
-    int nb = 0;
-    bool ok = true;
-    for (int seg = 0;; ++seg) {
-      Segment& g = ms.segment[seg & 1];
+    int nb = blocks0, seg = first;
+    bool ok = ok0;
+    // First pass over a q8 pool: a warp fetches the scales of K or V of 32 of a block's tokens, a lane a token's, and
+    // looks at them a block later. (Elsewhere it costs 5-20 % of the time: the copying warp and the preparing ones
+    // set the pace over a q8 pool.)
+    // First pass over a q8 pool: a warp looks at the scales of K or V of 32 of a block's tokens, a lane at a token's, which
+    // are on their way while it waits for the block's scores. (1-5 % of the time; 5-25 % with the copying or the
+    // preparing warps, which set the pace over a q8 pool.)
+    [[maybe_unused]] uint32_t scales[NS];
+    [[maybe_unused]] auto fetch = [&](int b, int pages) {
+      const int kv = quad & 1, k = quad >> 1, page = __shfl_sync(0xffffffffu, pages, 2 * k + lane / kPage);
+#pragma unroll
+      for (int w = 0; w < NS; ++w) scales[w] = 0;
+      if (wk.has_page(page) && b * kBN + 64 * half + 32 * k + lane < wk.v.kv_len) {  // (below 2^31: check_pool)
+        const int row = (page * a.pool.hkv + wk.h) * kPage + lane % kPage;
+        token_scales<NS>(static_cast<const uint8_t*>(kv ? a.pool.v_scale : a.pool.k_scale) + static_cast<int64_t>(row) * (NS * 4), scales);
+      }
+    };
+    [[maybe_unused]] auto look = [&] {
+      if (any_large(scales)) atomicMin(&ms.large, wk.seg);
+    };
+    for (;; ++seg) {
+      Segment& g = ms.segment[(seg + shift) & 1];
       if (warp == 0) {
-        const bool more = wk.next();
+        const bool more = take();
         if (lane == 0) g = Segment{wk.s, wk.h, wk.mt, wk.b0, wk.b1, more, wk.v, wk.t};
       }
       named_sync(5, 256);
@@ -757,12 +797,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = wk.b0; i < wk.b1; ++i, ++nb) {
         const int b = wk.t.block(i);
         const uint32_t gone = __ballot_sync(0xffffffffu, !wk.has_page(pages)) & 0xfu;
+        // the lane's tokens of the half (lane, lane + 32) that are large: bits 0, 1 for K, 2, 3 for V
+        [[maybe_unused]] uint32_t large = 0;
+        if constexpr (LARGE) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int page = __shfl_sync(0xffffffffu, pages, 2 * k + lane / kPage);
+            if (!wk.has_page(page)) continue;
+            const int64_t at = static_cast<int64_t>((page * a.pool.hkv + wk.h) * kPage + lane % kPage) * (NS * 4);
+            large |= (large_token<NS>(static_cast<const uint8_t*>(a.pool.k_scale) + at) ? 1u : 0u) << k |
+                     (large_token<NS>(static_cast<const uint8_t*>(a.pool.v_scale) + at) ? 4u : 0u) << k;
+          }
+        }
+        [[maybe_unused]] auto large_bits = [&](int kv, int k) { return __ballot_sync(0xffffffffu, large >> (2 * kv + k) & 1); };
+        if constexpr (Q8 && !LARGE) fetch(b, pages);
         if (i + 1 < wk.b1 && lane < 4) pages = wk.entry(wk.t.block(i + 1), 4 * half + lane);
         ok &= wait(ms.s_full[nb & 1], (nb >> 1) & 1);
+        if constexpr (Q8 && !LARGE) look();
         tc_fence_after();
         if (warp_valid) {
           if (i == wk.b0 && valid)  // scale x log2(e) x 2^e, kept normal and finite so that -inf x c is -inf
-            c = fminf(fmaxf(a.c * __uint_as_float(static_cast<uint32_t>(127 + ms.qe[wk.seg % 3][wr]) << 23), 1.2e-38f), 3e38f);
+            c = fminf(fmaxf(a.c * __uint_as_float(static_cast<uint32_t>(127 + ms.qe[(wk.seg + shift) % 3][wr]) << 23), 1.2e-38f), 3e38f);
           const uint32_t sa = tm + lanes + 256 + (nb & 1) * kBN;
           uint32_t x[32], y[32];
           uint32_t sx = 0xffffffffu, sy = 0xffffffffu;
@@ -790,13 +845,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(sa + 64 * half + 32, y);
           tmem_wait_ld(x);
           tmem_wait_ld(y);
+          const float cb = LARGE ? 1.f : c;  // the scores times cb are the exponents
+          if constexpr (LARGE) {
+            auto exponents = [&](uint32_t (&v)[32], uint32_t k_large, uint32_t v_large) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                v[j] = __float_as_uint(fmaf(__uint_as_float(v[j]) * c, k_large >> j & 1 ? 256.f : 1.f, v_large >> j & 1 ? 8.f : 0.f));
+            };
+            exponents(x, large_bits(0, 0), large_bits(1, 0));
+            exponents(y, large_bits(0, 1), large_bits(1, 1));
+          }
           if (part) {
             hide(x, sx);
             hide(y, sy);
           }
           top(x);
           top(y);
-          float my = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;  // c > 0
+          float my = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cb;  // cb > 0
           ms.swap[nb & 1][half][wr] = my;
           named_sync(1 + quad, 64);
           my = fmaxf(my, ms.swap[nb & 1][half ^ 1][wr]);
@@ -820,10 +885,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float mm = (m == -INFINITY ? 0.f : m) - kLift;
-          const uint64_t c2 = pack2(c, c), m2 = pack2(-mm, -mm);
+          const uint64_t c2 = pack2(cb, cb), m2 = pack2(-mm, -mm);
           uint64_t l2 = pack2(0.f, 0.f), l3 = l2;
           // P of the half lies over its own scores, which are in registers
-          auto weigh = [&](const uint32_t (&v)[32], uint64_t& sum, uint32_t dst) {
+          auto weigh = [&](const uint32_t (&v)[32], uint64_t& sum, uint32_t dst, [[maybe_unused]] uint32_t v_large) {
             uint32_t h[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
@@ -831,13 +896,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               unpack2(fma2(pack2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), c2, m2), e0, e1);
               e0 = ex2(e0);
               e1 = ex2(e1);
-              sum = add2(sum, pack2(e0, e1));
               h[j] = pack_half2(e0, e1);
+              if constexpr (LARGE) {
+                if (v_large >> (2 * j) & 1) e0 *= 0.00390625f;
+                if (v_large >> (2 * j + 1) & 1) e1 *= 0.00390625f;
+              }
+              sum = add2(sum, pack2(e0, e1));
             }
             tmem_st16(dst, h);
           };
-          weigh(x, l2, sa + 64 * half);
-          weigh(y, l3, sa + 64 * half + 16);
+          weigh(x, l2, sa + 64 * half, LARGE ? large_bits(1, 0) : 0);
+          weigh(y, l3, sa + 64 * half + 16, LARGE ? large_bits(1, 1) : 0);
           float a0, a1;
           unpack2(add2(l2, l3), a0, a1);
           l += a0 + a1;
@@ -850,17 +919,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the result of the segment: O, once its last product is done. (Not by
       // pv_done: a wait tells only two neighbouring phases apart, and here the
       // one before the last may be open as well as the last one over.)
-      ok &= wait(ms.o_full, wk.seg & 1);
+      ok &= wait(ms.o_full, (wk.seg + shift) & 1);
+      if constexpr (Q8 && !LARGE) named_sync(5, 256);  // what any warp noted is known to all
       if (!warp_valid) continue;
       tc_fence_after();
       ms.swap[nb & 1][half][wr] = l;  // (read there last two blocks ago)
       named_sync(1 + quad, 64);
       l += ms.swap[nb & 1][half ^ 1][wr];
       named_sync(1 + quad, 64);
+      if (Q8 && !LARGE && *const_cast<volatile int*>(&ms.large) <= wk.seg) continue;  // left to the second pass
       const bool whole = wk.whole();
       const int slot = 2 * worker + (wk.seg == 0 ? 0 : 1);
       const int row = wk.v.r0 + at.tok, head = wk.h * a.G + at.head;
-      const bool patch = *const_cast<volatile int*>(&ms.flag[wk.seg & 3]) == wk.seg + 1;
+      const bool patch = *const_cast<volatile int*>(&ms.flag[(wk.seg + shift) & 3]) == wk.seg + shift + 1;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       if (!whole && valid && half == 0) a.ml[slot * M + r] = ok ? make_float2(m, l) : make_float2(0.f, NAN);
 #pragma unroll 1
@@ -910,12 +981,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
     }
+    if (Q8 && !LARGE && tid == 0) {
+      ms.taken = seg;
+      ms.blocks = nb;
+    }
   } else {
     // ------------------------------------------------------ operand preparing
     const int pw = warp - kWarpPrep, pt = pw * 32 + lane;
     constexpr int kPT = kPrep * 32;
-    int n = 0;
-    bool ok = true;
+    int n = units0;
+    bool ok = ok0;
     [[maybe_unused]] int turn = 0;  // warp whose turn it is to convert a box
     // unit u of K or V of block b: hand it over, converted (q8) and cleared (V
     // of a partly seen block). One body of code for K and V: more would not
@@ -1005,6 +1080,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(row + ((ch ^ (tok & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (tok & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
           }
+          if constexpr (LARGE) {  // 2^-8 of the values of large tokens, in place of what was stored
+            const uint32_t large = __ballot_sync(0xffffffffu, large_token<NS>(src + C::kSlot / 2 + (page * kPage + lane % kPage) * (NS * 4)));
+            const __half2 small = __half2half2(__ushort_as_half(0x1c00));
+#pragma unroll 1
+            for (int t = 0; t < kSteps; ++t) {
+              const int tok = tok0 + t * kTok;
+              if (!(large >> tok & 1)) continue;
+              const uint4 code = *reinterpret_cast<const uint4*>(src + pb * (kPage * C::kBox) + t * 512 + lane * 16);
+              const __half2 d2 = __half2half2(sc[(page * kPage + tok) * (2 * NS) + (slab0 * 64 + dim) / 32]);
+              const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
+              uint32_t o[8];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t w = cw[j] ^ 0x80808080u;
+                const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
+                const __half2 a2 = __hmul2(__hmul2(__hsub2(*reinterpret_cast<const __half2*>(&lo), off), small), d2);
+                const __half2 b2 = __hmul2(__hmul2(__hsub2(*reinterpret_cast<const __half2*>(&hi), off), small), d2);
+                o[2 * j] = *reinterpret_cast<const uint32_t*>(&a2);
+                o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&b2);
+              }
+              uint8_t* row = slab + (tok >> 3) * group + (tok & 7) * 128;
+              *reinterpret_cast<uint4*>(row + ((ch ^ (tok & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (tok & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+          }
           if (gone || partly) {  // missing pages read as zeros, unseen V values too
 #pragma unroll 1
             for (int t = 0; t < kSteps; ++t) {
@@ -1027,9 +1127,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (found) {
         if (CG == 1) {
-          *const_cast<volatile int*>(&ms.flag[wk.seg & 3]) = wk.seg + 1;
+          *const_cast<volatile int*>(&ms.flag[(wk.seg + shift) & 3]) = wk.seg + shift + 1;
         } else {
-          for (int k = 0; k < 2; ++k) st_cluster(peer_addr(smem_u32(&ms.flag[wk.seg & 3]), k), wk.seg + 1);
+          for (int k = 0; k < 2; ++k) st_cluster(peer_addr(smem_u32(&ms.flag[(wk.seg + shift) & 3]), k), wk.seg + shift + 1);
           asm volatile("fence.acq_rel.cluster;" ::: "memory");
         }
       }
@@ -1041,7 +1141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kRPP = 32 / kLPR;              // rows per warp and pass
     constexpr int kPass = (128 + kPrep * kRPP - 1) / (kPrep * kRPP), kBatch = kPass < 11 ? kPass : 11;
     const int ch = lane % kLPR, sub = lane / kLPR;
-    while (ok && wk.next()) {
+    while (ok && take()) {
       // Q of the tile: the first rows are fetched before the products of the
       // segment before are known to no longer read it, and stored after that
       const int rows = min(128, wk.t.rows - rank * 128);
@@ -1071,7 +1171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 4; ++j) o[t][j] = qp[2 * j] | static_cast<uint32_t>(qp[2 * j + 1]) << 16;
           }
         }
-        if (pass == 0 && wk.seg > 0) ok = wait(ms.q_free, (wk.seg - 1) & 1);
+        if (pass == 0 && wk.seg + shift > 0) ok = wait(ms.q_free, (wk.seg + shift - 1) & 1);
 #pragma unroll
         for (int t = 0; t < kBatch; ++t) {
           const int r0 = ((pass + t) * kPrep + pw) * kRPP, r = r0 + sub;
@@ -1099,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (r < rows && ch < 8 * NS)
             *reinterpret_cast<uint4*>(sq + (ch / 8) * 16384 + r * 128 + (((ch % 8) ^ (r & 7)) << 4)) =
                 make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
-          if (ch == 0 && r < rows) ms.qe[wk.seg % 3][r] = static_cast<int8_t>(e);
+          if (ch == 0 && r < rows) ms.qe[(wk.seg + shift) % 3][r] = static_cast<int8_t>(e);
         }
       }
       if (!ok) break;
@@ -1133,11 +1233,77 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 0; ok && u < C::VU; ++u) ok = unit(1, u, wk.t.block(i - 1));
       }
     }
+    if (Q8 && !LARGE && pt == 0) ms.units = n;
   }
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  if (CG == 2) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// (A function of its own: inlined it took registers from the first pass, 3 % of the time over q8 pools.)
+template <int NS, int CG>
+__device__ __noinline__ void large_pass(const AttendParams& a, const CUtensorMap& tk, const CUtensorMap& tv, uint8_t* smem, uint32_t tm) {
+  attend_pass<NS, true, CG, true>(a, tk, tv, smem, tm);
+}
+
+template <int NS, bool Q8, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_kernel(const __grid_constant__ AttendParams a, const __grid_constant__ CUtensorMap tk,
+                  const __grid_constant__ CUtensorMap tv) {
+  using C = Cfg<NS, Q8, CG>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* const ring = smem + C::kQ;
+  Misc& ms = *reinterpret_cast<Misc*>(ring + C::kSlots * C::kSlot + C::kRawSlots * C::kRaw);
+  const int tid = threadIdx.x, warp = tid / 32;
+  const int rank = CG == 2 ? static_cast<int>(blockIdx.x & 1) : 0;
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+  // all warps (of both blocks): what they did to shared and tensor memory is done
+  auto meet = [] {
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  };
+  if (tid == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      bar_init(bar(ms.full[i]), 1);
+      bar_init(bar(ms.ready[i]), CG * kPrep);
+      bar_init(bar(ms.empty[i]), 1);
+    }
+    for (int i = 0; i < C::kRawSlots; ++i) {
+      bar_init(bar(ms.raw_full[i]), 1);
+      bar_init(bar(ms.raw_empty[i]), kPrep);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bar(ms.s_full[i]), 1);
+      bar_init(bar(ms.p_ready[i]), 8 * CG);
+    }
+    bar_init(bar(ms.pv_done), 1);
+    bar_init(bar(ms.o_full), 1);
+    bar_init(bar(ms.q_ready), CG * kPrep);
+    bar_init(bar(ms.q_free), 1);
+    ms.dead = (smem_u32(smem) & 1023u) != 0;  // (the swizzled tiles need the alignment)
+    for (int i = 0; i < 4; ++i) ms.flag[i] = 0;
+    ms.large = INT_MAX;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kWarpMma) tmem_alloc<CG>(smem_u32(&ms.tmem), 512);
+  find_start<C::M>(a, reinterpret_cast<int*>(ring), &ms.start, blockIdx.x / CG, rank == 0);
+  fence_async_shared();  // the scratch lay where tensor copies go
+  meet();
+  tc_fence_after();
+  const uint32_t tm = ms.tmem;
+  asm volatile("griddepcontrol.launch_dependents;");
+  attend_pass<NS, Q8, CG, false>(a, tk, tv, smem, tm);
+  if constexpr (Q8 && CG == 2) {  // both blocks of a pair go on alike, even if the pool changes under the kernel
+    __syncthreads();
+    if (threadIdx.x == 0) min_cluster(peer_addr(smem_u32(&ms.large), static_cast<uint32_t>(~blockIdx.x & 1)), ms.large);
+  }
+  meet();
+  if constexpr (Q8) {
+    if (ms.large != INT_MAX) {
+      tc_fence_after();
+      large_pass<NS, CG>(a, tk, tv, smem, tm);
+      meet();
+    }
+  }
   if (warp == kWarpMma) tmem_free<CG>(tm, 512);
 }
 

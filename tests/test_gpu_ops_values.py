@@ -1,6 +1,6 @@
 """Attention over values at the ends of the types' ranges, against the 64-bit reference of
-tests/ops_helpers.py: weights far below a row's largest; bf16
-queries of every magnitude the type has."""
+tests/ops_helpers.py: q8 blocks past binary16's largest value, seen and unseen; weights far below
+a row's largest; bf16 queries of every magnitude the type has."""
 import math
 import os
 import sys
@@ -25,6 +25,124 @@ def ops(request):
 def attend(ops, c, **kw):
     pool, rows = c.ops()
     return ops.attend(pool, rows, c.q, **kw)[:c.rows_used]
+
+
+# ------------------------------------------------- q8 values past binary16
+def _put(c, name, seq, pos, head, block, scale, codes):
+    """One q8 block of a cached token: 32 codes and their scale (binary16)."""
+    page, slot, dims = int(c.tables[seq, pos // 16]), pos % 16, slice(32 * block, 32 * block + 32)
+    codes = codes.to(torch.int8).cuda()
+    d = torch.tensor(scale).half().cuda()
+    c.pool[name][page, head, slot, dims] = codes
+    c.pool[name + "_scale"][page, head, slot, block] = d
+    c.value[name][page, head, slot, dims] = codes.double() * d.double()
+
+
+LARGE = [([(150, 400), (3, 700), (1, 33)], 6, 2, 64), ([(2, 90), (140, 300)], 4, 2, 128), ([(70, 150), (4, 500)], 3, 1, 192),
+         ([(60, 333), (1, 40)], 12, 2, 256), ([(3, 1000), (1, 129)], 12, 2, 256)]
+
+
+@pytest.mark.parametrize("amp", [1e5, 1.5e6])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3)])
+@pytest.mark.parametrize("seqs,hq,hkv,dh", LARGE)
+def test_q8_pools_of_large_values(ops, seqs, hq, hkv, dh, window, sinks, amp):
+    """Every block's scale is past 516, where 127 codes leave binary16."""
+    c = Case(seqs, hq, hkv, dh, "q8", "bf16", seed=40, amp=amp)
+    s = 1.0 / (amp * math.sqrt(dh))  # scores of ordinary size
+    got = attend(ops, c, window=window, sinks=sinks, scale=s)
+    assert_within(got, *c.attend_ref(window, sinks, scale=s))
+
+
+@pytest.mark.parametrize("scale,dtype", [(511.5, "f16"), (516.0, "f16"), (600.0, "f16"), (511.5, "bf16"), (516.0, "bf16"), (8000.0, "bf16"),
+                                         (65504.0, "bf16")])
+@pytest.mark.parametrize("dh,hq,hkv,n", [(64, 4, 2, 40), (128, 4, 1, 90), (192, 2, 1, 150), (256, 6, 1, 60), (256, 6, 1, 3)])
+def test_q8_large_blocks_seen_and_unseen(ops, dh, hq, hkv, n, scale, dtype):
+    """Some blocks of a few tokens are large. Rows that see them give the definition's values; the
+    others are as if the tokens were not there (their bound knows nothing of the large values)."""
+    first, window = 60, 25
+    c = Case([(n, n + first), (2, 50)], hq, hkv, dh, "q8", dtype, seed=41, pad_rows=0)
+    g = torch.Generator().manual_seed(42)
+    codes = torch.randint(-127, 128, (32,), generator=g)
+    codes[0], codes[1], codes[2] = 127, -127, -128
+    block = dh // 32 - 1
+    # the queries are small where K is large, so that the scores stay of ordinary size
+    c.q[..., 32 * block:] = (c.q[..., 32 * block:].float() * (2.0 / (scale * 127))).to(c.dtype)
+    large = [first + n - 2, first + n // 2, 5]  # seen by the last rows, by the later half, outside most windows
+    for pos in large:
+        _put(c, "v", 0, pos, 0, 0, scale, codes)
+        _put(c, "k", 0, pos, hkv - 1, block, scale, codes)
+    for window in (0, window):
+        got = attend(ops, c, window=window)
+        want, bound = c.attend_ref(window)
+        assert_within(got, want, bound)
+        was = c.value["v"]
+        c.value["v"] = was.clone()
+        for pos in large:
+            c.value["v"][int(c.tables[0, pos // 16]), 0, pos % 16, :32] = 0
+        want, bound = c.attend_ref(window)
+        c.value["v"] = was
+        p = torch.arange(first, first + n)
+        sees = torch.zeros(n, dtype=torch.bool)
+        for pos in large:
+            sees |= (pos <= p) & ((p - pos < window) if window else True)
+        blind = torch.cat([~sees, torch.ones(2, dtype=torch.bool)]).cuda()  # the second sequence too
+        assert window == 0 or n < 30 or int(blind.sum()) > 5
+        assert_within(got[blind], want[blind], bound[blind])
+
+
+@pytest.mark.parametrize("n", [1, 5, 100])
+def test_q8_large_tokens_all_over_a_long_context(ops, n):
+    """Every tenth token has large blocks of V, every seventh of K, of all sizes up to the largest scale."""
+    T, dh = 3000, 256
+    c = Case([(n, T)], 6, 1, dh, "q8", "bf16", seed=43)
+    page, slot = c.tables[0].long().repeat_interleave(16)[:T], torch.arange(T, device="cuda") % 16
+    g = torch.Generator().manual_seed(44)
+    for name, step, block in (("v", 10, 3), ("k", 7, 0)):
+        t = torch.arange(0, T, step)
+        d = (512 * 127 ** torch.rand(len(t), generator=g)).half().cuda()
+        P, S = page[t], slot[t]
+        c.pool[name + "_scale"][P, 0, S, block] = d
+        dims = slice(32 * block, 32 * block + 32)
+        c.value[name][P, 0, S, dims] = c.pool[name][P, 0, S, dims].double() * d.double()[:, None]
+    c.q[..., :32] = (c.q[..., :32].float() * 1e-6).to(c.dtype)
+    assert_within(attend(ops, c), *c.attend_ref())
+    assert_within(attend(ops, c, window=700, sinks=30), *c.attend_ref(700, 30))
+
+
+@pytest.mark.parametrize("n,count,dh,hq,hkv", [(1, 400, 64, 4, 2), (3, 250, 256, 6, 1), (100, 24, 128, 4, 2)])
+def test_q8_large_tokens_in_some_of_many_sequences(ops, n, count, dh, hq, hkv):
+    """Blocks take several sequences each, and cut them: results before the first large value, behind it
+    and across the cuts, into an output of their own, over the queries and over the gate."""
+    c = Case([(min(n, 20 + 37 * i % 400), 20 + 37 * i % 400) for i in range(count)], hq, hkv, dh, "q8", "bf16", seed=50, pad_rows=3)
+    g = torch.Generator().manual_seed(51)
+    codes = torch.randint(-127, 128, (32,), generator=g)
+    for i in (count // 3, count // 3 + 1, count - 1):
+        T = c.seqs[i][1]
+        for pos in (0, T // 2, T - 1):
+            _put(c, "v", i, pos, hkv - 1, 1, 3000.0 + i, codes)
+            _put(c, "k", i, pos, 0, 0, 900.0, codes)
+    c.q[..., :32] = (c.q[..., :32].float() * 2e-5).to(c.dtype)
+    pool, rows = c.ops()
+    q, gate = c.q.clone(), c.gate.clone()
+    for out in (torch.full_like(q, 5.0), c.q, c.gate):
+        behind = out[c.rows_used:].clone()
+        got = ops.attend(pool, rows, c.q, gate=c.gate, out=out)
+        assert torch.equal(got[c.rows_used:], behind)
+        got = got[:c.rows_used].clone()
+        c.q.copy_(q)
+        c.gate.copy_(gate)
+        assert_within(got, *c.attend_ref(gate=True))
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_q8_scales_that_are_no_numbers_in_unused_places(ops, n):
+    """What lies behind a sequence's end or on no page of it changes nothing, not even a bit."""
+    c = Case([(n, 333), (1, 17)], 6, 1, 256, "q8", "f16", seed=52)
+    want = attend(ops, c)
+    for name in ("k_scale", "v_scale"):
+        s = c.pool[name]
+        s[torch.isnan(s)] = 60000.0
+    assert torch.equal(attend(ops, c), want)
 
 
 # ------------------------------------------------- weights far below the largest
