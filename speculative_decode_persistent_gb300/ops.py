@@ -149,6 +149,19 @@ class KVRows:
         return _ROWS(*self._head, n_rows, self._stride, mean if self.max_q is None else min(self.max_q, n_rows))
 
 
+def _overlap(n: int, heads: int, dh: int, row: int, head: int) -> bool:
+    """Whether two of the n x heads vectors of dh elements at r row + h head share an element."""
+    if n == 0 or head >= dh and (n == 1 or row >= (heads - 1) * head + dh):  # rows of heads
+        return False
+    if row >= dh and (heads == 1 or head >= (n - 1) * row + dh):  # heads of rows
+        return False
+    if n > 1 and row < dh or heads > 1 and head < dh:
+        return True
+    # the multiples of row on both sides of each multiple of head
+    return any(a < n and abs(a * row - b * head) < dh
+               for b in range(1, heads) for a in (b * head // row, b * head // row + 1))
+
+
 def _dense(t, heads: int, dh: int, what: str, out=False):
     """(address, row stride, head stride) of a dense tensor, checked."""
     shape = t.shape
@@ -157,7 +170,7 @@ def _dense(t, heads: int, dh: int, what: str, out=False):
     row, head, one = t.stride()
     if one != 1:
         _refuse(f"{what} (contiguous head dim)")
-    if out and shape[0] and not (head >= dh and (shape[0] == 1 or row >= (heads - 1) * head + dh)):
+    if out and _overlap(shape[0], heads, dh, row, head):
         _refuse(f"{what} (rows of an output must not overlap)")
     if t.requires_grad and torch.is_grad_enabled():
         _refuse(f"{what} (no gradient is defined: detach it or use torch.no_grad)")
