@@ -1820,8 +1820,11 @@ cudaError_t launch_q8_encode(const float* x, int64_t n_blocks, int8_t* q, uint16
   const int64_t grid = (n_blocks * 32 + kBlock - 1) / kBlock;
   if (n_blocks <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  q8_encode_kernel<<<static_cast<unsigned>(grid), kBlock, 0, stream>>>(x, n_blocks, q, d16);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};  // (the launch's own status, not an error that an earlier call left)
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kBlock);
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, q8_encode_kernel, x, n_blocks, q, d16);
 }
 
 // One row of K or V that an earlier phase of this launch stored into the pool

@@ -69,8 +69,11 @@ __global__ void pack_units_kernel(PackSrc p, uint8_t* __restrict__ dst, int n_ti
 cudaError_t pack_units(const PackSrc& p, uint8_t* dst, int n_tiles, int nsb, cudaStream_t s) {
   const int units = n_tiles * nsb;
   if (units == 0) return cudaSuccess;
-  pack_units_kernel<<<units, 128, 0, s>>>(p, dst, n_tiles, nsb);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};  // (the launch's own status, not an error that an earlier call left)
+  cfg.gridDim = dim3(units);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  return cudaLaunchKernelEx(&cfg, pack_units_kernel, p, dst, n_tiles, nsb);
 }
 
 }  // namespace mk

@@ -123,5 +123,9 @@ extern "C" mk_status mk_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, c
       !encode_map(&tv, pool->v, *pool, box, kPage, slabs_v))
     return MK_ERR_CUDA;
   const cudaError_t e = (q8 ? launch_attend_q8 : launch_attend_f16)(ns, cg, p, tk, tv, device, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return MK_ERR_CUDA;
+  }
+  return MK_OK;
 }

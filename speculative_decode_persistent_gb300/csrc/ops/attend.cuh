@@ -1342,10 +1342,7 @@ template <int NS, bool Q8, int CG>
 cudaError_t launch_attend(AttendParams a, const CUtensorMap& tk, const CUtensorMap& tv, int device, cudaStream_t stream) {
   using C = Cfg<NS, Q8, CG>;
   a.workers = resident_workers<NS, Q8, CG>(device);
-  if (!a.workers) {
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? cudaErrorInvalidDevice : e;
-  }
+  if (!a.workers) return cudaErrorInvalidDevice;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;

@@ -165,9 +165,16 @@ mk_status run(const mk_kv_pool* pool, const mk_kv_rows* rows, const mk_dense* k,
     RowsArgs a{*pool, *rows, *k, *v, static_cast<int>(r),
                static_cast<int>(rows->n_rows - r < slab ? rows->n_rows - r : slab), static_cast<uint32_t>(per_row),
                static_cast<uint32_t>((1ll << 32) / per_row)};
-    fn<<<static_cast<unsigned>((a.n * per_row + kBlock - 1) / kBlock), kBlock, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    cudaLaunchConfig_t cfg{};  // (the launch's own status: an error that an earlier call left is not this one's)
+    cfg.gridDim = dim3(static_cast<unsigned>((a.n * per_row + kBlock - 1) / kBlock));
+    cfg.blockDim = dim3(kBlock);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    if (cudaLaunchKernelEx(&cfg, fn, a) != cudaSuccess) {
+      cudaGetLastError();
+      return MK_ERR_CUDA;
+    }
   }
-  return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+  return MK_OK;
 }
 
 }  // namespace

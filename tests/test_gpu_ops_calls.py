@@ -1,4 +1,5 @@
-"""Calls of the KV-cache operators around the GPU work: outputs in other layouts."""
+"""Calls of the KV-cache operators around the GPU work: outputs in other layouts, errors that another
+call left."""
 import os
 import sys
 
@@ -35,3 +36,33 @@ def test_outputs_with_heads_first(ops, kv):
         assert torch.equal(view(o), want) and torch.equal(view(ok), k) and torch.equal(view(ov), v)
         for t in (o, ok, ov):
             assert bool((t[:, c.n_rows:] == 7).all())
+
+
+def _tiny(**kw):
+    from gen import configs
+    from gen.synth import make_weights
+    from speculative_decode_persistent_gb300 import mk
+    return mk.Engine(configs.TINY, make_weights(configs.TINY, 0), 0, 16, **kw)
+
+
+def test_an_error_that_another_call_left(ops):
+    """The runtime's last error, left by an unrelated host call, is neither reported nor cleared by the
+    calls that are queued after it."""
+    from speculative_decode_persistent_gb300 import mk
+    c = Case([(3, 20)], 4, 2, 64, "q8", "f16", seed=51, pad_rows=0)
+    pool, rows = c.ops()
+    x = torch.randn((4, 32), device="cuda")
+    calls = (lambda: ops.kv_write(pool, rows, c.new_k, c.new_v), lambda: ops.kv_read(pool, rows),
+             lambda: ops.attend(pool, rows, c.q), lambda: mk.q8_encode(x))
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    host = torch.empty(64)
+    for call in calls:
+        assert int(torch.cuda.cudart().cudaHostUnregister(host.data_ptr())) != 0  # it was never registered
+        call()
+        with pytest.raises(RuntimeError):  # still there, for the next check of torch's own
+            torch.ones(3, device="cuda")
+        torch.cuda.synchronize()
+    k, _ = ops.kv_read(pool, rows)
+    assert float((k.float() - c.new_k.float()).abs().max()) < 0.05
