@@ -274,17 +274,20 @@ class Engine:
                 np.int8 if arr.dtype == np.int8 else np.int16)))
 
     def seq_set(self, seq: int, length: int, pages, S=None, conv=None):
-        """Install a sequence; S/conv (numpy fp32) go into its state slot 0."""
+        """Install a sequence; S/conv (numpy arrays or tensors) go into its state slot 0 as fp32."""
         Sv, Cv = self.state_views()
         if Sv is None:
             S = conv = None
         if S is not None:
-            Sv[seq, 0].copy_(self.torch.from_numpy(np.ascontiguousarray(S, np.float32)))
+            Sv[seq, 0].copy_(self._tensor(S))
         if conv is not None:
-            Cv[seq, 0].copy_(self.torch.from_numpy(np.ascontiguousarray(conv, np.float32)))
+            Cv[seq, 0].copy_(self._tensor(conv))
         self.torch.cuda.synchronize(self.device)
         pages = np.ascontiguousarray(pages, np.int32)
         _check(lib.mk_seq_set(self.ctx, seq, length, _np_ptr(pages), len(pages)), "mk_seq_set")
+
+    def _tensor(self, x):
+        return x.detach() if self.torch.is_tensor(x) else self.torch.from_numpy(np.ascontiguousarray(x, np.float32))
 
     def seq_get(self, seq: int):
         n = self.layout.max_pages_per_seq
@@ -369,7 +372,8 @@ class Engine:
         saved elsewhere: CUDA tensors [kv layers][tokens][kv heads][head dim]
         (K after RoPE), stored on the lowest free pages, rounded or quantised
         as the step stores its own rows. S, conv: its recurrent state, as in
-        seq_set; zero when not given."""
+        seq_set or as seq_get gives it; zero when not given. A refused load
+        leaves everything as it was."""
         from . import ops
         torch, m = self.torch, self.model
         n_kv = sum(1 for x in m["kinds"] if x == 1) + (1 if self.layout.has_mtp else 0)
@@ -377,9 +381,16 @@ class Engine:
             raise MkError(-1, "seq_load (k, v [kv layers][tokens][kv heads][head dim])")
         if not 0 <= seq < self.max_seqs:
             raise MkError(-1, "seq_load (sequence)")
+        state = []
         for x, view in zip((S, conv), self.state_views()):
-            if x is not None and view is not None and tuple(np.shape(x)) != tuple(view.shape[2:]):
-                raise MkError(-1, "seq_load (shape of the recurrent state)")
+            if x is not None and view is not None:
+                try:
+                    x = self._tensor(x).to(self.device, torch.float32)
+                except (TypeError, ValueError, RuntimeError):
+                    raise MkError(-1, "seq_load (the recurrent state is numbers)") from None
+                if x.shape != view.shape[2:]:
+                    raise MkError(-1, "seq_load (shape of the recurrent state)")
+            state.append(x)
         used = set()
         for s in range(self.max_seqs):
             if s != seq:
@@ -402,7 +413,7 @@ class Engine:
                 Sv[seq, 0].zero_()
             if conv is None:
                 Cv[seq, 0].zero_()
-        self.seq_set(seq, n, pages, S, conv)
+        self.seq_set(seq, n, pages, *state)
 
     def seq_kv(self, seq: int, dtype=None):
         """Dense K and V of a committed sequence, [kv layers][tokens][kv heads]

@@ -1,8 +1,9 @@
 """Calls of the KV-cache operators around the GPU work: outputs in other layouts, errors that another
-call left."""
+call left, contexts loaded into an engine."""
 import os
 import sys
 
+import numpy as np
 import pytest
 import torch
 
@@ -66,3 +67,59 @@ def test_an_error_that_another_call_left(ops):
         torch.cuda.synchronize()
     k, _ = ops.kv_read(pool, rows)
     assert float((k.float() - c.new_k.float()).abs().max()) < 0.05
+
+
+def _decode(eng, seq, n):
+    """n greedy tokens of a sequence, one row a step, each step's token fed into the next."""
+    got, token = [], 11
+    for _ in range(n):
+        out, _ = eng.step([token], [eng.seq_get(seq)["length"]], [seq])
+        eng.commit([seq], [1])
+        token = int(out[0])
+        got.append(token)
+    return got
+
+
+def test_a_context_saved_and_loaded_again(ops):
+    """What seq_kv and seq_get give is what seq_load takes: K, V and the recurrent state, on the device or
+    from the host."""
+    eng = _tiny()
+    eng.seq_new(0)
+    eng.step([5, 6, 7, 8], [0, 1, 2, 3], [0] * 4, [1, 1, 1, 2])
+    info, (k, v) = eng.seq_get(0), eng.seq_kv(0)
+    assert info["length"] == 4 and k.shape[1] == 4
+    S, conv = info["S"].clone(), info["conv"].clone()
+    eng.seq_load(1, k, v, info["S"], info["conv"])
+    eng.seq_load(2, k, v, S.cpu().numpy(), conv.double())
+    eng.seq_load(3, k, v, S.cpu(), conv.cpu().numpy())
+    for s in (1, 2, 3):
+        now = eng.seq_get(s)
+        assert now["length"] == 4 and torch.equal(now["S"], S) and torch.equal(now["conv"], conv)
+        assert all(torch.equal(a, b) for a, b in zip(eng.seq_kv(s), (k, v)))
+    want = _decode(eng, 0, 5)
+    assert all(_decode(eng, s, 5) == want for s in (1, 2, 3))
+    eng.close()
+
+
+def test_a_refused_load_leaves_the_old_context(ops):
+    from speculative_decode_persistent_gb300.mk import MkError
+    eng = _tiny()
+    eng.seq_new(0)
+    eng.step([5, 6, 7, 8], [0, 1, 2, 3], [0] * 4, [1, 1, 1, 2])
+    eng.seq_load(0, *eng.seq_kv(0), eng.seq_get(0)["S"], eng.seq_get(0)["conv"])  # state in slot 0 now
+    info, (k, v) = eng.seq_get(0), eng.seq_kv(0)
+    S, conv, pages = info["S"].clone(), info["conv"].clone(), list(info["pages"])
+    other = torch.randn_like(k)
+    words = np.full(tuple(S.shape), "x")
+    for status, args in ((-1, (other, other, words)), (-1, (other, other, S * 2, np.full(tuple(conv.shape), "x"))),
+                         (-1, (other, other, None, conv[1:])), (-1, (other, other, S * 2, conv[..., 1:])), (-1, (other, other, S[None])),
+                         (-1, (other.double(), other.double())), (-1, (other, other.float())), (-1, (other, other.cpu())),
+                         (-1, (other, other[:, :2])), (-1, (torch.randn((1, 16 * 16 + 1, 1, 64), device="cuda"),) * 2)):
+        with pytest.raises(MkError) as e:
+            eng.seq_load(0, *args)
+        assert e.value.status == status
+        now = eng.seq_get(0)
+        assert now["length"] == 4 and list(now["pages"]) == pages
+        assert torch.equal(now["S"], S) and torch.equal(now["conv"], conv)
+        assert all(torch.equal(a, b) for a, b in zip(eng.seq_kv(0), (k, v)))
+    eng.close()
