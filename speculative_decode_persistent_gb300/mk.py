@@ -402,6 +402,7 @@ class Engine:
         pages = [p for p in range(self.layout.n_pages) if p not in used][:need]
         if len(pages) < need:
             raise MkError(-2, "seq_load (no free pages)")
+        self._before_current()
         if n:
             dev = [torch.tensor(x, dtype=torch.int32, device=self.device) for x in ([0, n], [n], [pages])]
             rows = ops.KVRows(*dev, n_rows=n)
@@ -424,11 +425,18 @@ class Engine:
         n_kv = sum(1 for x in m["kinds"] if x == 1) + (1 if self.layout.has_mtp else 0)
         k, v = (torch.empty((n_kv, n, m["hkv"], m["dh"]), dtype=dtype or torch.float16, device=self.device) for _ in "kv")
         if n:
+            self._before_current()
             rows = self.seq_rows([seq], [n])
             for i in range(n_kv):
                 ops.kv_read(self.kv_pool(i), rows, out=(k[i], v[i]))
             self._after_current()
         return k, v
+
+    def _before_current(self):
+        """What the current stream does with the pool comes after the steps queued so far."""
+        current = self.torch.cuda.current_stream(self.device)
+        if current != self.stream:
+            current.wait_stream(self.stream)
 
     def _after_current(self):
         """Later steps come after what the current stream still reads from the pool."""
@@ -442,6 +450,7 @@ class Engine:
         from . import ops
         if q.dim() != 3 or q.shape[1] != self.layout.fa_hq:
             raise MkError(-1, "attend (q [rows][query heads][head dim])")
+        self._before_current()
         out = ops.attend(self.kv_pool(layer), self.seq_rows(seqs, new_rows), q, window=window, sinks=sinks, gate=gate,
                          out=out)
         self._after_current()

@@ -1,5 +1,5 @@
 """Calls of the KV-cache operators around the GPU work: outputs in other layouts, errors that another
-call left, contexts loaded into an engine."""
+call left, contexts loaded into an engine, the engine's own stream."""
 import os
 import sys
 
@@ -122,4 +122,31 @@ def test_a_refused_load_leaves_the_old_context(ops):
         assert now["length"] == 4 and list(now["pages"]) == pages
         assert torch.equal(now["S"], S) and torch.equal(now["conv"], conv)
         assert all(torch.equal(a, b) for a, b in zip(eng.seq_kv(0), (k, v)))
+    eng.close()
+
+
+def test_calls_on_another_stream_come_after_the_engines_work(ops):
+    """The engine on a stream of its own, the calls on the default one: they see what was queued there
+    before, and what they write is not overtaken by it."""
+    s = torch.cuda.Stream()
+    eng = _tiny(stream=s)
+    one = lambda x: torch.full((1, 40, 1, 64), x, device="cuda", dtype=torch.float16)  # noqa: E731
+    eng.seq_load(0, one(1.0), one(1.0))
+    half = torch.float16
+
+    def later(x):  # the pool's values change on the engine's stream, a tenth of a second from now
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(200_000_000)
+            for t in eng.kv_views().values():
+                t.view(half).fill_(x)
+
+    later(2.0)
+    assert all(bool((t == 2).all()) for t in eng.seq_kv(0))
+    q = torch.zeros((3, 4, 64), device="cuda", dtype=half)
+    later(3.0)
+    assert bool((eng.attend(0, q, [0], [3]) == 3).all())
+    later(4.0)
+    eng.seq_load(0, one(5.0), one(5.0))
+    assert all(bool((t == 5).all()) for t in eng.seq_kv(0))
     eng.close()
