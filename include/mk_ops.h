@@ -132,6 +132,14 @@ typedef struct mk_attend_args {
 size_t mk_attend_work_bytes(const mk_kv_pool* pool, const mk_kv_rows* rows, int32_t hq);
 mk_status mk_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, const mk_attend_args* args, void* stream);
 
+/*
+ * Test hook, of the whole process: in the mk_attend calls that follow, waits
+ * give up after wait_us (0: the two seconds, the most), and the worker skip_worker (a
+ * thread block, or a pair of them; -1: none) never gets its queries, so that its
+ * waits run out. Errors: MK_ERR_INVALID.
+ */
+mk_status mk_debug_attend_wait(int32_t wait_us, int32_t skip_worker);
+
 #ifdef __cplusplus
 }
 #endif

@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "attend.cuh"
@@ -27,6 +28,10 @@ mk_status check_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, int32_t h
   const double tiles = static_cast<double>(rows->n_rows) * hq / 128 + static_cast<double>(rows->n_seqs) * pool->hkv;
   return tiles * (rows->table_stride / (kBN / kPage) + 2 + item_cost(256)) > 2e9 ? MK_ERR_UNSUPPORTED : MK_OK;
 }
+
+// Test hook (mk_debug_attend_wait).
+constexpr int kWaitUs = 2000000;
+std::atomic<int> g_wait_us{kWaitUs}, g_skip{-1};
 
 constexpr size_t kJoinBytes = (kMaxWorkers * sizeof(JoinInfo) + 255) / 256 * 256;
 // two parts per worker of 128 rows a block
@@ -71,6 +76,13 @@ extern "C" size_t mk_attend_work_bytes(const mk_kv_pool* pool, const mk_kv_rows*
   return kJoinBytes + kMlBytes + 2ull * kMaxWorkers * 128 * pool->dh * sizeof(float);
 }
 
+extern "C" mk_status mk_debug_attend_wait(int32_t wait_us, int32_t skip_worker) {
+  if (wait_us < 0 || wait_us > mk::ops::kWaitUs || skip_worker < -1) return MK_ERR_INVALID;
+  mk::ops::g_wait_us.store(wait_us ? wait_us : mk::ops::kWaitUs);
+  mk::ops::g_skip.store(skip_worker);
+  return MK_OK;
+}
+
 extern "C" mk_status mk_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, const mk_attend_args* a, void* stream) {
   using namespace mk::ops;
   if (!a) return MK_ERR_INVALID;
@@ -106,6 +118,8 @@ extern "C" mk_status mk_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, c
   if (p.vo && reinterpret_cast<uintptr_t>(a->out.data) % 32 == 0 && a->out.row_stride % 16 == 0 && a->out.head_stride % 16 == 0)
     p.vo = 2;
   p.vg = dense_vec(a->gate, a->dtype);
+  p.wait_us = g_wait_us.load();
+  p.skip = g_skip.load();
   uint8_t* w = static_cast<uint8_t*>(a->work);
   p.join = reinterpret_cast<JoinInfo*>(w);
   p.ml = reinterpret_cast<float2*>(w + kJoinBytes);

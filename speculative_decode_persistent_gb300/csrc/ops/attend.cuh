@@ -61,7 +61,9 @@
 // pages; 4 x 3 rows over 23,003 fp16 tokens each in 71 us, 5.3 TB/s, q8 in 69 us
 // (200 MB; converting again). One row over 4,097 tokens: 15.6 us, latency.
 //
-// Every wait is bounded; a worker that gives up writes NaN for its rows.
+// Every wait is bounded; a worker that gives up writes NaN for its rows. Before its
+// blocks end it waits (with a limit again) for the copies and products that are
+// still under way: they would reach shared and tensor memory of the next blocks.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -82,7 +84,6 @@ constexpr int kMaxWorkers = 160;     // at least the SM count
 // it, and what the weights are raised by. (4 and 11 against 8 and 7: the same times
 // within 0.3 %, and 2^4 times finer weights.)
 constexpr float kLazy = 4.f, kLift = 15.f - kLazy;
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kJoinSplit = 8;        // join blocks per cut
 // An item's start and end in blocks, 4 for one block, 8 for a pair (a 4,096-row
 // prompt over 24 heads of 256: 2 208 us, 4 178 us, 8 166 us; one row over 4K q8
@@ -101,6 +102,8 @@ struct AttendParams {
   int hq, G, g_inv, dtype, window, sinks, workers;  // g_inv = 2^20 / G + 1: x / G = x g_inv >> 20 for x < 2^20 / G
   float c;         // scale x log2(e)
   int vq, vo, vg;  // 16-byte access to q, out, gate (out: 2 with 32 bytes)
+  int skip;        // test hook: the worker whose queries are not handed over, -1: none
+  int wait_us;     // after which a wait gives up
   JoinInfo* join;  // [kMaxWorkers]
   float2* ml;      // [2 workers][128 CG] reference and sum of a part
   float* part;     // [2 workers][128 CG][dh] unnormalised output
@@ -294,9 +297,10 @@ struct Segment {
 
 struct Misc {
   uint64_t ready[8], full[8], empty[8], raw_full[6], raw_empty[6];
-  uint64_t s_full[2], p_ready[2], pv_done, o_full, q_ready, q_free;
+  uint64_t s_full[2], p_ready[2], pv_done, o_full, q_ready, q_free, drained;
   uint32_t tmem;
-  int dead;
+  int dead, wait_us;  // side by side: bar_wait
+  int failed;  // the pair's products stopped before their end: `drained` follows
   Start start;
   int large;             // first segment with large q8 values, INT_MAX: none; the same in both blocks of a pair
   int taken, units, blocks;  // segments, units and blocks of the first pass
@@ -544,7 +548,7 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
   const int worker = blockIdx.x / CG;
   volatile int* const dead = &ms.dead;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
-  auto wait1 = [&](uint64_t& b, uint32_t parity) { return bar_wait(smem_u32(&b), parity, dead, kWaitNs); };
+  auto wait1 = [&](uint64_t& b, uint32_t parity) { return bar_wait(smem_u32(&b), parity, dead); };
   auto wait = [&](uint64_t& b, uint32_t parity) { return __all_sync(0xffffffffu, wait1(b, parity)) != 0; };  // whole warps
   // barriers the product-issuing block waits on, reached from both blocks
   auto lead_arrive = [&](uint64_t& b) {
@@ -646,9 +650,7 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
       const int ns = Q8 ? C::kRawSlots : C::kSlots;
       for (int k = max(0, n - ns); k < n; ++k) {
         uint64_t& b = Q8 ? ms.raw_full[k % ns] : ms.full[k % ns];
-        const uint64_t t0 = now_ns();
-        while (!bar_try(bar(b), (k / ns) & 1) && now_ns() - t0 < 50000000ull) {
-        }
+        bar_drain(bar(b), (k / ns) & 1);
       }
     }
   } else if (warp == kWarpMma) {
@@ -738,6 +740,14 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
           }
           if (!ok) break;
         }
+      }
+      // a wait gave up: what was issued, and its arrivals on both blocks' barriers, come to an end first
+      if (ok0 && __any_sync(0xffffffffu, !ok || *dead)) {
+        if (elect_one()) {
+          for (int k = 0; k < CG; ++k) st_cluster(peer_addr(smem_u32(&ms.failed), k), 1);
+          mma_commit<CG>(bar(ms.drained));
+        }
+        __syncwarp();
       }
     }
   } else if (warp < 8) {
@@ -1277,9 +1287,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     bar_init(bar(ms.pv_done), 1);
     bar_init(bar(ms.o_full), 1);
-    bar_init(bar(ms.q_ready), CG * kPrep);
+    bar_init(bar(ms.q_ready), CG * kPrep + (static_cast<int>(blockIdx.x / CG) == a.skip));  // (an arrival that never comes)
     bar_init(bar(ms.q_free), 1);
+    bar_init(bar(ms.drained), 1);
     ms.dead = (smem_u32(smem) & 1023u) != 0;  // (the swizzled tiles need the alignment)
+    ms.wait_us = a.wait_us;
+    ms.failed = 0;
     for (int i = 0; i < 4; ++i) ms.flag[i] = 0;
     ms.large = INT_MAX;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1303,6 +1316,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       large_pass<NS, CG>(a, tk, tv, smem, tm);
       meet();
     }
+  }
+  if (*const_cast<volatile int*>(&ms.failed)) {
+    if (warp == kWarpMma) bar_drain(bar(ms.drained), 0);
+    meet();
   }
   if (warp == kWarpMma) tmem_free<CG>(tm, 512);
 }

@@ -55,10 +55,11 @@ for _name, _res, _args in (
         ("mk_kv_write", i32, [_P(mk_kv_pool), _P(mk_kv_rows), _P(mk_dense), _P(mk_dense), i32, vp]),
         ("mk_kv_read", i32, [_P(mk_kv_pool), _P(mk_kv_rows), _P(mk_dense), _P(mk_dense), i32, vp]),
         ("mk_attend_work_bytes", sz, [_P(mk_kv_pool), _P(mk_kv_rows), i32]),
-        ("mk_attend", i32, [_P(mk_kv_pool), _P(mk_kv_rows), _P(mk_attend_args), vp])):
+        ("mk_attend", i32, [_P(mk_kv_pool), _P(mk_kv_rows), _P(mk_attend_args), vp]),
+        ("mk_debug_attend_wait", i32, [i32, i32])):
     _fn = getattr(lib, _name)
     _fn.restype, _fn.argtypes = _res, _args
-EXPORTS = ["mk_kv_write", "mk_kv_read", "mk_attend_work_bytes", "mk_attend"]
+EXPORTS = ["mk_kv_write", "mk_kv_read", "mk_attend_work_bytes", "mk_attend", "mk_debug_attend_wait"]
 
 # The calls below pass the structs as packed bytes, which costs a few hundred
 # nanoseconds less a field than ctypes structures: a small call is bound by

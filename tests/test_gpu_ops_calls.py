@@ -1,5 +1,5 @@
 """Calls of the KV-cache operators around the GPU work: outputs in other layouts, errors that another
-call left, contexts loaded into an engine, the engine's own stream."""
+call left, contexts loaded into an engine, the engine's own stream, waits that give up."""
 import os
 import sys
 
@@ -150,3 +150,35 @@ def test_calls_on_another_stream_come_after_the_engines_work(ops):
     eng.seq_load(0, one(5.0), one(5.0))
     assert all(bool((t == 5).all()) for t in eng.seq_kv(0))
     eng.close()
+
+
+# (workers that have blocks: an item's 4 or 8 first units of the line have none, with few items a worker may get only such)
+@pytest.mark.parametrize("kv,seqs,hq,hkv,dh,skip,large", [
+    ("f16", [(3, 3000), (1, 500)], 6, 2, 128, 15, False), ("f16", [(300, 2000), (2, 60)], 6, 2, 256, 4, False),
+    ("q8", [(3, 5000)], 6, 2, 256, 20, False), ("q8", [(150, 900), (1, 400)], 12, 2, 256, 5, False),
+    ("q8", [(1, 300)] * 200, 4, 2, 64, 5, False), ("q8", [(3, 3000)] * 3, 6, 2, 256, 40, True), ("q8", [(150, 900)] * 8, 12, 2, 128, 3, True)])
+def test_a_wait_that_gives_up(ops, kv, seqs, hq, hkv, dh, skip, large):
+    """One worker's queries are never handed over: its waits run out after 2 ms, its rows become NaN, all
+    others are right, the call ends and so does the next one, with the right result."""
+    c = Case(seqs, hq, hkv, dh, kv, "bf16", seed=60, amp=2e5 if large else 1.0)
+    kw = dict(scale=1.0 / (2e5 * dh ** 0.5)) if large else {}
+    pool, rows = c.ops()
+    want, bound = c.attend_ref(**kw)
+    before = ops.attend(pool, rows, c.q, **kw)[:c.rows_used]
+    assert_within(before, want, bound)
+    assert [ops.lib.mk_debug_attend_wait(*x) for x in ((-1, -1), (2_000_001, -1), (0, -2))] == [-1] * 3
+    assert ops.lib.mk_debug_attend_wait(2_000, skip) == 0
+    try:
+        for _ in range(2):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            got = ops.attend(pool, rows, c.q, **kw)[:c.rows_used]
+            b.record()
+            torch.cuda.synchronize()
+            lost = torch.isnan(got).all(-1)
+            assert bool(lost.any()) and not bool(lost.all())
+            assert_within(got[~lost], want[~lost], bound[~lost])
+            assert a.elapsed_time(b) < 1000.0
+    finally:
+        ops.lib.mk_debug_attend_wait(0, -1)
+    assert torch.equal(ops.attend(pool, rows, c.q, **kw)[:c.rows_used], before)
