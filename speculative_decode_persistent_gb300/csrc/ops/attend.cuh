@@ -53,13 +53,14 @@
 // the factor of a K token goes into its scores, that of a V token into its weight's
 // exponent (also in the running maximum, so that the weight stays a binary16
 // number) and out of the sum of the weights. (That code in the only pass: 69 -> 83 us
-// for 4 x 3 rows, 202 -> 252 us for 512 rows over 20K tokens.)
+// for 4 x 3 rows over 23K tokens, 202 -> 252 us for 512 rows over 20K. Two passes take
+// 2.7 times as long as one: 204 and 556 us.)
 //
 // Bound and measured (24 query heads, 4 kv heads of 256). Many rows: the
-// products; 2,048 rows over 20,512 fp16 tokens in 565 us, 1,736 TFLOP/s, over
-// q8 tokens in 687 us, where converting the codes takes as long. Few rows: the
-// pages; 4 x 3 rows over 23,003 fp16 tokens each in 71 us, 5.3 TB/s, q8 in 69 us
-// (200 MB; converting again). One row over 4,097 tokens: 15.6 us, latency.
+// products; 2,048 rows over 20,512 fp16 tokens in 559 us, 1,755 TFLOP/s, over
+// q8 tokens in 682 us, where converting the codes takes as long. Few rows: the
+// pages; 4 x 3 rows over 23,003 fp16 tokens each in 71 us, 5.3 TB/s, q8 in 71 us
+// (200 MB; converting again). One row over 4,097 tokens: 15.8 us, latency.
 //
 // Every wait is bounded; a worker that gives up writes NaN for its rows. Before its
 // blocks end it waits (with a limit again) for the copies and products that are
@@ -81,8 +82,8 @@ namespace ops {
 constexpr int kBN = 128;             // tokens per block: eight pages
 constexpr int kMaxWorkers = 160;     // at least the SM count
 // Reference of the softmax (see above), as powers of two: how far a score may pass
-// it, and what the weights are raised by. (4 and 11 against 8 and 7: the same times
-// within 0.3 %, and 2^4 times finer weights.)
+// it, and what the weights are raised by. (4 and 11 against 8 and 7: 2^4 times finer
+// weights; the same times, but 2 % more where a window begins with a few sinks.)
 constexpr float kLazy = 4.f, kLift = 15.f - kLazy;
 constexpr int kJoinSplit = 8;        // join blocks per cut
 // An item's start and end in blocks, 4 for one block, 8 for a pair (a 4,096-row
@@ -299,7 +300,7 @@ struct Misc {
   uint64_t ready[8], full[8], empty[8], raw_full[6], raw_empty[6];
   uint64_t s_full[2], p_ready[2], pv_done, o_full, q_ready, q_free, drained;
   uint32_t tmem;
-  int dead, wait_us;  // side by side: bar_wait
+  int dead[2];  // whether a wait gave up; the microseconds after which one does
   int failed;  // the pair's products stopped before their end: `drained` follows
   Start start;
   int large;             // first segment with large q8 values, INT_MAX: none; the same in both blocks of a pair
@@ -546,7 +547,7 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
   const int rank = CG == 2 ? static_cast<int>(blockIdx.x & 1) : 0;
   const int worker = blockIdx.x / CG;
-  volatile int* const dead = &ms.dead;
+  volatile int* const dead = ms.dead;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
   auto wait1 = [&](uint64_t& b, uint32_t parity) { return bar_wait(smem_u32(&b), parity, dead); };
   auto wait = [&](uint64_t& b, uint32_t parity) { return __all_sync(0xffffffffu, wait1(b, parity)) != 0; };  // whole warps
@@ -1290,8 +1291,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bar_init(bar(ms.q_ready), CG * kPrep + (static_cast<int>(blockIdx.x / CG) == a.skip));  // (an arrival that never comes)
     bar_init(bar(ms.q_free), 1);
     bar_init(bar(ms.drained), 1);
-    ms.dead = (smem_u32(smem) & 1023u) != 0;  // (the swizzled tiles need the alignment)
-    ms.wait_us = a.wait_us;
+    ms.dead[0] = (smem_u32(smem) & 1023u) != 0;  // (the swizzled tiles need the alignment)
+    ms.dead[1] = a.wait_us;
     ms.failed = 0;
     for (int i = 0; i < 4; ++i) ms.flag[i] = 0;
     ms.large = INT_MAX;
