@@ -84,6 +84,11 @@ extern "C" mk_status mk_debug_attend_wait(int32_t wait_us, int32_t skip_worker) 
 }
 
 extern "C" mk_status mk_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, const mk_attend_args* a, void* stream) {
+  return mk_attend_tree(pool, rows, a, nullptr, stream);
+}
+
+extern "C" mk_status mk_attend_tree(const mk_kv_pool* pool, const mk_kv_rows* rows, const mk_attend_args* a, const int32_t* parents,
+                                    void* stream) {
   using namespace mk::ops;
   if (!a) return MK_ERR_INVALID;
   const mk_status st = check_attend(pool, rows, a->hq);
@@ -109,6 +114,7 @@ extern "C" mk_status mk_attend(const mk_kv_pool* pool, const mk_kv_rows* rows, c
   p.G = a->hq / pool->hkv;
   p.g_inv = (1 << 20) / p.G + 1;
   p.dtype = a->dtype;
+  p.parents = parents;
   // a window beyond every length is none, and keeps the positions' arithmetic in range
   p.window = a->window >= rows->table_stride * kPage ? 0 : a->window;
   p.sinks = p.window ? a->sinks : 0;

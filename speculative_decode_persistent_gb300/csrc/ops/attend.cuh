@@ -103,6 +103,7 @@ struct AttendParams {
   int hq, G, g_inv, dtype, window, sinks, workers;  // g_inv = 2^20 / G + 1: x / G = x g_inv >> 20 for x < 2^20 / G
   float c;         // scale x log2(e)
   int vq, vo, vg;  // 16-byte access to q, out, gate (out: 2 with 32 bytes)
+  const int32_t* parents;  // the rows are nodes of trees: their parents; NULL: consecutive tokens
   int skip;        // test hook: the worker whose queries are not handed over, -1: none
   int wait_us;     // after which a wait gives up
   JoinInfo* join;  // [kMaxWorkers]
@@ -115,13 +116,14 @@ struct AttendParams {
 struct Tile {
   int rows;         // valid rows
   int t0, h0;       // token (within the new rows) and head (within the group) of the first row
-  int p0, p1;       // positions of its first and last token
+  int p0, p1;       // slots of its first and last token
+  int pf;           // every row sees the tokens up to here (a window aside)
   int nblk;         // 128-token blocks some row may see, at least 1
   int sink_b, lo;   // block i is i < sink_b ? i : lo + i - sink_b
   __device__ __forceinline__ int block(int i) const { return i < sink_b ? i : lo + i - sink_b; }
 };
 __device__ __forceinline__ int tiles_of(const SeqView& v, int G, int M) { return (v.q_len * G + M - 1) / M; }
-__device__ __forceinline__ Tile make_tile(const SeqView& v, int G, int M, int mt, int window, int sinks) {
+__device__ __forceinline__ Tile make_tile(const SeqView& v, int G, int M, int mt, int window, int sinks, bool tree) {
   Tile t;
   const int R0 = mt * M, R1 = min(R0 + M, v.q_len * G);
   t.rows = R1 - R0;
@@ -129,12 +131,13 @@ __device__ __forceinline__ Tile make_tile(const SeqView& v, int G, int M, int mt
   t.h0 = R0 - t.t0 * G;
   t.p0 = v.kv_len - v.q_len + t.t0;
   t.p1 = v.kv_len - v.q_len + (R1 - 1) / G;
+  t.pf = tree ? v.kv_len - v.q_len - 1 : t.p0;
   t.sink_b = t.lo = 0;
   t.nblk = 1;
   if (t.p1 >= 0) {
     const int hi = t.p1 / kBN;
     if (window > 0) {
-      t.lo = max(0, t.p0 - window + 1) / kBN;
+      t.lo = max(0, (tree ? t.pf + 1 : t.p0) - window + 1) / kBN;  // (a node's position is at least the tree's first slot)
       t.sink_b = (min(sinks, t.p1 + 1) + kBN - 1) / kBN;
       if (t.sink_b >= t.lo) t.lo = t.sink_b = 0;
     }
@@ -161,6 +164,25 @@ __device__ __forceinline__ uint32_t seen_bits(int p, int base, int window, int s
   uint32_t m = low_bits(p - base + 1);
   if (window > 0) m &= ~low_bits(p - window + 1 - base) | low_bits(sinks - base);
   return m;
+}
+
+// The same for node `node` of a tree whose nodes lie in slots tree0 on: tokens base .. base+63. A node's position is
+// tree0 plus its depth, at most its slot. A function of its own: inlined, its registers would be the softmax's.
+static __device__ __noinline__ uint64_t seen_tree(const int32_t* parents, int node, int tree0, int base, int window, int sinks) {
+  uint32_t lo = low_bits(tree0 - base), hi = low_bits(tree0 - base - 32);
+  if (tree0 + node < 0) return 0;  // (a row without a slot)
+  int depth = 0;
+  if (window > 0) {
+    for (int n = parent_of(parents, node); n >= 0; n = parent_of(parents, n)) ++depth;
+    const int first = tree0 + depth - window + 1;
+    lo &= ~low_bits(first - base) | low_bits(sinks - base);
+    hi &= ~low_bits(first - base - 32) | low_bits(sinks - base - 32);
+  }
+  for (int n = node, d = 0; n >= 0 && tree0 + n >= base; n = parent_of(parents, n), ++d) {
+    const int at = tree0 + n - base;
+    if (at < 64 && (window <= 0 || d < window || tree0 + depth - d < sinks)) (at < 32 ? lo : hi) |= 1u << (at & 31);
+  }
+  return static_cast<uint64_t>(hi) << 32 | lo;
 }
 
 // A q8 token is large when one of its 2 NS scales is 512 or more (infinite and NaN ones too): 128 times it, the
@@ -225,7 +247,7 @@ struct Walk {
       }
     }
     ++seg;
-    t = make_tile(v, a->G, M, mt, a->window, a->sinks);
+    t = make_tile(v, a->G, M, mt, a->window, a->sinks, a->parents != nullptr);
     b0 = max(0, off - item_cost(M));
     b1 = min(t.nblk, max(0, off + left - item_cost(M)));
     left -= t.nblk + item_cost(M) - off;
@@ -383,7 +405,7 @@ __device__ void find_start(const AttendParams& a, int* scratch, Start* out, int 
     const int n = tiles_of(v, a.G, M);
     int sum = n <= kFew ? 0 : -1;
     for (int mt = 0; mt < min(n, kFew) && sum >= 0; ++mt)
-      sum += make_tile(v, a.G, M, mt, a.window, a.sinks).nblk + item_cost(M);
+      sum += make_tile(v, a.G, M, mt, a.window, a.sinks, a.parents != nullptr).nblk + item_cost(M);
     scratch[s] = sum;
     many |= sum < 0;
   }
@@ -393,7 +415,7 @@ __device__ void find_start(const AttendParams& a, int* scratch, Start* out, int 
       const SeqView v = seq_view(a.rows, s);
       const int n = tiles_of(v, a.G, M);
       int sum = 0;
-      for (int mt = lane; mt < n; mt += 32) sum += make_tile(v, a.G, M, mt, a.window, a.sinks).nblk + item_cost(M);
+      for (int mt = lane; mt < n; mt += 32) sum += make_tile(v, a.G, M, mt, a.window, a.sinks, a.parents != nullptr).nblk + item_cost(M);
       sum = warp_sum(sum);
       __syncwarp();
       if (lane == 0) scratch[s] = sum;
@@ -439,7 +461,7 @@ __device__ void find_start(const AttendParams& a, int* scratch, Start* out, int 
       if (lane == 0) out->n = 0;
       return;
     }
-    const int nb = mt + lane < n_mt ? make_tile(v, a.G, M, mt + lane, a.window, a.sinks).nblk + item_cost(M) : 0;
+    const int nb = mt + lane < n_mt ? make_tile(v, a.G, M, mt + lane, a.window, a.sinks, a.parents != nullptr).nblk + item_cost(M) : 0;
     const int inc = warp_scan(nb, lane);
     const uint32_t hit = __ballot_sync(0xffffffffu, g0 < at + inc && nb > 0);
     if (hit) {
@@ -801,7 +823,7 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
       const int base_p = wk.v.kv_len - wk.v.q_len, last = wk.t.rows - 1;
       const RowOf at = row_of(wk.t, min(r, last), a.G, a.g_inv);
       const int p = base_p + at.tok;
-      const int wp0 = base_p + row_of(wk.t, min(r_warp, last), a.G, a.g_inv).tok;
+      const int wp0 = a.parents ? wk.t.pf : base_p + row_of(wk.t, min(r_warp, last), a.G, a.g_inv).tok;
       const int wp1 = base_p + row_of(wk.t, min(r_warp + 31, last), a.G, a.g_inv).tok;
       float m = valid ? -INFINITY : 0.f, l = 0.f, c = 0.f;
       int pages = lane < 4 ? wk.entry(wk.t.block(wk.b0), 4 * half + lane) : 0;
@@ -834,8 +856,14 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
           uint32_t sx = 0xffffffffu, sy = 0xffffffffu;
           const bool part = gone || !block_full(b, wp0, wp1, a.window, a.sinks);
           if (part) {
-            sx = seen_bits(p, b * kBN + 64 * half, a.window, a.sinks);
-            sy = seen_bits(p, b * kBN + 64 * half + 32, a.window, a.sinks);
+            if (a.parents) {
+              const uint64_t seen = seen_tree(a.parents + wk.v.r0, at.tok, base_p, b * kBN + 64 * half, a.window, a.sinks);
+              sx = static_cast<uint32_t>(seen);
+              sy = static_cast<uint32_t>(seen >> 32);
+            } else {
+              sx = seen_bits(p, b * kBN + 64 * half, a.window, a.sinks);
+              sy = seen_bits(p, b * kBN + 64 * half + 32, a.window, a.sinks);
+            }
             if (gone & 1) sx &= 0xffff0000u;
             if (gone & 2) sx &= 0x0000ffffu;
             if (gone & 4) sy &= 0xffff0000u;
@@ -957,9 +985,12 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
           // rows that see a cleared value add it: +-inf or NaN whatever its weight
           for (int i = wk.b0; i < wk.b1; ++i) {
             const int b = wk.t.block(i);
+            uint64_t tree = 0;
             for (int t = 0; t < kBN; ++t) {
+              if (a.parents && t % 64 == 0) tree = seen_tree(a.parents + wk.v.r0, at.tok, base_p, b * kBN + t, a.window, a.sinks);
               const int pg = wk.entry(b, t / kPage);
-              if (!wk.has_page(pg) || !(seen_bits(p, b * kBN + (t & ~31), a.window, a.sinks) >> (t & 31) & 1)) continue;
+              const bool seen = a.parents ? tree >> (t & 63) & 1 : seen_bits(p, b * kBN + (t & ~31), a.window, a.sinks) >> (t & 31) & 1;
+              if (!wk.has_page(pg) || !seen) continue;
               const int64_t e = ((static_cast<int64_t>(pg) * a.pool.hkv + wk.h) * kPage + t % kPage) * DH + 32 * k;
               if (Q8) {
                 const float d = __half2float(static_cast<const __half*>(a.pool.v_scale)[e / 32]);
@@ -1014,7 +1045,7 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
       const int key0 = CG == 2 ? (kv ? 0 : 64 * rank) : (kv ? u * C::kKeysV : 0);
       uint8_t* const dst = ring + slot * C::kSlot;
       bool found = false;
-      const bool partly = kv && !block_full(b, wk.t.p0, wk.t.p1, a.window, a.sinks);
+      const bool partly = kv && !block_full(b, wk.t.pf, wk.t.p1, a.window, a.sinks);
       if constexpr (!Q8) {
         if (!wait(ms.full[slot], phase)) return false;
         if (partly) {

@@ -37,6 +37,16 @@ inline mk_status check_rows(const mk_kv_rows* r) {
   return MK_OK;
 }
 
+inline mk_status check_layers(const mk_kv_layers* l) {
+  if (!l) return MK_ERR_INVALID;
+  const mk_status st = check_pool(&l->pool);
+  if (st != MK_OK) return st;
+  const int64_t layer = static_cast<int64_t>(l->pool.n_pages) * l->pool.hkv * kPage * l->pool.dh;
+  // (a multiple of 256 elements keeps every layer's scales on 16 bytes)
+  if (l->n_layers <= 0 || (l->n_layers > 1 && (l->layer_stride < layer || l->layer_stride % 256))) return MK_ERR_INVALID;
+  return l->n_layers > 65535 ? MK_ERR_UNSUPPORTED : MK_OK;
+}
+
 inline int elem_bytes(int dtype) { return dtype == MK_F32 ? 4 : 2; }
 
 // Whether eight elements can be moved with 16-byte accesses.
@@ -59,21 +69,37 @@ __device__ __forceinline__ SeqView seq_view(const mk_kv_rows& m, int s) {
   return v;
 }
 
-// Token row (page * 16 + slot) of dense row r, -1 when it has none, -2 when r
-// belongs to no sequence. The sequence is the first whose end lies behind r.
-__device__ __forceinline__ int token_row(const mk_kv_rows& m, int n_pages, int r) {
+// Token row (page * 16 + slot) of position pos of sequence s, -1 when it has none.
+__device__ __forceinline__ int token_at(const mk_kv_rows& m, int n_pages, int s, int pos) {
+  if (pos < 0 || pos >= m.table_stride * kPage) return -1;
+  const int page = __ldg(m.tables + static_cast<int64_t>(s) * m.table_stride + pos / kPage);
+  return page >= 0 && page < n_pages ? page * kPage + pos % kPage : -1;
+}
+
+// Sequence of dense row r, the first whose end lies behind r, and its view; -1 when r belongs to none.
+__device__ __forceinline__ int seq_of_row(const mk_kv_rows& m, int r, SeqView& v) {
   int lo = 0, hi = m.n_seqs;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (__ldg(m.row_start + mid + 1) > r) hi = mid; else lo = mid + 1;
   }
-  if (lo >= m.n_seqs) return -2;
-  const SeqView v = seq_view(m, lo);
-  if (r < v.r0 || r >= v.r0 + v.q_len) return -2;
-  const int pos = v.kv_len - v.q_len + (r - v.r0);
-  if (pos < 0) return -1;
-  const int page = __ldg(m.tables + static_cast<int64_t>(lo) * m.table_stride + pos / kPage);
-  return page >= 0 && page < n_pages ? page * kPage + pos % kPage : -1;
+  if (lo >= m.n_seqs) return -1;
+  v = seq_view(m, lo);
+  return r < v.r0 || r >= v.r0 + v.q_len ? -1 : lo;
+}
+
+// Token row of dense row r, -1 when it has none, -2 when r belongs to no sequence.
+__device__ __forceinline__ int token_row(const mk_kv_rows& m, int n_pages, int r) {
+  SeqView v;
+  const int s = seq_of_row(m, r, v);
+  return s < 0 ? -2 : token_at(m, n_pages, s, v.kv_len - v.q_len + (r - v.r0));
+}
+
+// A node's parent in a tree of drafts (parents: of its sequence's rows), -1 for none: only a node before it can be one,
+// so every walk towards the root ends.
+__device__ __forceinline__ int parent_of(const int32_t* parents, int node) {
+  const int p = __ldg(parents + node);
+  return p >= 0 && p < node ? p : -1;
 }
 
 // ------------------------------------------------------------- eight values

@@ -1,0 +1,219 @@
+// Greedy verification of a tree of drafts.
+//
+// Each node's greedy token g is the argmax of its logits (the lowest index where
+// several are largest). The path starts at a sequence's first row and goes on to the
+// lowest child whose draft token is g of the node it has reached. Children lie behind
+// their parents, so one scan of the nodes finds it.
+//
+// Two launches: tree_top takes the maximum of a row's part per block, tree_walk (launched
+// early) joins the parts and walks, a block per sequence. Bound by the logits' bytes when
+// the vocabulary is large, by the two launches when it is small.
+#include <climits>
+
+#include <cuda_runtime.h>
+
+#include "ops_internal.cuh"
+
+namespace mk {
+namespace ops {
+namespace {
+
+constexpr int kBlock = 256;
+constexpr int kMaxSplit = 128;  // parts of a row
+constexpr int kSpan = 2048;     // a part is a multiple of so many logits
+
+// A logit and its index as one number that grows with the logit and falls with the
+// index; a NaN is above every number.
+constexpr uint64_t kNan = ~0ull;
+__device__ __forceinline__ uint64_t key_of(float x, int i) {
+  const uint32_t b = __float_as_uint(x == 0.f ? 0.f : x);  // (-0 is 0)
+  return static_cast<uint64_t>(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | (0xffffffffu - static_cast<uint32_t>(i));
+}
+__device__ __forceinline__ int token_of(uint64_t key) {
+  return key == kNan || key == 0 ? -1 : static_cast<int>(0xffffffffu - static_cast<uint32_t>(key));
+}
+__device__ __forceinline__ uint64_t warp_max(uint64_t k) {
+#pragma unroll
+  for (int m = 16; m; m >>= 1) {
+    const uint64_t o = __shfl_xor_sync(0xffffffffu, k, m);
+    k = o > k ? o : k;
+  }
+  return k;
+}
+
+struct TreeArgs {
+  mk_kv_rows rows;
+  const int32_t* parents;
+  const int32_t* tokens;
+  const void* logits;
+  int64_t row_stride;
+  int vocab, split, span;  // parts of a row, logits of a part
+  int32_t* path;
+  int32_t* count;
+  int32_t* emitted;
+  uint64_t* part;  // [rows][split]
+  int32_t* greedy;  // [rows]
+};
+
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kBlock) tree_top(const __grid_constant__ TreeArgs a) {
+  using T = typename Elem<DT>::T;
+  __shared__ uint64_t top[kBlock / 32];
+  for (int row = blockIdx.y; row < a.rows.n_rows; row += gridDim.y) {
+    const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
+    const int end = min(a.vocab, (static_cast<int>(blockIdx.x) + 1) * a.span);
+    float best = -INFINITY;
+    int at = INT_MAX;
+    bool nan = false;
+    auto see = [&](float y, int i) {
+      if (!(y <= best)) {  // larger, or a NaN
+        nan |= y != y;
+        best = y;
+        at = i;
+      }
+    };
+    // ascending, eight at a time: the first of equal ones stays
+    int i = static_cast<int>(blockIdx.x) * a.span + threadIdx.x * 8;
+    const int i0 = i;
+    constexpr int kStep = kBlock * 8;
+    auto eight = [&](int j) {
+      float y[8];
+      load8<DT, VEC>(x + j, y);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) see(y[k], j + k);
+    };
+    for (; i + 3 * kStep + 8 <= end; i += 4 * kStep) {
+      float y[4][8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) load8<DT, VEC>(x + i + u * kStep, y[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) see(y[u][k], i + u * kStep + k);
+    }
+    for (; i + 8 <= end; i += kStep) eight(i);
+    for (; i < end; ++i) see(Elem<DT>::get(x[i]), i);
+    uint64_t key = nan ? kNan : at != INT_MAX ? key_of(best, at) : i0 < end ? key_of(-INFINITY, i0) : 0;
+    key = warp_max(key);
+    if ((threadIdx.x & 31) == 0) top[threadIdx.x / 32] = key;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      key = warp_max(threadIdx.x < kBlock / 32 ? top[threadIdx.x] : 0);
+      if (threadIdx.x == 0) a.part[static_cast<int64_t>(row) * a.split + blockIdx.x] = key;
+    }
+    __syncthreads();
+  }
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+
+__global__ void __launch_bounds__(kBlock) tree_walk(const __grid_constant__ TreeArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const SeqView v = seq_view(a.rows, blockIdx.x);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there from here on
+  for (int j = warp; j < v.q_len; j += kBlock / 32) {
+    uint64_t key = 0;
+    for (int p = lane; p < a.split; p += 32) {
+      const uint64_t o = a.part[static_cast<int64_t>(v.r0 + j) * a.split + p];
+      key = o > key ? o : key;
+    }
+    key = warp_max(key);
+    if (lane == 0) a.greedy[v.r0 + j] = token_of(key);
+  }
+  __syncthreads();
+  if (warp) return;
+  int count = 0, cur = 0, want = -1;
+  auto reach = [&](int node) {
+    cur = node;
+    want = a.greedy[v.r0 + node];
+    if (lane == 0) {
+      a.path[v.r0 + count] = node;
+      a.emitted[v.r0 + count] = want;
+    }
+    ++count;
+  };
+  if (v.q_len) reach(0);
+  for (int j0 = 1; j0 < v.q_len; j0 += 32) {
+    const int j = j0 + lane;
+    int parent = -1, tok = -1;
+    if (j < v.q_len) {
+      parent = a.parents ? parent_of(a.parents + v.r0, j) : j - 1;
+      tok = __ldg(a.tokens + v.r0 + j);
+    }
+    for (;;) {  // (each hit lies behind the one before: no more than 32)
+      const uint32_t hit = __ballot_sync(0xffffffffu, j < v.q_len && parent == cur && want >= 0 && tok == want);
+      if (!hit) break;
+      reach(j0 + __ffs(hit) - 1);
+    }
+  }
+  for (int j = count + lane; j < v.q_len; j += 32) {
+    a.path[v.r0 + j] = -1;
+    a.emitted[v.r0 + j] = -1;
+  }
+  if (lane == 0) a.count[blockIdx.x] = count;
+}
+
+// Parts of a row: about four blocks an SM over all rows, each of at least kSpan logits.
+int split_of(int n_rows, int vocab) {
+  const int64_t most = (static_cast<int64_t>(vocab) + kSpan - 1) / kSpan, want = (608 + n_rows - 1) / (n_rows > 0 ? n_rows : 1);
+  const int64_t n = want < most ? want : most;
+  return static_cast<int>(n < 1 ? 1 : n > kMaxSplit ? kMaxSplit : n);
+}
+int64_t part_bytes(int n_rows, int vocab) { return (static_cast<int64_t>(n_rows) * split_of(n_rows, vocab) * 8 + 255) / 256 * 256; }
+
+template <int DT>
+cudaError_t launch(const TreeArgs& a, bool vec, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.split, a.rows.n_rows < 65535 ? a.rows.n_rows : 65535);
+  cfg.blockDim = dim3(kBlock);
+  cfg.stream = stream;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, vec ? tree_top<DT, true> : tree_top<DT, false>, a);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(a.rows.n_seqs);
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_walk, a);
+}
+
+}  // namespace
+}  // namespace ops
+}  // namespace mk
+
+extern "C" size_t mk_tree_work_bytes(int32_t n_rows, int32_t vocab) {
+  if (n_rows < 0 || vocab <= 0 || vocab > (1 << 30)) return 0;
+  return static_cast<size_t>(mk::ops::part_bytes(n_rows, vocab)) + static_cast<size_t>(n_rows) * 4 + 256;
+}
+
+extern "C" mk_status mk_tree_accept(const mk_kv_rows* rows, const mk_tree_args* t, void* stream) {
+  using namespace mk::ops;
+  const mk_status st = check_rows(rows);
+  if (st != MK_OK) return st;
+  if (!t || t->vocab <= 0 || t->dtype < MK_F32 || t->dtype > MK_BF16) return MK_ERR_INVALID;
+  if (t->vocab > (1 << 30)) return MK_ERR_UNSUPPORTED;  // (indices of a row's parts stay within 32 bits)
+  if (rows->n_seqs == 0) return MK_OK;
+  if (!t->count) return MK_ERR_INVALID;
+  if (rows->n_rows > 0) {
+    if (!t->tokens || !t->logits || !t->path || !t->emitted || (reinterpret_cast<uintptr_t>(t->logits) & (elem_bytes(t->dtype) - 1)))
+      return MK_ERR_INVALID;
+    if (!t->work || (reinterpret_cast<uintptr_t>(t->work) & 255u) || t->work_bytes < mk_tree_work_bytes(rows->n_rows, t->vocab))
+      return MK_ERR_INVALID;
+  }
+  TreeArgs a{*rows, t->parents, t->tokens, t->logits, t->row_stride, t->vocab, 1, 0, t->path, t->count, t->emitted, nullptr, nullptr};
+  a.split = split_of(rows->n_rows, t->vocab);
+  a.span = static_cast<int>(((static_cast<int64_t>(t->vocab) + a.split - 1) / a.split + 7) / 8 * 8);
+  a.part = static_cast<uint64_t*>(t->work);
+  a.greedy = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(t->work) + part_bytes(rows->n_rows, t->vocab));
+  const bool vec = dense_vec(mk_dense{const_cast<void*>(t->logits), t->row_stride, 0}, t->dtype);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (rows->n_rows == 0) {  // no path anywhere
+    e = cudaMemsetAsync(t->count, 0, sizeof(int32_t) * rows->n_seqs, s);
+  } else {
+    e = t->dtype == MK_F32 ? launch<MK_F32>(a, vec, s) : t->dtype == MK_F16 ? launch<MK_F16>(a, vec, s) : launch<MK_BF16>(a, vec, s);
+  }
+  if (e == cudaSuccess) return MK_OK;
+  cudaGetLastError();
+  return MK_ERR_CUDA;
+}

@@ -327,7 +327,11 @@ class Engine:
         if len(free) < n:
             raise MkError(-3, "clone_sequence (no free pages)")
         new = np.array(free[:n], np.int32)
-        if n:
+        if n and src != dst:
+            from . import ops
+            self._before_current()
+            ops.kv_copy(self.kv_layers(), *(torch.from_numpy(a.astype(np.int32)).to(self.device) for a in (info["pages"], new)))
+        elif n:  # onto pages that may be its own: all are read before one is written
             si = torch.as_tensor(info["pages"].astype(np.int64), device=self.device)
             di = torch.as_tensor(new.astype(np.int64), device=self.device)
             for v in self.kv_views().values():  # [kv layers][pages][...]
@@ -349,6 +353,38 @@ class Engine:
         if not 0 <= layer < views[names[0]].shape[0]:
             raise MkError(-1, "kv_pool (layer)")
         return ops.KVPool(*(views[n][layer] for n in names))
+
+    def kv_layers(self):
+        """All KV layers of the pool as an ops.KVLayers: for ops.kv_copy, kv_keep."""
+        from . import ops
+        views = self.kv_views()
+        return ops.KVLayers(*(views[n] for n in (("kq", "vq", "ks", "vs") if self.layout.kv_dtype == MK_KV_Q8 else ("k", "v"))))
+
+    def seq_keep(self, seq: int, new_rows: int, keep):
+        """Keep some of a committed sequence's last new_rows cached tokens (the
+        accepted path of a tree of drafts, say): keep lists them, ascending,
+        as indices among those rows; they move up behind the tokens before, in
+        all KV layers, the length shrinks, and pages wholly behind it return to
+        the pool. The committed recurrent state stays what it is; a pending
+        step is dropped. Returns the new length."""
+        from . import ops
+        torch = self.torch
+        info = self.seq_get(seq)
+        new_rows, keep = int(new_rows), [int(k) for k in keep]
+        if not 0 <= new_rows <= info["length"] or any(not a < b < new_rows for a, b in zip([-1] + keep, keep)):
+            raise MkError(-1, "seq_keep (0 to length rows, ascending indices among them)")
+        length = info["length"] - new_rows + len(keep)
+        if new_rows:
+            self._before_current()
+            rows = self.seq_rows([seq], [new_rows])
+            entries = torch.tensor(keep + [-1] * (new_rows - len(keep)), dtype=torch.int32, device=self.device)
+            ops.kv_keep(self.kv_layers(), rows, entries)
+        Sv, Cv = self.state_views()
+        if Sv is not None and info["slot"]:
+            Sv[seq, 0].copy_(Sv[seq, info["slot"]])
+            Cv[seq, 0].copy_(Cv[seq, info["slot"]])
+        self.seq_set(seq, length, info["pages"][:-(-length // 16)])
+        return length
 
     def seq_rows(self, seqs, new_rows):
         """ops.KVRows of committed sequences: the last new_rows[i] cached
@@ -444,15 +480,16 @@ class Engine:
         if current != self.stream:
             self.stream.wait_stream(current)
 
-    def attend(self, layer: int, q, seqs, new_rows, window: int = 0, sinks: int = 0, gate=None, out=None):
+    def attend(self, layer: int, q, seqs, new_rows, window: int = 0, sinks: int = 0, gate=None, out=None, parents=None):
         """Attention of the last new_rows[i] cached tokens of each seqs[i]
-        over KV layer `layer` (ops.attend): q [sum of new_rows][fa_hq][fa_dh]."""
+        over KV layer `layer` (ops.attend; with parents they are trees of
+        drafts): q [sum of new_rows][fa_hq][fa_dh]."""
         from . import ops
         if q.dim() != 3 or q.shape[1] != self.layout.fa_hq:
             raise MkError(-1, "attend (q [rows][query heads][head dim])")
         self._before_current()
         out = ops.attend(self.kv_pool(layer), self.seq_rows(seqs, new_rows), q, window=window, sinks=sinks, gate=gate,
-                         out=out)
+                         out=out, parents=parents)
         self._after_current()
         return out
 

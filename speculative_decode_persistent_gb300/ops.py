@@ -1,14 +1,24 @@
-"""Operators on one attention layer of the paged KV pool, outside the fused
-step (include/mk_ops.h): kv_write stores new rows (rounded, or quantised),
-kv_read gathers rows back, attend runs the attention of a chunk of new rows
-over the cached tokens. Like the engine binding this is argument marshalling
-only; the work runs in the CUDA library, on the current torch stream of the
-tensors' device, without waiting, so calls can be captured into CUDA graphs.
+"""Operators on the paged KV pool, outside the fused step (include/mk_ops.h):
+kv_write stores new rows of one layer (rounded, or quantised), rope_write does
+so behind the heads' norm and the position rotation, kv_read gathers rows back,
+attend runs the attention of new rows over the cached tokens, tree_accept
+verifies a tree of drafts greedily, kv_keep keeps some of a sequence's tokens in
+all layers, kv_copy copies pages. Like the engine binding this is argument
+marshalling only; the work runs in the CUDA library, on the current torch stream
+of the tensors' device, without waiting, so calls can be captured into CUDA graphs.
 
     pool = KVPool(k, v)                      # one layer; Engine.kv_pool(layer) gives an engine's
     rows = KVRows(row_start, kv_len, tables) # which rows of the dense tensors are whose
     kv_write(pool, rows, new_k, new_v)       # [rows][kv heads][head dim]
     out = attend(pool, rows, q)              # [rows][query heads][head dim]
+
+A step over trees of drafts, whose nodes are the rows:
+
+    rope = Rope(dims, base, q_gain, k_gain)                        # once per layer
+    q = rope_write(pool, rows, rope, q, k, v, parents=parents)     # in each layer
+    out = attend(pool, rows, q, parents=parents)
+    path, count, emitted = tree_accept(rows, parents, tokens, logits)
+    kv_len = kv_keep(KVLayers(k, v), rows, path)                   # in all layers at once
 
 The new rows of a sequence are the LAST of its kv_len tokens: kv_len counts
 them. Errors are MkError, as everywhere in the package.
@@ -50,28 +60,58 @@ class mk_attend_args(ctypes.Structure):
                 ("window", i32), ("sinks", i32), ("work", vp), ("work_bytes", u64)]
 
 
+class mk_rope(ctypes.Structure):
+    _fields_ = [("turns", vp), ("q_gain", vp), ("k_gain", vp), ("rot", i32), ("eps", f32)]
+
+
+class mk_rope_args(ctypes.Structure):
+    _fields_ = [("q", mk_dense), ("out", mk_dense), ("k", mk_dense), ("v", mk_dense), ("hq", i32), ("dtype", i32),
+                ("rope", mk_rope), ("parents", vp), ("positions", vp)]
+
+
+class mk_tree_args(ctypes.Structure):
+    _fields_ = [("parents", vp), ("tokens", vp), ("logits", vp), ("row_stride", i64), ("vocab", i32), ("dtype", i32),
+                ("path", vp), ("count", vp), ("emitted", vp), ("work", vp), ("work_bytes", u64)]
+
+
+class mk_kv_layers(ctypes.Structure):
+    _fields_ = [("pool", mk_kv_pool), ("n_layers", i32), ("layer_stride", i64)]
+
+
 _P = ctypes.POINTER
 for _name, _res, _args in (
         ("mk_kv_write", i32, [_P(mk_kv_pool), _P(mk_kv_rows), _P(mk_dense), _P(mk_dense), i32, vp]),
         ("mk_kv_read", i32, [_P(mk_kv_pool), _P(mk_kv_rows), _P(mk_dense), _P(mk_dense), i32, vp]),
         ("mk_attend_work_bytes", sz, [_P(mk_kv_pool), _P(mk_kv_rows), i32]),
         ("mk_attend", i32, [_P(mk_kv_pool), _P(mk_kv_rows), _P(mk_attend_args), vp]),
+        ("mk_attend_tree", i32, [_P(mk_kv_pool), _P(mk_kv_rows), _P(mk_attend_args), vp, vp]),
+        ("mk_rope_turns", i32, [i32, ctypes.c_double, vp, vp]),
+        ("mk_rope_write", i32, [_P(mk_kv_pool), _P(mk_kv_rows), _P(mk_rope_args), vp]),
+        ("mk_tree_work_bytes", sz, [i32, i32]),
+        ("mk_tree_accept", i32, [_P(mk_kv_rows), _P(mk_tree_args), vp]),
+        ("mk_kv_copy", i32, [_P(mk_kv_layers), vp, vp, i32, vp]),
+        ("mk_kv_keep", i32, [_P(mk_kv_layers), _P(mk_kv_rows), vp, vp, vp]),
         ("mk_debug_attend_wait", i32, [i32, i32])):
     _fn = getattr(lib, _name)
     _fn.restype, _fn.argtypes = _res, _args
-EXPORTS = ["mk_kv_write", "mk_kv_read", "mk_attend_work_bytes", "mk_attend", "mk_debug_attend_wait"]
+EXPORTS = ["mk_kv_write", "mk_kv_read", "mk_attend_work_bytes", "mk_attend", "mk_attend_tree", "mk_rope_turns", "mk_rope_write",
+           "mk_tree_work_bytes", "mk_tree_accept", "mk_kv_copy", "mk_kv_keep", "mk_debug_attend_wait"]
 
 # The calls below pass the structs as packed bytes, which costs a few hundred
 # nanoseconds less a field than ctypes structures: a small call is bound by
 # this file, not by the GPU.
 _fast = ctypes.CDLL(LIB_PATH)
-for _name, _n in (("mk_kv_write", 4), ("mk_kv_read", 4), ("mk_attend", 3)):
+for _name, _args in (("mk_kv_write", [vp] * 4 + [i32, vp]), ("mk_kv_read", [vp] * 4 + [i32, vp]), ("mk_attend_tree", [vp] * 5),
+                     ("mk_rope_write", [vp] * 4), ("mk_tree_accept", [vp] * 3), ("mk_kv_copy", [vp] * 3 + [i32, vp]),
+                     ("mk_kv_keep", [vp] * 5)):
     _fn = getattr(_fast, _name)
-    _fn.restype, _fn.argtypes = i32, [vp] * _n + ([i32] if _n == 4 else []) + [vp]
-_kv_write, _kv_read, _attend = _fast.mk_kv_write, _fast.mk_kv_read, _fast.mk_attend
-_POOL, _ROWS, _DENSE, _ARGS = (struct.Struct(f).pack for f in ("@4P4i", "@3P4i", "@Pqq", "@PqqPqqPqqiifiiPQ"))
-assert all(struct.calcsize(f) <= ctypes.sizeof(t) for f, t in (
-    ("@4P4i", mk_kv_pool), ("@3P4i", mk_kv_rows), ("@Pqq", mk_dense), ("@PqqPqqPqqiifiiPQ", mk_attend_args)))
+    _fn.restype, _fn.argtypes = i32, _args
+_kv_write, _kv_read, _attend = _fast.mk_kv_write, _fast.mk_kv_read, _fast.mk_attend_tree
+_rope_write, _tree_accept, _kv_copy, _kv_keep = _fast.mk_rope_write, _fast.mk_tree_accept, _fast.mk_kv_copy, _fast.mk_kv_keep
+_FORMATS = (("@4P4i", mk_kv_pool), ("@3P4i", mk_kv_rows), ("@Pqq", mk_dense), ("@PqqPqqPqqiifiiPQ", mk_attend_args),
+            ("@PqqPqqPqqPqqiiPPPifPP", mk_rope_args), ("@PPPqiiPPPPQ", mk_tree_args), ("@4P4iiq", mk_kv_layers))
+_POOL, _ROWS, _DENSE, _ARGS, _ROPE, _TREE, _LAYERS = (struct.Struct(f).pack for f, _ in _FORMATS)
+assert all(struct.calcsize(f) <= ctypes.sizeof(t) for f, t in _FORMATS)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _HALF = (torch.float16, torch.int16)
 
@@ -113,6 +153,74 @@ class KVPool:
                 _refuse("KVPool (binary16, or int8 codes with scales)")
             self.tensors = (k, v)
             self.c = _POOL(k.data_ptr(), v.data_ptr(), 0, 0, MK_KV_F16, self.n_pages, self.hkv, self.dh)
+
+
+class KVLayers:
+    """Layers of a paged pool that have their pages in common: the tensors of
+    KVPool with the layers in front, [layers][pages][kv heads][16][head dim]
+    (a slice of an engine's, say). Each layer is contiguous."""
+
+    __slots__ = ("tensors", "device", "q8", "n_layers", "n_pages", "hkv", "dh", "c")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 5 or k.shape[0] == 0 or v.shape != k.shape:
+            _refuse("KVLayers (k and v are [layers][pages][kv heads][16][head dim] of one type)")
+        n = k.shape[0]
+        scales = [s for s in (k_scale, v_scale) if s is not None]
+        if any(s.dim() != 5 or s.shape[0] != n for s in scales):
+            _refuse("KVLayers (scales [layers][pages][kv heads][16][head dim / 32])")
+        first = KVPool(k[0], v[0], *(None if s is None else s[0] for s in (k_scale, v_scale)))
+        stride = k.stride(0) if n > 1 else 0
+        if n > 1 and (v.stride(0) != stride or any(s.stride(0) * 32 != stride for s in scales) or stride % 256 or
+                      stride < k[0].numel()):
+            _refuse("KVLayers (layers of all tensors equally far apart)")
+        self.tensors = (k, v, k_scale, v_scale)
+        self.device, self.q8, self.n_layers = first.device, first.q8, n
+        self.n_pages, self.hkv, self.dh = first.n_pages, first.hkv, first.dh
+        ks, vs = (0, 0) if not scales else (k_scale.data_ptr(), v_scale.data_ptr())
+        self.c = _LAYERS(k.data_ptr(), v.data_ptr(), ks, vs, MK_KV_Q8 if self.q8 else MK_KV_F16, self.n_pages, self.hkv, self.dh,
+                         n, stride)
+
+
+class Rope:
+    """Rotation of the first `dims` dims of a head by position (a multiple of
+    64; pairs i and i + dims / 2), pair i at freq[i] radians a position
+    (default: base^(-2i / dims)). With q_gain, k_gain (float32 [head dim]) the
+    heads of q, k are first normalised by their root mean square (with eps) and
+    multiplied by it. Made once, on the gains' device or `device`."""
+
+    __slots__ = ("tensors", "device", "dims", "gain", "c")
+
+    def __init__(self, dims: int, base: float = 1e7, q_gain=None, k_gain=None, eps: float = 1e-6, freq=None, device=None):
+        if dims < 0 or dims % 64 or dims > 65536:
+            _refuse("Rope (dims: a multiple of 64)")
+        if not 0.0 <= eps < 3.4e38:
+            _refuse("Rope (eps)")
+        gains = [g for g in (q_gain, k_gain) if g is not None]
+        device = torch.device(device) if device is not None else gains[0].device if gains else torch.device("cuda")
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        for g in gains:
+            if g.dtype != torch.float32 or g.dim() != 1 or not g.is_contiguous() or g.device != device or g.shape != gains[0].shape:
+                _refuse("Rope (gains: contiguous float32 [head dim] on one device)")
+            if g.requires_grad and torch.is_grad_enabled():
+                _refuse("Rope (no gradient is defined: detach the gains or use torch.no_grad)")
+            if g.data_ptr() % 16:
+                _refuse("Rope (gains: 16-byte aligned)")
+        turns = (u64 * max(dims // 2, 1))()
+        if freq is not None:
+            freq = [float(f) for f in freq]
+            if len(freq) != dims // 2:
+                _refuse("Rope (dims / 2 frequencies)")
+            freq = (ctypes.c_double * max(len(freq), 1))(*freq)
+        rc = lib.mk_rope_turns(dims, float(base), freq, turns)
+        if rc != 0:
+            raise MkError(rc, "mk_rope_turns")
+        signed = [t - (1 << 64) if t >> 63 else t for t in turns]
+        table = torch.tensor(signed, dtype=torch.int64).to(device)
+        self.tensors, self.device, self.dims = (table, q_gain, k_gain), device, dims
+        self.gain = gains[0].shape[0] if gains else 0
+        self.c = (table.data_ptr(), *(0 if g is None else g.data_ptr() for g in (q_gain, k_gain)), dims, float(eps))
 
 
 class KVRows:
@@ -196,6 +304,15 @@ def _same(pool: KVPool, rows: KVRows, t, *more):
     return n, device.index
 
 
+def _index(t, n: int, device, what: str) -> int:
+    """Address of a contiguous int32 tensor of n elements (0 for none)."""
+    if t is None:
+        return 0
+    if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.device != device:
+        _refuse(f"{what} (contiguous int32 [{n}] on the pool's device)")
+    return t.data_ptr()
+
+
 def _run(device: int, what: str, fn, *args):
     """fn(*args, stream) with the device current, on its current stream."""
     was = torch._C._cuda_getDevice()
@@ -237,17 +354,52 @@ def kv_read(pool: KVPool, rows: KVRows, dtype=torch.float16, out=None):
     return k, v
 
 
+def rope_write(pool: KVPool, rows: KVRows, rope: Rope, q, k, v, parents=None, positions=None, out=None):
+    """New rows into use in one pass: q [rows][query heads][head dim] and k
+    [rows][kv heads][head dim] normalised (when rope has gains) and rotated by
+    the rows' positions, q into out (made here unless given; it may be q
+    itself; rows of no sequence are left as they are, undefined when it is
+    made here), k and v into the pool as by kv_write. A row's position is
+    positions[row], or that of its slot; for nodes of trees (parents, as for
+    attend) the tree's first position plus the node's depth. All tensors are
+    of one type; q, k, v may be slices of one projection's output. Two rows of
+    one call must not share a slot of the pool. Returns out."""
+    hkv, dh, shape = pool.hkv, pool.dh, q.shape
+    hq = shape[1] if len(shape) == 3 else 0
+    qd = _dense(q, hq, dh, "rope_write q")
+    kd, vd = _dense(k, hkv, dh, "rope_write k"), _dense(v, hkv, dh, "rope_write v")
+    if out is None:
+        n, device = _same(pool, rows, q, k, v)
+        out = torch.empty(shape, dtype=q.dtype, device=pool.device)
+        od = (out.data_ptr(), hq * dh, dh)
+    else:
+        od = _dense(out, hq, dh, "rope_write out", True)
+        n, device = _same(pool, rows, q, k, v, out)
+    if rope.device != pool.device or rope.dims > dh or rope.gain not in (0, dh):
+        _refuse("rope_write (a Rope on the pool's device, of no more dims than a head and gains for all of them)")
+    if parents is not None and positions is not None:
+        _refuse("rope_write (parents or positions)")
+    args = _ROPE(*qd, *od, *kd, *vd, hq, DTYPES[q.dtype], *rope.c, _index(parents, n, pool.device, "rope_write parents"),
+                 _index(positions, n, pool.device, "rope_write positions"))
+    _run(device, "mk_rope_write", _rope_write, pool.c, rows._at(n), args)
+    return out
+
+
 _work_bytes: dict = {}  # of mk_attend_work_bytes, which goes by the head dim alone
 
 
-def attend(pool: KVPool, rows: KVRows, q, scale=None, window: int = 0, sinks: int = 0, gate=None, out=None):
+def attend(pool: KVPool, rows: KVRows, q, scale=None, window: int = 0, sinks: int = 0, gate=None, out=None, parents=None):
     """Attention of the new rows q [rows][query heads][head dim] (float16 or
     bfloat16) over the cached tokens, the rows' own among them (kv_write
     first): causal; with window > 0 a row sees the last `window` tokens and
     the first `sinks` ones. Query heads share kv heads in equal groups, in
     order. scale defaults to 1/sqrt(head dim). With gate (like q) the output
-    is multiplied by sigmoid(gate). A row that sees no token gives 0. Returns
-    out, like q (made here unless given; it may be q or gate itself; rows of
+    is multiplied by sigmoid(gate). A row that sees no token gives 0. With
+    parents (int32 [rows]) the rows of a sequence are the nodes of a tree of
+    drafts: parents[row] is the row's parent, an index into its sequence's rows
+    before its own, or -1 where the node follows the cached tokens directly; a
+    node sees the tokens before the tree, its ancestors and itself, and windows
+    count positions, the tree's first slot plus a node's depth. Returns out, like q (made here unless given; it may be q or gate itself; rows of
     no sequence are left as they are, undefined when it is made here)."""
     shape, dtype, dh = q.shape, q.dtype, pool.dh
     hq = shape[1] if len(shape) == 3 else 0
@@ -275,5 +427,72 @@ def attend(pool: KVPool, rows: KVRows, q, scale=None, window: int = 0, sinks: in
     work = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=pool.device)
     args = _ARGS(*qd, *gd, *od, hq, DTYPES[dtype], scale, window, sinks, work.data_ptr(),
                  work.numel())
-    _run(device, "mk_attend", _attend, pool.c, at, args)
+    _run(device, "mk_attend", _attend, pool.c, at, args, _index(parents, n, pool.device, "attend parents"))
     return out
+
+
+def tree_accept(rows: KVRows, parents, tokens, logits):
+    """Greedy verification of trees of drafts (parents as for attend; None: a
+    chain per sequence): tokens int32 [rows], the nodes' drafts, of which a
+    sequence's first, its last emitted token, stands; logits [rows][vocabulary]
+    (float32, float16 or bfloat16), the model's after each node. Returns int32
+    (path [rows], count [sequences], emitted [rows]): from a sequence's first
+    row on the nodes that the model's greedy choices lead through (the lowest
+    child that agrees) and those choices, the accepted drafts and one token
+    more; -1 behind them; their number. Of equal logits the lowest index
+    counts; a node with a NaN among its logits has the choice -1, and none of its children
+    is accepted. Rows of no sequence are undefined."""
+    if logits.dim() != 2 or logits.dtype not in DTYPES or logits.shape[1] == 0 or logits.stride(1) != 1:
+        _refuse("tree_accept (logits [rows][vocabulary], float32, float16 or bfloat16, a row contiguous)")
+    n, vocab = logits.shape
+    device = rows.device
+    if rows.n_rows is not None and rows.n_rows != n:
+        _refuse("rows of the logits differ from KVRows.n_rows")
+    if device.type != "cuda" or logits.device != device:
+        _refuse("tree_accept (rows and logits on one CUDA device)")
+    if tokens is None:
+        _refuse("tree_accept (tokens)")
+    par, tok = _index(parents, n, device, "tree_accept parents"), _index(tokens, n, device, "tree_accept tokens")
+    out = torch.empty(2 * n + rows.n_seqs, dtype=torch.int32, device=device)
+    path, emitted, count = out[:n], out[n:2 * n], out[2 * n:]
+    nbytes = lib.mk_tree_work_bytes(n, vocab)
+    work = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    at = out.data_ptr()
+    args = _TREE(par, tok, logits.data_ptr(), logits.stride(0), vocab, DTYPES[logits.dtype], at, at + 8 * n, at + 4 * n,
+                 work.data_ptr(), nbytes)
+    _run(device.index, "mk_tree_accept", _tree_accept, rows._at(n), args)
+    return path, count, emitted
+
+
+def kv_copy(layers: KVLayers, src, dst) -> None:
+    """Copy page src[i] to page dst[i] in all layers (int32 tensors of one
+    length). Pairs with an id that is no page are passed over. A page may be
+    copied several times; one that is written must not be another pair's
+    source or target."""
+    if src.dim() != 1:
+        _refuse("kv_copy (int32 [n])")
+    n = src.shape[0]
+    if layers.device.type != "cuda":
+        _refuse("kv_copy (a CUDA device)")
+    _run(layers.device.index, "mk_kv_copy", _kv_copy, layers.c, _index(src, n, layers.device, "kv_copy src"),
+         _index(dst, n, layers.device, "kv_copy dst"), n)
+
+
+def kv_keep(layers: KVLayers, rows: KVRows, keep):
+    """Keep some of each sequence's new rows, in all layers: keep int32 [rows]
+    lists, from a sequence's first row on, indices into its rows, ascending;
+    the first entry that does not ascend (-1, say) ends the list, so that
+    tree_accept's path can be given as it is. Row keep[i] moves, in place, to the
+    i-th slot behind the tokens before the rows. Returns the new lengths, int32
+    [sequences]; the caller frees the pages wholly behind them. Sequences of one
+    call must not share pages that a row moves to."""
+    device = layers.device
+    if device.type != "cuda" or rows.device != device:
+        _refuse("kv_keep (layers and rows on one CUDA device)")
+    if keep.dim() != 1 or rows.n_rows is not None and rows.n_rows != keep.shape[0]:
+        _refuse("kv_keep (an entry per row)")
+    n = keep.shape[0]
+    at = _index(keep, n, device, "kv_keep keep")
+    kv_len = torch.empty(rows.n_seqs, dtype=torch.int32, device=device)
+    _run(device.index, "mk_kv_keep", _kv_keep, layers.c, rows._at(n), at, kv_len.data_ptr())
+    return kv_len
