@@ -10,10 +10,9 @@
 
 namespace mk {
 namespace ops {
-cudaError_t launch_attend_f16(int ns, int cg, const AttendParams& a, const CUtensorMap& tk, const CUtensorMap& tv,
-                              int device, cudaStream_t stream);
-cudaError_t launch_attend_q8(int ns, int cg, const AttendParams& a, const CUtensorMap& tk, const CUtensorMap& tv,
-                             int device, cudaStream_t stream);
+using Launch = cudaError_t(int ns, int cg, const AttendParams& a, const CUtensorMap& tk, const CUtensorMap& tv, int device,
+                           cudaStream_t stream);
+Launch launch_attend_f16, launch_attend_q8, launch_attend_tree_f16, launch_attend_tree_q8;
 
 namespace {
 
@@ -142,7 +141,8 @@ extern "C" mk_status mk_attend_tree(const mk_kv_pool* pool, const mk_kv_rows* ro
   if (cudaGetDevice(&device) != cudaSuccess || !encode_map(&tk, pool->k, *pool, box, slabs_k == 1 ? kPage : 8, slabs_k) ||
       !encode_map(&tv, pool->v, *pool, box, kPage, slabs_v))
     return MK_ERR_CUDA;
-  const cudaError_t e = (q8 ? launch_attend_q8 : launch_attend_f16)(ns, cg, p, tk, tv, device, static_cast<cudaStream_t>(stream));
+  Launch* const launch = parents ? (q8 ? launch_attend_tree_q8 : launch_attend_tree_f16) : q8 ? launch_attend_q8 : launch_attend_f16;
+  const cudaError_t e = launch(ns, cg, p, tk, tv, device, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) {
     cudaGetLastError();
     return MK_ERR_CUDA;

@@ -117,7 +117,6 @@ struct Tile {
   int rows;         // valid rows
   int t0, h0;       // token (within the new rows) and head (within the group) of the first row
   int p0, p1;       // slots of its first and last token
-  int pf;           // every row sees the tokens up to here (a window aside)
   int nblk;         // 128-token blocks some row may see, at least 1
   int sink_b, lo;   // block i is i < sink_b ? i : lo + i - sink_b
   __device__ __forceinline__ int block(int i) const { return i < sink_b ? i : lo + i - sink_b; }
@@ -131,13 +130,12 @@ __device__ __forceinline__ Tile make_tile(const SeqView& v, int G, int M, int mt
   t.h0 = R0 - t.t0 * G;
   t.p0 = v.kv_len - v.q_len + t.t0;
   t.p1 = v.kv_len - v.q_len + (R1 - 1) / G;
-  t.pf = tree ? v.kv_len - v.q_len - 1 : t.p0;
   t.sink_b = t.lo = 0;
   t.nblk = 1;
   if (t.p1 >= 0) {
     const int hi = t.p1 / kBN;
     if (window > 0) {
-      t.lo = max(0, (tree ? t.pf + 1 : t.p0) - window + 1) / kBN;  // (a node's position is at least the tree's first slot)
+      t.lo = max(0, (tree ? v.kv_len - v.q_len : t.p0) - window + 1) / kBN;  // (a node's position is at least the tree's first slot)
       t.sink_b = (min(sinks, t.p1 + 1) + kBN - 1) / kBN;
       if (t.sink_b >= t.lo) t.lo = t.sink_b = 0;
     }
@@ -223,6 +221,7 @@ struct Start {
   int s, h, mt, off, n;  // item, offset into its part of the line, length of the worker's piece
   SeqView v;
 };
+template <bool TREE>
 struct Walk {
   const AttendParams* a;
   int s, h, mt, off, left, n_mt, M, seg;
@@ -247,7 +246,7 @@ struct Walk {
       }
     }
     ++seg;
-    t = make_tile(v, a->G, M, mt, a->window, a->sinks, a->parents != nullptr);
+    t = make_tile(v, a->G, M, mt, a->window, a->sinks, TREE);
     b0 = max(0, off - item_cost(M));
     b1 = min(t.nblk, max(0, off + left - item_cost(M)));
     left -= t.nblk + item_cost(M) - off;
@@ -392,7 +391,7 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {
   }
   return x;
 }
-template <int M>
+template <int M, bool TREE>
 __device__ void find_start(const AttendParams& a, int* scratch, Start* out, int worker, bool leader) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, nw = blockDim.x / 32;
   const int n_seqs = a.rows.n_seqs, hkv = a.pool.hkv;
@@ -405,7 +404,7 @@ __device__ void find_start(const AttendParams& a, int* scratch, Start* out, int 
     const int n = tiles_of(v, a.G, M);
     int sum = n <= kFew ? 0 : -1;
     for (int mt = 0; mt < min(n, kFew) && sum >= 0; ++mt)
-      sum += make_tile(v, a.G, M, mt, a.window, a.sinks, a.parents != nullptr).nblk + item_cost(M);
+      sum += make_tile(v, a.G, M, mt, a.window, a.sinks, TREE).nblk + item_cost(M);
     scratch[s] = sum;
     many |= sum < 0;
   }
@@ -415,7 +414,7 @@ __device__ void find_start(const AttendParams& a, int* scratch, Start* out, int 
       const SeqView v = seq_view(a.rows, s);
       const int n = tiles_of(v, a.G, M);
       int sum = 0;
-      for (int mt = lane; mt < n; mt += 32) sum += make_tile(v, a.G, M, mt, a.window, a.sinks, a.parents != nullptr).nblk + item_cost(M);
+      for (int mt = lane; mt < n; mt += 32) sum += make_tile(v, a.G, M, mt, a.window, a.sinks, TREE).nblk + item_cost(M);
       sum = warp_sum(sum);
       __syncwarp();
       if (lane == 0) scratch[s] = sum;
@@ -461,7 +460,7 @@ __device__ void find_start(const AttendParams& a, int* scratch, Start* out, int 
       if (lane == 0) out->n = 0;
       return;
     }
-    const int nb = mt + lane < n_mt ? make_tile(v, a.G, M, mt + lane, a.window, a.sinks, a.parents != nullptr).nblk + item_cost(M) : 0;
+    const int nb = mt + lane < n_mt ? make_tile(v, a.G, M, mt + lane, a.window, a.sinks, TREE).nblk + item_cost(M) : 0;
     const int inc = warp_scan(nb, lane);
     const uint32_t hit = __ballot_sync(0xffffffffu, g0 < at + inc && nb > 0);
     if (hit) {
@@ -512,25 +511,46 @@ __global__ void __launch_bounds__(256) attend_join(const AttendParams a) {
   for (int r0 = first; r0 < j.rows; r0 += cuts * gridDim.y * (8 / share)) {
     const int r = share == 1 ? r0 + warp : r0;
     if (r < j.rows) {
-      float m = -INFINITY;
-      for (int k = lane; k <= cuts; k += 32) m = fmaxf(m, a.ml[(k ? 2 * (j.w0 + k) : j.slot0) * M + r].x);
+      // A batch of parts, the first together with the references and sums of all (a lane's k is `lane`): one wait for
+      // memory instead of two.
+      constexpr int kBatch = 4;
+      const int k0 = share == 1 ? 0 : warp;
+      auto slot_of = [&](int k) { return k ? 2 * (j.w0 + k) : j.slot0; };
+      float2 y[kBatch][kPer / 2];
+      auto fetch = [&](int k) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          if (k + u * share > cuts) continue;
+          const float* p = a.part + (static_cast<int64_t>(slot_of(k + u * share)) * M + r) * DH + lane * kPer;
+#pragma unroll
+          for (int i = 0; i < kPer / 2; ++i) y[u][i] = reinterpret_cast<const float2*>(p)[i];
+        }
+      };
+      const float2 near = lane <= cuts ? a.ml[slot_of(lane) * M + r] : make_float2(-INFINITY, 0.f);
+      fetch(k0);
+      float m = near.x;
+      for (int k = 32 + lane; k <= cuts; k += 32) m = fmaxf(m, a.ml[slot_of(k) * M + r].x);
 #pragma unroll
       for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
       if (m == -INFINITY) m = 0.f;
       float l = 0.f, o[kPer] = {};
-#pragma unroll 4
-      for (int k = share == 1 ? 0 : warp; k <= cuts; k += share) {
-        const int slot = k ? 2 * (j.w0 + k) : j.slot0;
-        const float2 x = a.ml[slot * M + r];
-        const float f = ex2(x.x - m);
-        l += f * x.y;
-        const float* p = a.part + (static_cast<int64_t>(slot) * M + r) * DH + lane * kPer;
+      for (int k = k0; k <= cuts;) {
 #pragma unroll
-        for (int i = 0; i < kPer; i += 2) {
-          const float2 y = *reinterpret_cast<const float2*>(p + i);
-          o[i] += f * y.x;
-          o[i + 1] += f * y.y;
+        for (int u = 0; u < kBatch; ++u) {
+          const int ku = k + u * share;
+          if (ku > cuts) break;
+          const float2 x = ku < 32 ? make_float2(__shfl_sync(0xffffffffu, near.x, ku & 31), __shfl_sync(0xffffffffu, near.y, ku & 31))
+                                   : a.ml[slot_of(ku) * M + r];
+          const float f = ex2(x.x - m);
+          l += f * x.y;
+#pragma unroll
+          for (int i = 0; i < kPer / 2; ++i) {
+            o[2 * i] += f * y[u][i].x;
+            o[2 * i + 1] += f * y[u][i].y;
+          }
         }
+        k += kBatch * share;
+        if (k <= cuts) fetch(k);
       }
 #pragma unroll
       for (int i = 0; i < kPer; ++i) sums[warp][lane * kPer + i] = o[i];
@@ -557,7 +577,7 @@ __global__ void __launch_bounds__(256) attend_join(const AttendParams a) {
 }
 
 // The worker's segments, every warp its part. LARGE: once more, from segment `first` on, with large q8 values.
-template <int NS, bool Q8, int CG, bool LARGE>
+template <int NS, bool Q8, int CG, bool TREE, bool LARGE>
 __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtensorMap& tk, const CUtensorMap& tv, uint8_t* smem,
                                             uint32_t tm) {
   using C = Cfg<NS, Q8, CG>;
@@ -578,7 +598,7 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
     if (CG == 1) bar_arrive(smem_u32(&b)); else bar_arrive_cluster(peer_addr(smem_u32(&b), 0));
   };
 
-  Walk wk(a, ms.start, M);
+  Walk<TREE> wk(a, ms.start, M);
   // barriers and buffers go by the number of segments taken so far: seg + shift
   const int first = LARGE ? ms.large : 0, shift = LARGE ? ms.taken - first : 0;
   const int units0 = LARGE ? ms.units : 0, blocks0 = LARGE ? ms.blocks : 0;
@@ -823,7 +843,7 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
       const int base_p = wk.v.kv_len - wk.v.q_len, last = wk.t.rows - 1;
       const RowOf at = row_of(wk.t, min(r, last), a.G, a.g_inv);
       const int p = base_p + at.tok;
-      const int wp0 = a.parents ? wk.t.pf : base_p + row_of(wk.t, min(r_warp, last), a.G, a.g_inv).tok;
+      const int wp0 = TREE ? base_p - 1 : base_p + row_of(wk.t, min(r_warp, last), a.G, a.g_inv).tok;
       const int wp1 = base_p + row_of(wk.t, min(r_warp + 31, last), a.G, a.g_inv).tok;
       float m = valid ? -INFINITY : 0.f, l = 0.f, c = 0.f;
       int pages = lane < 4 ? wk.entry(wk.t.block(wk.b0), 4 * half + lane) : 0;
@@ -856,7 +876,7 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
           uint32_t sx = 0xffffffffu, sy = 0xffffffffu;
           const bool part = gone || !block_full(b, wp0, wp1, a.window, a.sinks);
           if (part) {
-            if (a.parents) {
+            if constexpr (TREE) {
               const uint64_t seen = seen_tree(a.parents + wk.v.r0, at.tok, base_p, b * kBN + 64 * half, a.window, a.sinks);
               sx = static_cast<uint32_t>(seen);
               sy = static_cast<uint32_t>(seen >> 32);
@@ -985,11 +1005,16 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
           // rows that see a cleared value add it: +-inf or NaN whatever its weight
           for (int i = wk.b0; i < wk.b1; ++i) {
             const int b = wk.t.block(i);
-            uint64_t tree = 0;
+            [[maybe_unused]] uint64_t tree = 0;
             for (int t = 0; t < kBN; ++t) {
-              if (a.parents && t % 64 == 0) tree = seen_tree(a.parents + wk.v.r0, at.tok, base_p, b * kBN + t, a.window, a.sinks);
+              bool seen;
+              if constexpr (TREE) {
+                if (t % 64 == 0) tree = seen_tree(a.parents + wk.v.r0, at.tok, base_p, b * kBN + t, a.window, a.sinks);
+                seen = tree >> (t & 63) & 1;
+              } else {
+                seen = seen_bits(p, b * kBN + (t & ~31), a.window, a.sinks) >> (t & 31) & 1;
+              }
               const int pg = wk.entry(b, t / kPage);
-              const bool seen = a.parents ? tree >> (t & 63) & 1 : seen_bits(p, b * kBN + (t & ~31), a.window, a.sinks) >> (t & 31) & 1;
               if (!wk.has_page(pg) || !seen) continue;
               const int64_t e = ((static_cast<int64_t>(pg) * a.pool.hkv + wk.h) * kPage + t % kPage) * DH + 32 * k;
               if (Q8) {
@@ -1045,7 +1070,7 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
       const int key0 = CG == 2 ? (kv ? 0 : 64 * rank) : (kv ? u * C::kKeysV : 0);
       uint8_t* const dst = ring + slot * C::kSlot;
       bool found = false;
-      const bool partly = kv && !block_full(b, wk.t.pf, wk.t.p1, a.window, a.sinks);
+      const bool partly = kv && !block_full(b, TREE ? wk.v.kv_len - wk.v.q_len - 1 : wk.t.p0, wk.t.p1, a.window, a.sinks);
       if constexpr (!Q8) {
         if (!wait(ms.full[slot], phase)) return false;
         if (partly) {
@@ -1280,12 +1305,12 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
 }
 
 // (A function of its own: inlined it took registers from the first pass, 3 % of the time over q8 pools.)
-template <int NS, int CG>
+template <int NS, int CG, bool TREE>
 __device__ __noinline__ void large_pass(const AttendParams& a, const CUtensorMap& tk, const CUtensorMap& tv, uint8_t* smem, uint32_t tm) {
-  attend_pass<NS, true, CG, true>(a, tk, tv, smem, tm);
+  attend_pass<NS, true, CG, TREE, true>(a, tk, tv, smem, tm);
 }
 
-template <int NS, bool Q8, int CG>
+template <int NS, bool Q8, int CG, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ AttendParams a, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv) {
@@ -1329,14 +1354,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     ms.large = INT_MAX;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (tid == 32 * kWarpCopy) {  // (the first copy waited for them: 0.4 us of a short call)
+    tensormap_prefetch(&tk);
+    tensormap_prefetch(&tv);
+  }
   if (warp == kWarpMma) tmem_alloc<CG>(smem_u32(&ms.tmem), 512);
-  find_start<C::M>(a, reinterpret_cast<int*>(ring), &ms.start, blockIdx.x / CG, rank == 0);
+  find_start<C::M, TREE>(a, reinterpret_cast<int*>(ring), &ms.start, blockIdx.x / CG, rank == 0);
   fence_async_shared();  // the scratch lay where tensor copies go
   meet();
   tc_fence_after();
   const uint32_t tm = ms.tmem;
   asm volatile("griddepcontrol.launch_dependents;");
-  attend_pass<NS, Q8, CG, false>(a, tk, tv, smem, tm);
+  attend_pass<NS, Q8, CG, TREE, false>(a, tk, tv, smem, tm);
   if constexpr (Q8 && CG == 2) {  // both blocks of a pair go on alike, even if the pool changes under the kernel
     __syncthreads();
     if (threadIdx.x == 0) min_cluster(peer_addr(smem_u32(&ms.large), static_cast<uint32_t>(~blockIdx.x & 1)), ms.large);
@@ -1345,7 +1374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (Q8) {
     if (ms.large != INT_MAX) {
       tc_fence_after();
-      large_pass<NS, CG>(a, tk, tv, smem, tm);
+      large_pass<NS, CG, TREE>(a, tk, tv, smem, tm);
       meet();
     }
   }
@@ -1358,14 +1387,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------- launch
 // Blocks (pairs) that are resident at once, found once per device; 0 on error.
-template <int NS, bool Q8, int CG>
+template <int NS, bool Q8, int CG, bool TREE>
 int resident_workers(int device) {
   using C = Cfg<NS, Q8, CG>;
   static std::atomic<int> known[64];
   if (device < 0 || device >= 64) return 0;
   int n = known[device].load();
   if (n) return n;
-  const auto fn = attend_kernel<NS, Q8, CG>;
+  const auto fn = attend_kernel<NS, Q8, CG, TREE>;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return 0;
   int sms = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return 0;
@@ -1387,10 +1416,10 @@ int resident_workers(int device) {
   return n;
 }
 
-template <int NS, bool Q8, int CG>
+template <int NS, bool Q8, int CG, bool TREE>
 cudaError_t launch_attend(AttendParams a, const CUtensorMap& tk, const CUtensorMap& tv, int device, cudaStream_t stream) {
   using C = Cfg<NS, Q8, CG>;
-  a.workers = resident_workers<NS, Q8, CG>(device);
+  a.workers = resident_workers<NS, Q8, CG, TREE>(device);
   if (!a.workers) return cudaErrorInvalidDevice;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
@@ -1402,7 +1431,7 @@ cudaError_t launch_attend(AttendParams a, const CUtensorMap& tk, const CUtensorM
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel<NS, Q8, CG>, a, tk, tv);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel<NS, Q8, CG, TREE>, a, tk, tv);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t jc{};
   cudaLaunchAttribute ja[1];
@@ -1416,16 +1445,16 @@ cudaError_t launch_attend(AttendParams a, const CUtensorMap& tk, const CUtensorM
   return cudaLaunchKernelEx(&jc, attend_join<NS, CG>, a);
 }
 
-template <bool Q8>
+template <bool Q8, bool TREE>
 cudaError_t launch_any(int ns, int cg, const AttendParams& a, const CUtensorMap& tk, const CUtensorMap& tv, int device,
                        cudaStream_t stream) {
   switch (ns * 2 + (cg - 1)) {
-    case 2: return launch_attend<1, Q8, 1>(a, tk, tv, device, stream);
-    case 4: return launch_attend<2, Q8, 1>(a, tk, tv, device, stream);
-    case 5: return launch_attend<2, Q8, 2>(a, tk, tv, device, stream);
-    case 6: return launch_attend<3, Q8, 1>(a, tk, tv, device, stream);
-    case 8: return launch_attend<4, Q8, 1>(a, tk, tv, device, stream);
-    case 9: return launch_attend<4, Q8, 2>(a, tk, tv, device, stream);
+    case 2: return launch_attend<1, Q8, 1, TREE>(a, tk, tv, device, stream);
+    case 4: return launch_attend<2, Q8, 1, TREE>(a, tk, tv, device, stream);
+    case 5: return launch_attend<2, Q8, 2, TREE>(a, tk, tv, device, stream);
+    case 6: return launch_attend<3, Q8, 1, TREE>(a, tk, tv, device, stream);
+    case 8: return launch_attend<4, Q8, 1, TREE>(a, tk, tv, device, stream);
+    case 9: return launch_attend<4, Q8, 2, TREE>(a, tk, tv, device, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -55,33 +55,49 @@ __global__ void __launch_bounds__(kCopyBlock) kv_copy_kernel(const __grid_consta
 // --------------------------------------------------------------- kept tokens
 // Entry i of a sequence's list moves new row keep[i] to slot base + i. The list
 // ascends, so keep[i] >= i: a slot is written by an entry at or before every entry that
-// reads it or a later slot. A block takes a 64-byte column of a head's rows (or its
-// scales) through the whole list, kTokens entries at a time: all are read, the block
-// meets, all are written. What later entries read lies behind everything that earlier
-// ones write, so columns need no order among blocks, and the next read may begin before
-// the write. `per` columns share one look at the list.
-constexpr int kTokens = 128;  // threads of a block, and entries at a time
-constexpr int kWide = 64;     // bytes of a column
+// reads it or a later slot. A block takes one column of a head's rows, or its scales,
+// through the whole list, a batch of entries at a time: all of a batch are read, the
+// block meets, all are written. What later entries read lies behind everything that
+// earlier ones write, so columns need no order among blocks, and the next batch is read
+// while this one is on its way. LANES lanes of 16 bytes take a token: 4 in long lists
+// (128 entries a batch, narrow columns, many blocks), 16 in short ones (32 entries).
+constexpr int kThreads = 128, kDeep = 4;  // threads of a block, tokens that a thread moves at a time
 
 struct KeepArgs {
   mk_kv_layers l;
   mk_kv_rows rows;
   const int32_t* keep;
   int32_t* kv_len;
-  int row_bytes, columns, data, per;  // bytes of a head's row; columns of a layer, those of K and V among them; columns of a block
+  int row_bytes, pieces, data;  // bytes of a head's row, columns of it; columns of a layer that are K's and V's
 };
 
-__global__ void __launch_bounds__(kTokens) kv_keep_kernel(const __grid_constant__ KeepArgs a) {
-  __shared__ int from[kTokens], to[kTokens], first;
+template <int LANES>
+__global__ void __launch_bounds__(kThreads) kv_keep_kernel(const __grid_constant__ KeepArgs a) {
+  constexpr int kTokens = kThreads * kDeep / LANES;  // entries of a batch
+  static_assert(kTokens <= kThreads && kTokens % 32 == 0, "a thread looks at one entry");
+  __shared__ int from[3][kTokens], to[3][kTokens];
+  __shared__ uint32_t ascends[3][kTokens / 32];
   const int s = blockIdx.y, tid = threadIdx.x;
   const SeqView v = seq_view(a.rows, s);
   const int base = v.kv_len - v.q_len, hkv = a.l.pool.hkv, n_pages = a.l.pool.n_pages;
   const int64_t layer = static_cast<int64_t>(blockIdx.z) * a.l.layer_stride;
-  const bool q8 = a.l.pool.kv_dtype == MK_KV_Q8;
-  const int c0 = blockIdx.x * a.per, c1 = min(c0 + a.per, a.columns);
-  int count = 0;
-  for (int i0 = 0; i0 < v.q_len; i0 += kTokens) {
-    const int i = i0 + tid;
+  // the column: its head's first row, the bytes from row to row, and those of a row that it moves
+  const int c = blockIdx.x, words = a.l.pool.dh / 64;
+  const bool scales = c >= a.data;
+  const int col = scales ? c - a.data : c, per = scales ? 1 : a.pieces, kvh = col / per, piece = col - kvh * per;
+  const bool is_v = kvh >= hkv;
+  const int head = is_v ? kvh - hkv : kvh, bytes = scales ? 4 * words : a.row_bytes;
+  uint8_t* p = static_cast<uint8_t*>(scales ? (is_v ? a.l.pool.v_scale : a.l.pool.k_scale) : is_v ? a.l.pool.v : a.l.pool.k) +
+               (scales ? layer / 16 : a.l.pool.kv_dtype == MK_KV_Q8 ? layer : 2 * layer) + static_cast<int64_t>(head) * kPage * bytes;
+  const int at16 = (piece * LANES + tid % LANES) * 16;
+  const bool mine = scales || at16 < bytes;
+  if (!scales) p += at16;
+
+  // Batch b of the list: rows of a head that its entries come from and go to (-1: does not move), and which entries follow
+  // the one before.
+  auto look = [&](int b, int buf) {
+    if (tid >= kTokens) return;
+    const int i = b * kTokens + tid;
     int f = -1, t = -1;
     bool good = false;
     if (i < v.q_len) {
@@ -90,55 +106,82 @@ __global__ void __launch_bounds__(kTokens) kv_keep_kernel(const __grid_constant_
       if (good && k != i) {
         f = token_at(a.rows, n_pages, s, base + k);
         t = token_at(a.rows, n_pages, s, base + i);
+        if (f < 0 || t < 0) f = -1;
       }
     }
-    if (tid == 0) first = kTokens;
-    __syncthreads();  // (also: the entries before have been taken from `from` and `to`)
-    from[tid] = t < 0 ? -1 : f;
-    to[tid] = t;
-    if (!good) atomicMin(&first, tid);
-    __syncthreads();
-    const int n = first;  // entries up to the first that does not ascend
-    count += n;
-    for (int c = c0; c < c1; ++c) {
-      const bool scales = c >= a.data;
-      const int per_row = scales ? 1 : a.row_bytes / kWide;
-      const int col = scales ? c - a.data : c, piece = col % per_row, kvh = col / per_row, head = kvh % hkv;
-      const bool is_v = kvh >= hkv;
-      // byte of token row r (page r / 16, slot r % 16) of the column
-      auto at = [&](int r, int bytes) { return ((static_cast<int64_t>(r / kPage) * hkv + head) * kPage + r % kPage) * bytes; };
-      if (!scales) {
-        uint8_t* const p = static_cast<uint8_t*>(is_v ? a.l.pool.v : a.l.pool.k) + (q8 ? layer : 2 * layer) + piece * kWide + tid % 4 * 16;
-        uint4 x[4];
-        int d[4];
+    from[buf][tid] = f < 0 ? -1 : f / kPage * (hkv * kPage) + f % kPage;  // (below 2^31: check_pool)
+    to[buf][tid] = t < 0 ? -1 : t / kPage * (hkv * kPage) + t % kPage;
+    const uint32_t ok = __ballot_sync(0xffffffffu, good);
+    if (tid % 32 == 0) ascends[buf][tid / 32] = ok;
+  };
+  struct Batch {
+    uint4 x[kDeep];
+    int d[kDeep];
+    int n;  // entries that count, up to the first that does not follow
+  };
+  auto load = [&](int buf) {
+    Batch t;
+    t.n = 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int e = u * (kTokens / 4) + tid / 4, r = e < n ? from[e] : -1;
-          d[u] = r < 0 ? -1 : to[e];
-          if (r >= 0) x[u] = *reinterpret_cast<const uint4*>(p + at(r, a.row_bytes));
-        }
-        __syncthreads();
+    for (int w = 0; w < kTokens / 32; ++w) {
+      const uint32_t end = ~ascends[buf][w];
+      if (t.n == 32 * w) t.n += end ? __ffs(end) - 1 : 32;
+    }
+    if (scales) {  // a thread a token, its scales word by word
+      const int r = tid < t.n ? from[buf][tid] : -1;
+      t.d[0] = r < 0 ? -1 : to[buf][tid];
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(p + static_cast<int64_t>(r) * bytes);
+      if (r >= 0) {
+        t.x[0].x = q[0];
+        if (words > 1) t.x[0].y = q[1];
+        if (words > 2) t.x[0].z = q[2];
+        if (words > 3) t.x[0].w = q[3];
+      }
+    } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (d[u] >= 0) *reinterpret_cast<uint4*>(p + at(d[u], a.row_bytes)) = x[u];
-      } else {
-        uint8_t* const p = static_cast<uint8_t*>(is_v ? a.l.pool.v_scale : a.l.pool.k_scale) + layer / 16;
-        const int words = a.l.pool.dh / 64, r = tid < n ? from[tid] : -1, d = r < 0 ? -1 : to[tid];
-        uint32_t x[4];
-        if (r >= 0) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            if (w < words) x[w] = reinterpret_cast<const uint32_t*>(p + at(r, 4 * words))[w];
-        }
-        __syncthreads();
-        if (d >= 0) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            if (w < words) reinterpret_cast<uint32_t*>(p + at(d, 4 * words))[w] = x[w];
-        }
+      for (int u = 0; u < kDeep; ++u) {
+        const int e = u * (kThreads / LANES) + tid / LANES, r = mine && e < t.n ? from[buf][e] : -1;
+        t.d[u] = r < 0 ? -1 : to[buf][e];
+        if (r >= 0) t.x[u] = *reinterpret_cast<const uint4*>(p + static_cast<int64_t>(r) * bytes);
       }
     }
-    if (n < kTokens) break;
+    return t;
+  };
+  auto store = [&](const Batch& t) {
+    if (scales) {
+      if (t.d[0] < 0) return;
+      uint32_t* q = reinterpret_cast<uint32_t*>(p + static_cast<int64_t>(t.d[0]) * bytes);
+      q[0] = t.x[0].x;
+      if (words > 1) q[1] = t.x[0].y;
+      if (words > 2) q[2] = t.x[0].z;
+      if (words > 3) q[3] = t.x[0].w;
+    } else {
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u)
+        if (t.d[u] >= 0) *reinterpret_cast<uint4*>(p + static_cast<int64_t>(t.d[u]) * bytes) = t.x[u];
+    }
+  };
+  look(0, 0);
+  look(1, 1);
+  __syncthreads();
+  Batch now = load(0);
+  int count = now.n;
+  for (int b = 0, buf = 0;; ++b) {
+    // batch b is on its way (or here), the list of batch b + 1 in shared memory
+    const int next = buf == 2 ? 0 : buf + 1, after = next == 2 ? 0 : next + 1;
+    const bool more = now.n == kTokens;
+    Batch then;
+    then.n = 0;
+    if (more) {
+      then = load(next);
+      look(b + 2, after);  // (its buffer was read two batches ago)
+    }
+    __syncthreads();  // every thread has read batch b
+    store(now);
+    if (!more) break;
+    now = then;
+    count += now.n;
+    buf = next;
   }
   if (a.kv_len && blockIdx.x == 0 && blockIdx.z == 0 && tid == 0) a.kv_len[s] = max(base + count, 0);
 }
@@ -186,17 +229,17 @@ extern "C" mk_status mk_kv_keep(const mk_kv_layers* layers, const mk_kv_rows* ro
   if (!keep && rows->n_rows > 0) return MK_ERR_INVALID;
   const mk_kv_pool& p = layers->pool;
   const bool q8 = p.kv_dtype == MK_KV_Q8;
-  KeepArgs a{*layers, *rows, keep, kv_len, p.dh * (q8 ? 1 : 2), 0, 0, 1};
-  const int64_t data = 2ll * p.hkv * (a.row_bytes / kWide), columns = data + (q8 ? 2ll * p.hkv : 0);
+  // short lists (drafts) in wide columns, long ones in narrow: the more blocks the more is on its way
+  const bool wide = rows->n_rows <= 32ll * rows->n_seqs;
+  const int width = 16 * (wide ? 16 : 4);
+  KeepArgs a{*layers, *rows, keep, kv_len, p.dh * (q8 ? 1 : 2), 0, 0};
+  a.pieces = (a.row_bytes + width - 1) / width;
+  const int64_t data = 2ll * p.hkv * a.pieces, columns = data + (q8 ? 2ll * p.hkv : 0);
   if (columns > (1 << 24)) return MK_ERR_UNSUPPORTED;
   a.data = static_cast<int>(data);
-  a.columns = static_cast<int>(columns);
-  // as many columns a block as leave eight blocks an SM, up to eight
-  const int64_t per = columns * rows->n_seqs * layers->n_layers / (152 * 8);
-  a.per = per < 1 ? 1 : per > 8 ? 8 : static_cast<int>(per);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.columns + a.per - 1) / a.per), rows->n_seqs, layers->n_layers);
-  cfg.blockDim = dim3(kTokens);
+  cfg.gridDim = dim3(static_cast<unsigned>(columns), rows->n_seqs, layers->n_layers);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = static_cast<cudaStream_t>(stream);
-  return launched(cudaLaunchKernelEx(&cfg, kv_keep_kernel, a));
+  return launched(cudaLaunchKernelEx(&cfg, wide ? kv_keep_kernel<16> : kv_keep_kernel<4>, a));
 }

@@ -14,10 +14,11 @@
 // Layout. dh / 16 neighbouring lanes hold a head vector, eight dims and the
 // eight that they are paired with per lane (dims that are not turned are paired
 // the same way): the turn stays in the thread, the norm's sum takes up to four
-// shuffles, and four lanes hold two 32-dim q8 blocks (r is a multiple of 64). A group
-// of lanes takes `per` heads of its row, so that with many rows the angles are made once
-// for several heads. Each thread reads its 16 values before it writes them: out may
-// be q.
+// shuffles, and four lanes hold two 32-dim q8 blocks (r is a multiple of 64). Such a
+// group of lanes takes PER heads, whose loads are all issued before anything else: with
+// many rows four, of one or several rows of its block. The block's threads look its rows
+// up and make their sines and cosines once for all heads, in shared memory. Each thread
+// reads its 16 values of a head before it writes them: out may be q.
 #include <cmath>
 
 #include <cuda_runtime.h>
@@ -30,6 +31,8 @@ namespace ops {
 namespace {
 
 constexpr int kBlock = 256;
+constexpr int kMaxRows = 16;  // of a block
+constexpr int kPer = 4;       // heads of a group, with many rows
 
 struct RopeArgs {
   mk_kv_pool pool;
@@ -38,103 +41,188 @@ struct RopeArgs {
   mk_rope rope;
   const int32_t* parents;
   const int32_t* positions;
-  int hq, heads, per;       // heads: of q, k and v; per: heads of a group
-  uint32_t row_groups;      // groups per row
-  int lanes_log2, row0, n;  // lanes of a group; rows [row0, row0 + n) of this launch
+  int hq, heads;                   // heads of q; of q, k and v
+  int block_rows, block_heads, head_blocks, heads_inv;  // a block's rows and heads; blocks per rows; 2^20 / block_heads + 1
+  int lanes_log2, row0, n;         // lanes of a group; rows [row0, row0 + n) of this launch
+  float inv_dh;
 };
 
-template <int DT, bool Q8, bool VEC>
-__global__ void __launch_bounds__(kBlock) rope_write_kernel(const __grid_constant__ RopeArgs a) {
+// Eight values as loaded.
+template <int DT>
+struct Raw {
+  uint4 w[DT == MK_F32 ? 2 : 1];
+};
+template <int DT, bool VEC>
+__device__ __forceinline__ Raw<DT> fetch8(const typename Elem<DT>::T* p) {
+  Raw<DT> r;
+  if (VEC) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) r.w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  } else {
+    alignas(16) typename Elem<DT>::T t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = p[i];
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) r.w[i] = reinterpret_cast<const uint4*>(t)[i];
+  }
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void values8(const Raw<DT>& r, float* x) {
+  const typename Elem<DT>::T* t = reinterpret_cast<const typename Elem<DT>::T*>(&r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = Elem<DT>::get(t[i]);
+}
+
+template <int DT, bool Q8, bool VEC, int PER>
+__global__ void __launch_bounds__(kBlock, PER == 1 || DT == MK_F32 || !VEC ? 2 : 4) rope_write_kernel(const __grid_constant__ RopeArgs a) {
   using T = typename Elem<DT>::T;
-  const int lanes = 1 << a.lanes_log2, c = threadIdx.x & (lanes - 1);
-  const uint32_t group = blockIdx.x * (kBlock >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
-  const uint32_t g = group / a.row_groups;
-  const int part = group - g * a.row_groups;
-  const bool live = g < static_cast<uint32_t>(a.n);
-  const int row = a.row0 + (live ? static_cast<int>(g) : a.n - 1);  // groups behind the end shadow the last row
-  const int lane = threadIdx.x & 31;
+  __shared__ int row_token[kMaxRows], row_pos[kMaxRows];  // token: -2 for rows of no sequence
+  extern __shared__ __align__(16) float table[];          // [block_rows][2][rot / 2]: cosines, sines
+  const int tid = threadIdx.x, lanes = 1 << a.lanes_log2, c = tid & (lanes - 1), groups = kBlock >> a.lanes_log2;
+  const int rb = static_cast<int>(blockIdx.x) / a.head_blocks, h0 = (static_cast<int>(blockIdx.x) - rb * a.head_blocks) * a.block_heads;
+  const int r0 = rb * a.block_rows;  // the block's first row, of this launch
+  const int n_rows = min(a.block_rows, a.n - r0), n_heads = min(a.block_heads, a.heads - h0);
+  const int lane = tid & 31;
   const uint32_t mask = ((1u << lanes) - 1) << (lane & ~(lanes - 1));
-  const int dh = a.pool.dh, rot = a.rope.rot, hkv = a.pool.hkv;
+  const int dh = a.pool.dh, rot = a.rope.rot, half = rot / 2, hkv = a.pool.hkv;
   // the lane's dims: eight from lo, eight from lo + step
   const bool in = c < dh / 16;  // (head dim 192 leaves four lanes of sixteen idle)
   const int ci = in ? c : 0, turned = rot / 16;
   const bool turns = ci < turned;
-  const int lo = turns ? 8 * ci : rot + 8 * (ci - turned), step = turns ? rot / 2 : (dh - rot) / 2;
+  const int lo = turns ? 8 * ci : rot + 8 * (ci - turned), step = turns ? half : (dh - rot) / 2;
 
-  int token = -1, pos = 0, seq = -1;
-  float cs[8], sn[8];
-  bool looked = false, angles = false;
-  for (int it = 0; it < a.per; ++it) {
-    const int slot = part + it * static_cast<int>(a.row_groups);
-    const bool has = slot < a.heads;
-    const int h = has ? slot : a.heads - 1;
-    const int kind = h < a.hq ? 0 : h < a.hq + hkv ? 1 : 2, head = kind == 0 ? h : kind == 1 ? h - a.hq : h - a.hq - hkv;
-    const mk_dense& src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-    const T* p = static_cast<const T*>(src.data) + row * src.row_stride + head * src.head_stride + lo;
-    float x[8], y[8];
-    load8<DT, VEC>(p, x);
-    load8<DT, VEC>(p + step, y);
-    if (!looked) {  // (behind the first loads: three dependent ones)
-      looked = true;
-      SeqView v;
-      seq = seq_of_row(a.rows, row, v);
-      if (seq >= 0) {
-        const int node = row - v.r0, at = v.kv_len - v.q_len + node;
-        token = token_at(a.rows, a.pool.n_pages, seq, at);
-        pos = at;
-        if (a.positions) {
-          pos = __ldg(a.positions + row);
-        } else if (a.parents) {
-          pos = at - node;
-          for (int n = parent_of(a.parents + v.r0, node); n >= 0; n = parent_of(a.parents + v.r0, n)) ++pos;
-        }
+  // the group's heads: pairs of a row and a head of the block, PER at a time
+  struct Item {
+    int row, kind, head;  // row of the block, -1: none; kind 0 q, 1 k, 2 v
+  };
+  auto item = [&](int p) {
+    const int r = a.block_rows == 1 ? 0 : (p * a.heads_inv) >> 20, h = p - r * a.block_heads;
+    Item t;
+    t.row = r < n_rows && h < n_heads ? r : -1;
+    const int g = h0 + (t.row < 0 ? 0 : h);
+    t.kind = g < a.hq ? 0 : g < a.hq + hkv ? 1 : 2;
+    t.head = t.kind == 0 ? g : t.kind == 1 ? g - a.hq : g - a.hq - hkv;
+    return t;
+  };
+  Raw<DT> x0[PER], y0[PER];
+  const int first = tid >> a.lanes_log2;
+#pragma unroll
+  for (int u = 0; u < PER; ++u) {
+    const Item t = item(first + u * groups);
+    if (t.row < 0) continue;
+    const mk_dense& src = t.kind == 0 ? a.q : t.kind == 1 ? a.k : a.v;
+    const T* p = static_cast<const T*>(src.data) + (a.row0 + r0 + t.row) * src.row_stride + t.head * src.head_stride + lo;
+    x0[u] = fetch8<DT, VEC>(p);
+    y0[u] = fetch8<DT, VEC>(p + step);
+  }
+  if (tid < n_rows) {
+    const int row = a.row0 + r0 + tid;
+    SeqView v;
+    const int seq = seq_of_row(a.rows, row, v);
+    int token = -2, pos = 0;
+    if (seq >= 0) {
+      const int node = row - v.r0, at = v.kv_len - v.q_len + node;
+      token = token_at(a.rows, a.pool.n_pages, seq, at);
+      pos = at;
+      if (a.positions) {
+        pos = __ldg(a.positions + row);
+      } else if (a.parents) {
+        pos = at - node;
+        for (int n = parent_of(a.parents + v.r0, node); n >= 0; n = parent_of(a.parents + v.r0, n)) ++pos;
       }
     }
-    if (kind < 2) {
-      if (!angles && turns) {
-        angles = true;
+    row_token[tid] = token;
+    row_pos[tid] = pos;
+  }
+  __syncthreads();
+  if (h0 < a.hq + hkv) {  // (a block of v alone turns nothing)
+    for (int i = tid; i < n_rows * half; i += kBlock) {
+      const int r = i / half, j = i - r * half;
+      const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(row_pos[r])) * __ldg(a.rope.turns + j);
+      float sn, cs;
+      sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
+      table[r * rot + j] = cs;
+      table[r * rot + half + j] = sn;
+    }
+  }
+  __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(pos)) * __ldg(a.rope.turns + lo + i);
-          sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 4.656612873077393e-10f, &sn[i], &cs[i]);  // 2^-31
-        }
+  for (int u = 0; u < PER; ++u) {
+    const Item t = item(first + u * groups);
+    if (t.row < 0) continue;  // (whole groups)
+    const int token = row_token[t.row];
+    float x[8], y[8];
+    values8<DT>(x0[u], x);
+    values8<DT>(y0[u], y);
+    if (t.kind < 2) {
+      // two values an instruction
+      uint64_t x2[4], y2[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x2[i] = pack2(x[2 * i], x[2 * i + 1]);
+        y2[i] = pack2(y[2 * i], y[2 * i + 1]);
       }
-      const float* gain = kind == 0 ? a.rope.q_gain : a.rope.k_gain;
+      const float* gain = t.kind == 0 ? a.rope.q_gain : a.rope.k_gain;
       if (gain) {
-        float sum = 0.f;
+        uint64_t s2 = mul2(x2[0], x2[0]), s3 = mul2(y2[0], y2[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += x[i] * x[i] + y[i] * y[i];
-        if (!in) sum = 0.f;
-        for (int m = lanes >> 1; m; m >>= 1) sum += __shfl_xor_sync(mask, sum, m);
-        const float f = rsqrtf(sum / static_cast<float>(dh) + a.rope.eps);
+        for (int i = 1; i < 4; ++i) {
+          s2 = fma2(x2[i], x2[i], s2);
+          s3 = fma2(y2[i], y2[i], s3);
+        }
+        float s0, s1;
+        unpack2(add2(s2, s3), s0, s1);
+        float sum = in ? s0 + s1 : 0.f;
+        sum += __shfl_xor_sync(mask, sum, 1);
+        sum += __shfl_xor_sync(mask, sum, 2);
+        if (lanes > 4) sum += __shfl_xor_sync(mask, sum, 4);
+        if (lanes > 8) sum += __shfl_xor_sync(mask, sum, 8);
+        const float f = rsqrtf(fmaf(sum, a.inv_dh, a.rope.eps));
+        const uint64_t f2 = pack2(f, f);
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 gx = __ldg(reinterpret_cast<const float4*>(gain + lo + i));
-          const float4 gy = __ldg(reinterpret_cast<const float4*>(gain + lo + step + i));
-          x[i] *= f * gx.x; x[i + 1] *= f * gx.y; x[i + 2] *= f * gx.z; x[i + 3] *= f * gx.w;
-          y[i] *= f * gy.x; y[i + 1] *= f * gy.y; y[i + 2] *= f * gy.z; y[i + 3] *= f * gy.w;
+        for (int i = 0; i < 4; i += 2) {
+          const ulonglong2 gx = __ldg(reinterpret_cast<const ulonglong2*>(gain + lo + 2 * i));
+          const ulonglong2 gy = __ldg(reinterpret_cast<const ulonglong2*>(gain + lo + step + 2 * i));
+          x2[i] = mul2(x2[i], mul2(f2, gx.x));
+          x2[i + 1] = mul2(x2[i + 1], mul2(f2, gx.y));
+          y2[i] = mul2(y2[i], mul2(f2, gy.x));
+          y2[i + 1] = mul2(y2[i + 1], mul2(f2, gy.y));
         }
       }
       if (turns) {
+        const float* cs = table + t.row * rot + lo;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float z = x[i] * cs[i] - y[i] * sn[i];
-          y[i] = y[i] * cs[i] + x[i] * sn[i];
-          x[i] = z;
+        for (int i = 0; i < 4; i += 2) {
+          const ulonglong2 c2 = *reinterpret_cast<const ulonglong2*>(cs + 2 * i);
+          const float4 s4 = *reinterpret_cast<const float4*>(cs + half + 2 * i);
+          const uint64_t sn[2] = {pack2(s4.x, s4.y), pack2(s4.z, s4.w)}, neg[2] = {pack2(-s4.x, -s4.y), pack2(-s4.z, -s4.w)};
+          const uint64_t cc[2] = {c2.x, c2.y};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint64_t z = fma2(x2[i + j], cc[j], mul2(y2[i + j], neg[j]));
+            y2[i + j] = fma2(y2[i + j], cc[j], mul2(x2[i + j], sn[j]));
+            x2[i + j] = z;
+          }
         }
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        unpack2(x2[i], x[2 * i], x[2 * i + 1]);
+        unpack2(y2[i], y[2 * i], y[2 * i + 1]);
+      }
     }
-    if (kind == 0) {
-      if (live && has && in && seq >= 0) {
-        T* o = static_cast<T*>(a.out.data) + row * a.out.row_stride + head * a.out.head_stride + lo;
+    if (t.kind == 0) {
+      if (in && token != -2) {
+        T* o = static_cast<T*>(a.out.data) + (a.row0 + r0 + t.row) * a.out.row_stride + t.head * a.out.head_stride + lo;
         store8<DT, VEC>(o, x);
         store8<DT, VEC>(o + step, y);
       }
       continue;
     }
-    const bool store = live && has && in && token >= 0;
-    const int64_t e = ((static_cast<int64_t>(token / kPage) * hkv + head) * kPage + token % kPage) * dh + lo;
-    void* pool = kind == 1 ? a.pool.k : a.pool.v;
+    const bool store = in && token >= 0;
+    const int64_t e = ((static_cast<int64_t>(token / kPage) * hkv + t.head) * kPage + token % kPage) * dh + lo;
+    void* pool = t.kind == 1 ? a.pool.k : a.pool.v;
     if constexpr (!Q8) {
       if (store) {
         store8<MK_F16, true>(static_cast<__half*>(pool) + e, x);
@@ -142,8 +230,8 @@ __global__ void __launch_bounds__(kBlock) rope_write_kernel(const __grid_constan
       }
     } else {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const float* z = half ? y : x;
+      for (int side = 0; side < 2; ++side) {
+        const float* z = side ? y : x;
         float m = fabsf(z[0]);
 #pragma unroll
         for (int j = 1; j < 8; ++j) m = fmaxf(m, fabsf(z[j]));
@@ -153,9 +241,9 @@ __global__ void __launch_bounds__(kBlock) rope_write_kernel(const __grid_constan
         uint32_t w[2];
         q8_codes<8>(z, d, m, w);
         if (store) {
-          const int64_t at = e + half * step;
+          const int64_t at = e + side * step;
           *reinterpret_cast<uint2*>(static_cast<int8_t*>(pool) + at) = make_uint2(w[0], w[1]);
-          if ((c & 3) == 0) static_cast<__half*>(kind == 1 ? a.pool.k_scale : a.pool.v_scale)[at / 32] = __float2half_rn(d);
+          if ((c & 3) == 0) static_cast<__half*>(t.kind == 1 ? a.pool.k_scale : a.pool.v_scale)[at / 32] = __float2half_rn(d);
         }
       }
     }
@@ -163,10 +251,10 @@ __global__ void __launch_bounds__(kBlock) rope_write_kernel(const __grid_constan
 }
 
 using Kernel = void (*)(const RopeArgs);
-template <int DT>
+template <int DT, int PER>
 Kernel pick(bool q8, bool vec) {
-  return q8 ? (vec ? rope_write_kernel<DT, true, true> : rope_write_kernel<DT, true, false>)
-            : (vec ? rope_write_kernel<DT, false, true> : rope_write_kernel<DT, false, false>);
+  return q8 ? (vec ? rope_write_kernel<DT, true, true, PER> : rope_write_kernel<DT, true, false, PER>)
+            : (vec ? rope_write_kernel<DT, false, true, PER> : rope_write_kernel<DT, false, false, PER>);
 }
 
 }  // namespace
@@ -205,20 +293,29 @@ extern "C" mk_status mk_rope_write(const mk_kv_pool* pool, const mk_kv_rows* row
   if (heads > (1 << 20)) return MK_ERR_UNSUPPORTED;
   const bool vec = dense_vec(r->q, r->dtype) && dense_vec(r->out, r->dtype) && dense_vec(r->k, r->dtype) && dense_vec(r->v, r->dtype);
   const bool q8 = pool->kv_dtype == MK_KV_Q8;
-  const Kernel fn = r->dtype == MK_F32 ? pick<MK_F32>(q8, vec) : r->dtype == MK_F16 ? pick<MK_F16>(q8, vec) : pick<MK_BF16>(q8, vec);
-  RopeArgs a{*pool, *rows, r->q, r->out, r->k, r->v, p, r->parents, r->positions, r->hq, static_cast<int>(heads), 1, 0, 0, 0, 0};
+  RopeArgs a{*pool, *rows, r->q, r->out, r->k, r->v, p, r->parents, r->positions, r->hq, static_cast<int>(heads), 1, 0, 1, 0, 0, 0, 0, 1.f / static_cast<float>(pool->dh)};
   a.lanes_log2 = pool->dh == 64 ? 2 : pool->dh == 128 ? 3 : 4;
   const int groups = kBlock >> a.lanes_log2;  // of a block
-  // One head a group while that is no more than four blocks an SM; with more rows four heads.
-  a.per = rows->n_rows * heads <= 600ll * groups ? 1 : 4;
-  a.row_groups = static_cast<uint32_t>((heads + a.per - 1) / a.per);
-  const int64_t slab = (1ll << 30) / (a.row_groups << a.lanes_log2);  // threads of one launch stay below 2^31
+  // A head a group while that makes no more than four blocks an SM; with more rows four heads, of as many rows as
+  // they come to.
+  const bool many = rows->n_rows * heads > 608ll * groups;
+  const int per = many ? kPer : 1;
+  a.block_heads = static_cast<int>(heads < per * groups ? heads : per * groups);
+  a.block_rows = per * groups / a.block_heads;
+  if (!many) a.block_rows = 1;
+  if (a.block_rows > kMaxRows) a.block_rows = kMaxRows;
+  a.head_blocks = static_cast<int>((heads + a.block_heads - 1) / a.block_heads);
+  a.heads_inv = (1 << 20) / a.block_heads + 1;  // exact: pairs < 512, heads < 1024
+  const Kernel fn = many ? (r->dtype == MK_F32 ? pick<MK_F32, kPer>(q8, vec) : r->dtype == MK_F16 ? pick<MK_F16, kPer>(q8, vec) : pick<MK_BF16, kPer>(q8, vec))
+                         : (r->dtype == MK_F32 ? pick<MK_F32, 1>(q8, vec) : r->dtype == MK_F16 ? pick<MK_F16, 1>(q8, vec) : pick<MK_BF16, 1>(q8, vec));
+  const int64_t slab = (1ll << 30) / a.head_blocks / a.block_rows * a.block_rows;  // blocks of one launch stay below 2^31
   for (int64_t r0 = 0; r0 < rows->n_rows; r0 += slab) {
     a.row0 = static_cast<int>(r0);
     a.n = static_cast<int>(rows->n_rows - r0 < slab ? rows->n_rows - r0 : slab);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.n) * a.row_groups + groups - 1) / groups));
+    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>((a.n + a.block_rows - 1) / a.block_rows) * a.head_blocks));
     cfg.blockDim = dim3(kBlock);
+    cfg.dynamicSmemBytes = sizeof(float) * a.block_rows * p.rot;
     cfg.stream = static_cast<cudaStream_t>(stream);
     if (cudaLaunchKernelEx(&cfg, fn, a) != cudaSuccess) {
       cudaGetLastError();

@@ -6,8 +6,9 @@
 // their parents, so one scan of the nodes finds it.
 //
 // Two launches: tree_top takes the maximum of a row's part per block, tree_walk (launched
-// early) joins the parts and walks, a block per sequence. Bound by the logits' bytes when
-// the vocabulary is large, by the two launches when it is small.
+// early) joins the parts and walks, a block per sequence. Where a sequence's logits are few,
+// tree_small does both in one launch. Bound by the logits' bytes when the vocabulary is large,
+// by the launches when it is small.
 #include <climits>
 
 #include <cuda_runtime.h>
@@ -20,7 +21,8 @@ namespace {
 
 constexpr int kBlock = 256;
 constexpr int kMaxSplit = 128;  // parts of a row
-constexpr int kSpan = 2048;     // a part is a multiple of so many logits
+constexpr int kSpan = 2048;     // logits of a part, at least
+constexpr int64_t kSmall = 1 << 16;
 
 // A logit and its index as one number that grows with the logit and falls with the
 // index; a NaN is above every number.
@@ -55,45 +57,61 @@ struct TreeArgs {
   int32_t* greedy;  // [rows]
 };
 
+// The largest of logits [i0, end) that a thread of `threads` sees, 16 bytes at a time from its own first ones on, as a key
+// (0: it sees none). Ascending, so that the first of equal ones stays.
+template <int DT, bool VEC>
+__device__ __forceinline__ uint64_t scan(const typename Elem<DT>::T* x, int begin, int end, int thread, int threads) {
+  using T = typename Elem<DT>::T;
+  constexpr int kV = 16 / sizeof(T), kDeep = 4;
+  const int step = threads * kV, i0 = begin + thread * kV;
+  float best = -INFINITY;
+  int at = INT_MAX;
+  bool nan = false;
+  auto see = [&](float y, int i) {
+    if (!(y <= best)) {  // larger, or a NaN
+      nan |= y != y;
+      best = y;
+      at = i;
+    }
+  };
+  auto get = [&](int j, float* y) {
+    if (VEC) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(x + j));
+#pragma unroll
+      for (int k = 0; k < kV; ++k) y[k] = Elem<DT>::get(reinterpret_cast<const T*>(&w)[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kV; ++k) y[k] = Elem<DT>::get(x[j + k]);
+    }
+  };
+  int i = i0;
+  for (; i + (kDeep - 1) * step + kV <= end; i += kDeep * step) {
+    float y[kDeep][kV];
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) get(i + u * step, y[u]);
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u)
+#pragma unroll
+      for (int k = 0; k < kV; ++k) see(y[u][k], i + u * step + k);
+  }
+  for (; i + kV <= end; i += step) {
+    float y[kV];
+    get(i, y);
+#pragma unroll
+    for (int k = 0; k < kV; ++k) see(y[k], i + k);
+  }
+  for (; i < end; ++i) see(Elem<DT>::get(x[i]), i);
+  return nan ? kNan : at != INT_MAX ? key_of(best, at) : i0 < end ? key_of(-INFINITY, i0) : 0;
+}
+
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kBlock) tree_top(const __grid_constant__ TreeArgs a) {
   using T = typename Elem<DT>::T;
   __shared__ uint64_t top[kBlock / 32];
   for (int row = blockIdx.y; row < a.rows.n_rows; row += gridDim.y) {
-    const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
-    const int end = min(a.vocab, (static_cast<int>(blockIdx.x) + 1) * a.span);
-    float best = -INFINITY;
-    int at = INT_MAX;
-    bool nan = false;
-    auto see = [&](float y, int i) {
-      if (!(y <= best)) {  // larger, or a NaN
-        nan |= y != y;
-        best = y;
-        at = i;
-      }
-    };
-    // ascending, eight at a time: the first of equal ones stays
-    int i = static_cast<int>(blockIdx.x) * a.span + threadIdx.x * 8;
-    const int i0 = i;
-    constexpr int kStep = kBlock * 8;
-    auto eight = [&](int j) {
-      float y[8];
-      load8<DT, VEC>(x + j, y);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) see(y[k], j + k);
-    };
-    for (; i + 3 * kStep + 8 <= end; i += 4 * kStep) {
-      float y[4][8];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) load8<DT, VEC>(x + i + u * kStep, y[u]);
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) see(y[u][k], i + u * kStep + k);
-    }
-    for (; i + 8 <= end; i += kStep) eight(i);
-    for (; i < end; ++i) see(Elem<DT>::get(x[i]), i);
-    uint64_t key = nan ? kNan : at != INT_MAX ? key_of(best, at) : i0 < end ? key_of(-INFINITY, i0) : 0;
+    const int begin = static_cast<int>(blockIdx.x) * a.span;
+    uint64_t key = scan<DT, VEC>(static_cast<const T*>(a.logits) + row * a.row_stride, begin, min(a.vocab, begin + a.span),
+                                 threadIdx.x, kBlock);
     key = warp_max(key);
     if ((threadIdx.x & 31) == 0) top[threadIdx.x / 32] = key;
     __syncthreads();
@@ -106,39 +124,31 @@ __global__ void __launch_bounds__(kBlock) tree_top(const __grid_constant__ TreeA
   asm volatile("griddepcontrol.launch_dependents;");
 }
 
-__global__ void __launch_bounds__(kBlock) tree_walk(const __grid_constant__ TreeArgs a) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const SeqView v = seq_view(a.rows, blockIdx.x);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there from here on
-  for (int j = warp; j < v.q_len; j += kBlock / 32) {
-    uint64_t key = 0;
-    for (int p = lane; p < a.split; p += 32) {
-      const uint64_t o = a.part[static_cast<int64_t>(v.r0 + j) * a.split + p];
-      key = o > key ? o : key;
-    }
-    key = warp_max(key);
-    if (lane == 0) a.greedy[v.r0 + j] = token_of(key);
-  }
-  __syncthreads();
-  if (warp) return;
+// A warp walks a sequence's tree, 32 nodes at a time; greedy: its nodes' greedy tokens.
+template <class Greedy>
+__device__ __forceinline__ void walk(const TreeArgs& a, const SeqView& v, int seq, int lane, Greedy greedy) {
   int count = 0, cur = 0, want = -1;
   auto reach = [&](int node) {
     cur = node;
-    want = a.greedy[v.r0 + node];
+    want = greedy(node);
     if (lane == 0) {
       a.path[v.r0 + count] = node;
       a.emitted[v.r0 + count] = want;
     }
     ++count;
   };
-  if (v.q_len) reach(0);
-  for (int j0 = 1; j0 < v.q_len; j0 += 32) {
-    const int j = j0 + lane;
-    int parent = -1, tok = -1;
+  int parent = -1, tok = -1;
+  auto fetch = [&](int j) {
     if (j < v.q_len) {
       parent = a.parents ? parent_of(a.parents + v.r0, j) : j - 1;
       tok = __ldg(a.tokens + v.r0 + j);
     }
+  };
+  fetch(1 + lane);
+  if (v.q_len) reach(0);
+  for (int j0 = 1; j0 < v.q_len; j0 += 32) {
+    const int j = j0 + lane;
+    if (j0 > 1) fetch(j);
     for (;;) {  // (each hit lies behind the one before: no more than 32)
       const uint32_t hit = __ballot_sync(0xffffffffu, j < v.q_len && parent == cur && want >= 0 && tok == want);
       if (!hit) break;
@@ -149,12 +159,47 @@ __global__ void __launch_bounds__(kBlock) tree_walk(const __grid_constant__ Tree
     a.path[v.r0 + j] = -1;
     a.emitted[v.r0 + j] = -1;
   }
-  if (lane == 0) a.count[blockIdx.x] = count;
+  if (lane == 0) a.count[seq] = count;
 }
 
-// Parts of a row: about four blocks an SM over all rows, each of at least kSpan logits.
+constexpr int kWalkBlock = 512, kNear = 1024;  // nodes whose greedy tokens are kept in shared memory
+
+__global__ void __launch_bounds__(kWalkBlock) tree_walk(const __grid_constant__ TreeArgs a) {
+  __shared__ int near[kNear];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const SeqView v = seq_view(a.rows, blockIdx.x);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there from here on
+  for (int j = warp; j < v.q_len; j += kWalkBlock / 32) {
+    uint64_t key = 0;
+    for (int p = lane; p < a.split; p += 32) {
+      const uint64_t o = a.part[static_cast<int64_t>(v.r0 + j) * a.split + p];
+      key = o > key ? o : key;
+    }
+    key = warp_max(key);
+    if (lane == 0) (j < kNear ? near[j] : a.greedy[v.r0 + j]) = token_of(key);
+  }
+  __syncthreads();
+  if (warp == 0) walk(a, v, blockIdx.x, lane, [&](int j) { return j < kNear ? near[j] : a.greedy[v.r0 + j]; });
+}
+
+// A block takes a whole sequence, a warp a row at a time.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kWalkBlock) tree_small(const __grid_constant__ TreeArgs a) {
+  using T = typename Elem<DT>::T;
+  __shared__ int near[kNear];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const SeqView v = seq_view(a.rows, blockIdx.x);
+  for (int j = warp; j < v.q_len; j += kWalkBlock / 32) {
+    const uint64_t key = warp_max(scan<DT, VEC>(static_cast<const T*>(a.logits) + (v.r0 + j) * a.row_stride, 0, a.vocab, lane, 32));
+    if (lane == 0) (j < kNear ? near[j] : a.greedy[v.r0 + j]) = token_of(key);
+  }
+  __syncthreads();
+  if (warp == 0) walk(a, v, blockIdx.x, lane, [&](int j) { return j < kNear ? near[j] : a.greedy[v.r0 + j]; });
+}
+
+// Parts of a row: about eight blocks an SM over all rows, each of at least kSpan logits.
 int split_of(int n_rows, int vocab) {
-  const int64_t most = (static_cast<int64_t>(vocab) + kSpan - 1) / kSpan, want = (608 + n_rows - 1) / (n_rows > 0 ? n_rows : 1);
+  const int64_t most = (static_cast<int64_t>(vocab) + kSpan - 1) / kSpan, want = (1216 + n_rows - 1) / (n_rows > 0 ? n_rows : 1);
   const int64_t n = want < most ? want : most;
   return static_cast<int>(n < 1 ? 1 : n > kMaxSplit ? kMaxSplit : n);
 }
@@ -163,6 +208,13 @@ int64_t part_bytes(int n_rows, int vocab) { return (static_cast<int64_t>(n_rows)
 template <int DT>
 cudaError_t launch(const TreeArgs& a, bool vec, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
+  // One launch while the rows of a sequence (as many as max_q says) hold no more logits than kSmall.
+  if (static_cast<int64_t>(a.rows.max_q) * a.vocab <= kSmall) {
+    cfg.gridDim = dim3(a.rows.n_seqs);
+    cfg.blockDim = dim3(kWalkBlock);
+    cfg.stream = stream;
+    return cudaLaunchKernelEx(&cfg, vec ? tree_small<DT, true> : tree_small<DT, false>, a);
+  }
   cfg.gridDim = dim3(a.split, a.rows.n_rows < 65535 ? a.rows.n_rows : 65535);
   cfg.blockDim = dim3(kBlock);
   cfg.stream = stream;
@@ -172,6 +224,7 @@ cudaError_t launch(const TreeArgs& a, bool vec, cudaStream_t stream) {
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(a.rows.n_seqs);
+  cfg.blockDim = dim3(kWalkBlock);
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, tree_walk, a);

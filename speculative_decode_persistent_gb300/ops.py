@@ -112,6 +112,8 @@ _FORMATS = (("@4P4i", mk_kv_pool), ("@3P4i", mk_kv_rows), ("@Pqq", mk_dense), ("
             ("@PqqPqqPqqPqqiiPPPifPP", mk_rope_args), ("@PPPqiiPPPPQ", mk_tree_args), ("@4P4iiq", mk_kv_layers))
 _POOL, _ROWS, _DENSE, _ARGS, _ROPE, _TREE, _LAYERS = (struct.Struct(f).pack for f, _ in _FORMATS)
 assert all(struct.calcsize(f) <= ctypes.sizeof(t) for f, t in _FORMATS)
+_tree_work_bytes = _fast.mk_tree_work_bytes
+_tree_work_bytes.restype, _tree_work_bytes.argtypes = sz, [i32, i32]
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _HALF = (torch.float16, torch.int16)
 
@@ -163,23 +165,32 @@ class KVLayers:
     __slots__ = ("tensors", "device", "q8", "n_layers", "n_pages", "hkv", "dh", "c")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        if k.dim() != 5 or k.shape[0] == 0 or v.shape != k.shape:
+        shape, dtype, device, step = k.shape, k.dtype, k.device, k.stride()
+        if len(shape) != 5 or v.shape != shape or shape[0] == 0 or shape[3] != PAGE_TOKENS or v.dtype != dtype:
             _refuse("KVLayers (k and v are [layers][pages][kv heads][16][head dim] of one type)")
-        n = k.shape[0]
-        scales = [s for s in (k_scale, v_scale) if s is not None]
-        if any(s.dim() != 5 or s.shape[0] != n for s in scales):
-            _refuse("KVLayers (scales [layers][pages][kv heads][16][head dim / 32])")
-        first = KVPool(k[0], v[0], *(None if s is None else s[0] for s in (k_scale, v_scale)))
-        stride = k.stride(0) if n > 1 else 0
-        if n > 1 and (v.stride(0) != stride or any(s.stride(0) * 32 != stride for s in scales) or stride % 256 or
-                      stride < k[0].numel()):
-            _refuse("KVLayers (layers of all tensors equally far apart)")
+        n, pages, heads, _, dh = shape
+        inner, layer = (heads * PAGE_TOKENS * dh, PAGE_TOKENS * dh, dh, 1), step[0]
+        if step[1:] != inner or v.stride() != step or n > 1 and (layer < pages * inner[0] or layer % 256):
+            _refuse("KVLayers (contiguous layers, equally far apart in all tensors)")
+        if v.device != device:
+            _refuse("KVLayers (one device)")
+        self.q8 = dtype == torch.int8
+        if self.q8:
+            blocks = dh // 32
+            want, at = (n, pages, heads, PAGE_TOKENS, blocks), (heads * PAGE_TOKENS * blocks, PAGE_TOKENS * blocks, blocks, 1)
+            for s in (k_scale, v_scale):
+                if s is None or s.dtype not in _HALF or s.shape != want or s.device != device:
+                    _refuse("KVLayers (an int8 pool needs binary16 scales [layers][pages][kv heads][16][head dim / 32])")
+                if s.stride()[1:] != at or n > 1 and s.stride(0) * 32 != layer:
+                    _refuse("KVLayers (contiguous layers, equally far apart in all tensors)")
+            ks, vs, kind = k_scale.data_ptr(), v_scale.data_ptr(), MK_KV_Q8
+        else:
+            if dtype not in _HALF or k_scale is not None or v_scale is not None:
+                _refuse("KVLayers (binary16, or int8 codes with scales)")
+            ks, vs, kind = 0, 0, MK_KV_F16
         self.tensors = (k, v, k_scale, v_scale)
-        self.device, self.q8, self.n_layers = first.device, first.q8, n
-        self.n_pages, self.hkv, self.dh = first.n_pages, first.hkv, first.dh
-        ks, vs = (0, 0) if not scales else (k_scale.data_ptr(), v_scale.data_ptr())
-        self.c = _LAYERS(k.data_ptr(), v.data_ptr(), ks, vs, MK_KV_Q8 if self.q8 else MK_KV_F16, self.n_pages, self.hkv, self.dh,
-                         n, stride)
+        self.device, self.n_layers, self.n_pages, self.hkv, self.dh = device, n, pages, heads, dh
+        self.c = _LAYERS(k.data_ptr(), v.data_ptr(), ks, vs, kind, pages, heads, dh, n, layer if n > 1 else 0)
 
 
 class Rope:
@@ -453,13 +464,12 @@ def tree_accept(rows: KVRows, parents, tokens, logits):
     if tokens is None:
         _refuse("tree_accept (tokens)")
     par, tok = _index(parents, n, device, "tree_accept parents"), _index(tokens, n, device, "tree_accept tokens")
-    out = torch.empty(2 * n + rows.n_seqs, dtype=torch.int32, device=device)
-    path, emitted, count = out[:n], out[n:2 * n], out[2 * n:]
-    nbytes = lib.mk_tree_work_bytes(n, vocab)
+    path, emitted = torch.empty(n, dtype=torch.int32, device=device), torch.empty(n, dtype=torch.int32, device=device)
+    count = torch.empty(rows.n_seqs, dtype=torch.int32, device=device)
+    nbytes = _tree_work_bytes(n, vocab)
     work = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    at = out.data_ptr()
-    args = _TREE(par, tok, logits.data_ptr(), logits.stride(0), vocab, DTYPES[logits.dtype], at, at + 8 * n, at + 4 * n,
-                 work.data_ptr(), nbytes)
+    args = _TREE(par, tok, logits.data_ptr(), logits.stride(0), vocab, DTYPES[logits.dtype], path.data_ptr(), count.data_ptr(),
+                 emitted.data_ptr(), work.data_ptr(), nbytes)
     _run(device.index, "mk_tree_accept", _tree_accept, rows._at(n), args)
     return path, count, emitted
 
