@@ -15,10 +15,11 @@
 // eight that they are paired with per lane (dims that are not turned are paired
 // the same way): the turn stays in the thread, the norm's sum takes up to four
 // shuffles, and four lanes hold two 32-dim q8 blocks (r is a multiple of 64). Such a
-// group of lanes takes PER heads, whose loads are all issued before anything else: with
-// many rows four, of one or several rows of its block. The block's threads look its rows
-// up and make their sines and cosines once for all heads, in shared memory. Each thread
-// reads its 16 values of a head before it writes them: out may be q.
+// group of lanes takes one head, whose gains stay in registers, of PER rows at a time and
+// reads the next ones ahead. The block's threads look all of its rows up and make their
+// sines and cosines once for all heads, in shared memory; with many rows there are as many
+// blocks as are resident, so that this is paid once. Each thread reads its 16 values of a
+// head before it writes them: out may be q.
 #include <cmath>
 
 #include <cuda_runtime.h>
@@ -31,8 +32,11 @@ namespace ops {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kMaxRows = 16;  // of a block
-constexpr int kPer = 4;       // heads of a group, with many rows
+// Rows of a group at a time, where there are many. (8,192 rows of 32 heads of 256, bf16, four rows and two blocks an SM: 52 us; two
+// and three: 56; two and four, nothing read ahead: 62; one and six: 74. What is on its way counts.)
+constexpr int kPer = 4, kPerF32 = 2;
+constexpr int kMaxRows = 256;  // of a block
+constexpr int kTable = 40960;  // bytes of its sines and cosines, at most (84 rows of 64 dims take 22 KB)
 
 struct RopeArgs {
   mk_kv_pool pool;
@@ -41,8 +45,8 @@ struct RopeArgs {
   mk_rope rope;
   const int32_t* parents;
   const int32_t* positions;
-  int hq, heads;                   // heads of q; of q, k and v
-  int block_rows, block_heads, head_blocks, heads_inv;  // a block's rows and heads; blocks per rows; 2^20 / block_heads + 1
+  int hq, heads;                                       // heads of q; of q, k and v
+  int block_heads, head_blocks, group_rows, batches;   // a block's heads; blocks per rows; groups per head; times PER rows
   int lanes_log2, row0, n;         // lanes of a group; rows [row0, row0 + n) of this launch
   float inv_dh;
 };
@@ -74,15 +78,28 @@ __device__ __forceinline__ void values8(const Raw<DT>& r, float* x) {
   for (int i = 0; i < 8; ++i) x[i] = Elem<DT>::get(t[i]);
 }
 
+// Eight values rounded and stored, two a conversion.
+template <int DT, bool VEC>
+__device__ __forceinline__ void put8(typename Elem<DT>::T* p, const float* x) {
+  if constexpr (DT == MK_F32 || !VEC) {
+    store8<DT, VEC>(p, x);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = DT == MK_F16 ? pack_half2(x[2 * i], x[2 * i + 1]) : pack_bf162(x[2 * i], x[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 template <int DT, bool Q8, bool VEC, int PER>
-__global__ void __launch_bounds__(kBlock, PER == 1 || DT == MK_F32 || !VEC ? 2 : 4) rope_write_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kBlock, 2) rope_write_kernel(const __grid_constant__ RopeArgs a) {
   using T = typename Elem<DT>::T;
   __shared__ int row_token[kMaxRows], row_pos[kMaxRows];  // token: -2 for rows of no sequence
-  extern __shared__ __align__(16) float table[];          // [block_rows][2][rot / 2]: cosines, sines
-  const int tid = threadIdx.x, lanes = 1 << a.lanes_log2, c = tid & (lanes - 1), groups = kBlock >> a.lanes_log2;
+  extern __shared__ __align__(16) float table[];          // [rows of the block][2][rot / 2]: cosines, sines
+  const int tid = threadIdx.x, lanes = 1 << a.lanes_log2, c = tid & (lanes - 1), group = tid >> a.lanes_log2;
   const int rb = static_cast<int>(blockIdx.x) / a.head_blocks, h0 = (static_cast<int>(blockIdx.x) - rb * a.head_blocks) * a.block_heads;
-  const int r0 = rb * a.block_rows;  // the block's first row, of this launch
-  const int n_rows = min(a.block_rows, a.n - r0), n_heads = min(a.block_heads, a.heads - h0);
+  const int r0 = rb * a.batches * a.group_rows * PER;  // the block's first row, of this launch
+  const int n_rows = min(a.batches * a.group_rows * PER, a.n - r0);
   const int lane = tid & 31;
   const uint32_t mask = ((1u << lanes) - 1) << (lane & ~(lanes - 1));
   const int dh = a.pool.dh, rot = a.rope.rot, half = rot / 2, hkv = a.pool.hkv;
@@ -92,32 +109,31 @@ __global__ void __launch_bounds__(kBlock, PER == 1 || DT == MK_F32 || !VEC ? 2 :
   const bool turns = ci < turned;
   const int lo = turns ? 8 * ci : rot + 8 * (ci - turned), step = turns ? half : (dh - rot) / 2;
 
-  // the group's heads: pairs of a row and a head of the block, PER at a time
-  struct Item {
-    int row, kind, head;  // row of the block, -1: none; kind 0 q, 1 k, 2 v
+  // the group's head and first row (the others lie group_rows apart); groups behind the last head have none
+  const int row_lane = group / a.block_heads, g = h0 + group - row_lane * a.block_heads;
+  const int first = row_lane < a.group_rows && g < a.heads ? row_lane : n_rows;
+  const int kind = g < a.hq ? 0 : g < a.hq + hkv ? 1 : 2;  // q, k, v
+  const int head = kind == 0 ? g : kind == 1 ? g - a.hq : g - a.hq - hkv;
+  const mk_dense& src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+  const T* p = static_cast<const T*>(src.data) + (a.row0 + r0 + first) * src.row_stride + head * src.head_stride + lo;
+  const int64_t next = a.group_rows * src.row_stride;
+  struct Batch {
+    Raw<DT> x[PER], y[PER];
   };
-  auto item = [&](int p) {
-    const int r = a.block_rows == 1 ? 0 : (p * a.heads_inv) >> 20, h = p - r * a.block_heads;
-    Item t;
-    t.row = r < n_rows && h < n_heads ? r : -1;
-    const int g = h0 + (t.row < 0 ? 0 : h);
-    t.kind = g < a.hq ? 0 : g < a.hq + hkv ? 1 : 2;
-    t.head = t.kind == 0 ? g : t.kind == 1 ? g - a.hq : g - a.hq - hkv;
+  auto fetch = [&](int row) {  // of the group's next rows, from `row` on
+    Batch t;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      if (row + u * a.group_rows >= n_rows) break;
+      t.x[u] = fetch8<DT, VEC>(p);
+      t.y[u] = fetch8<DT, VEC>(p + step);
+      p += next;
+    }
     return t;
   };
-  Raw<DT> x0[PER], y0[PER];
-  const int first = tid >> a.lanes_log2;
-#pragma unroll
-  for (int u = 0; u < PER; ++u) {
-    const Item t = item(first + u * groups);
-    if (t.row < 0) continue;
-    const mk_dense& src = t.kind == 0 ? a.q : t.kind == 1 ? a.k : a.v;
-    const T* p = static_cast<const T*>(src.data) + (a.row0 + r0 + t.row) * src.row_stride + t.head * src.head_stride + lo;
-    x0[u] = fetch8<DT, VEC>(p);
-    y0[u] = fetch8<DT, VEC>(p + step);
-  }
-  if (tid < n_rows) {
-    const int row = a.row0 + r0 + tid;
+  Batch now = fetch(first);
+  for (int i = tid; i < n_rows; i += kBlock) {
+    const int row = a.row0 + r0 + i;
     SeqView v;
     const int seq = seq_of_row(a.rows, row, v);
     int token = -2, pos = 0;
@@ -132,8 +148,8 @@ __global__ void __launch_bounds__(kBlock, PER == 1 || DT == MK_F32 || !VEC ? 2 :
         for (int n = parent_of(a.parents + v.r0, node); n >= 0; n = parent_of(a.parents + v.r0, n)) ++pos;
       }
     }
-    row_token[tid] = token;
-    row_pos[tid] = pos;
+    row_token[i] = token;
+    row_pos[i] = pos;
   }
   __syncthreads();
   if (h0 < a.hq + hkv) {  // (a block of v alone turns nothing)
@@ -146,16 +162,25 @@ __global__ void __launch_bounds__(kBlock, PER == 1 || DT == MK_F32 || !VEC ? 2 :
       table[r * rot + half + j] = sn;
     }
   }
-  __syncthreads();
+  const float* const gain = kind == 0 ? a.rope.q_gain : kind == 1 ? a.rope.k_gain : nullptr;
+  uint64_t gx[4], gy[4];
+  if (gain) {
 #pragma unroll
-  for (int u = 0; u < PER; ++u) {
-    const Item t = item(first + u * groups);
-    if (t.row < 0) continue;  // (whole groups)
-    const int token = row_token[t.row];
+    for (int i = 0; i < 4; i += 2) {
+      const ulonglong2 g0 = __ldg(reinterpret_cast<const ulonglong2*>(gain + lo + 2 * i));
+      const ulonglong2 g1 = __ldg(reinterpret_cast<const ulonglong2*>(gain + lo + step + 2 * i));
+      gx[i] = g0.x; gx[i + 1] = g0.y;
+      gy[i] = g1.x; gy[i + 1] = g1.y;
+    }
+  }
+  __syncthreads();
+  T* const out = static_cast<T*>(a.out.data) + (a.row0 + r0) * a.out.row_stride + head * a.out.head_stride + lo;
+  auto turn = [&](const Raw<DT>& rx, const Raw<DT>& ry, int row) {
+    const int token = row_token[row];
     float x[8], y[8];
-    values8<DT>(x0[u], x);
-    values8<DT>(y0[u], y);
-    if (t.kind < 2) {
+    values8<DT>(rx, x);
+    values8<DT>(ry, y);
+    if (kind < 2) {
       // two values an instruction
       uint64_t x2[4], y2[4];
 #pragma unroll
@@ -163,7 +188,6 @@ __global__ void __launch_bounds__(kBlock, PER == 1 || DT == MK_F32 || !VEC ? 2 :
         x2[i] = pack2(x[2 * i], x[2 * i + 1]);
         y2[i] = pack2(y[2 * i], y[2 * i + 1]);
       }
-      const float* gain = t.kind == 0 ? a.rope.q_gain : a.rope.k_gain;
       if (gain) {
         uint64_t s2 = mul2(x2[0], x2[0]), s3 = mul2(y2[0], y2[0]);
 #pragma unroll
@@ -181,17 +205,13 @@ __global__ void __launch_bounds__(kBlock, PER == 1 || DT == MK_F32 || !VEC ? 2 :
         const float f = rsqrtf(fmaf(sum, a.inv_dh, a.rope.eps));
         const uint64_t f2 = pack2(f, f);
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          const ulonglong2 gx = __ldg(reinterpret_cast<const ulonglong2*>(gain + lo + 2 * i));
-          const ulonglong2 gy = __ldg(reinterpret_cast<const ulonglong2*>(gain + lo + step + 2 * i));
-          x2[i] = mul2(x2[i], mul2(f2, gx.x));
-          x2[i + 1] = mul2(x2[i + 1], mul2(f2, gx.y));
-          y2[i] = mul2(y2[i], mul2(f2, gy.x));
-          y2[i + 1] = mul2(y2[i + 1], mul2(f2, gy.y));
+        for (int i = 0; i < 4; ++i) {
+          x2[i] = mul2(x2[i], mul2(f2, gx[i]));
+          y2[i] = mul2(y2[i], mul2(f2, gy[i]));
         }
       }
       if (turns) {
-        const float* cs = table + t.row * rot + lo;
+        const float* cs = table + row * rot + lo;
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
           const ulonglong2 c2 = *reinterpret_cast<const ulonglong2*>(cs + 2 * i);
@@ -212,21 +232,21 @@ __global__ void __launch_bounds__(kBlock, PER == 1 || DT == MK_F32 || !VEC ? 2 :
         unpack2(y2[i], y[2 * i], y[2 * i + 1]);
       }
     }
-    if (t.kind == 0) {
+    if (kind == 0) {
       if (in && token != -2) {
-        T* o = static_cast<T*>(a.out.data) + (a.row0 + r0 + t.row) * a.out.row_stride + t.head * a.out.head_stride + lo;
-        store8<DT, VEC>(o, x);
-        store8<DT, VEC>(o + step, y);
+        T* o = out + row * a.out.row_stride;
+        put8<DT, VEC>(o, x);
+        put8<DT, VEC>(o + step, y);
       }
-      continue;
+      return;
     }
     const bool store = in && token >= 0;
-    const int64_t e = ((static_cast<int64_t>(token / kPage) * hkv + t.head) * kPage + token % kPage) * dh + lo;
-    void* pool = t.kind == 1 ? a.pool.k : a.pool.v;
+    const int64_t e = ((static_cast<int64_t>(token / kPage) * hkv + head) * kPage + token % kPage) * dh + lo;
+    void* pool = kind == 1 ? a.pool.k : a.pool.v;
     if constexpr (!Q8) {
       if (store) {
-        store8<MK_F16, true>(static_cast<__half*>(pool) + e, x);
-        store8<MK_F16, true>(static_cast<__half*>(pool) + e + step, y);
+        put8<MK_F16, true>(static_cast<__half*>(pool) + e, x);
+        put8<MK_F16, true>(static_cast<__half*>(pool) + e + step, y);
       }
     } else {
 #pragma unroll
@@ -243,10 +263,18 @@ __global__ void __launch_bounds__(kBlock, PER == 1 || DT == MK_F32 || !VEC ? 2 :
         if (store) {
           const int64_t at = e + side * step;
           *reinterpret_cast<uint2*>(static_cast<int8_t*>(pool) + at) = make_uint2(w[0], w[1]);
-          if ((c & 3) == 0) static_cast<__half*>(t.kind == 1 ? a.pool.k_scale : a.pool.v_scale)[at / 32] = __float2half_rn(d);
+          if ((c & 3) == 0) static_cast<__half*>(kind == 1 ? a.pool.k_scale : a.pool.v_scale)[at / 32] = __float2half_rn(d);
         }
       }
     }
+  };
+  for (int row = first; row < n_rows; row += PER * a.group_rows) {  // (whole groups)
+    Batch then;
+    if (PER > 1 && row + PER * a.group_rows < n_rows) then = fetch(row + PER * a.group_rows);
+#pragma unroll
+    for (int u = 0; u < PER; ++u)
+      if (row + u * a.group_rows < n_rows) turn(now.x[u], now.y[u], row + u * a.group_rows);
+    if (PER > 1) now = then;
   }
 }
 
@@ -293,29 +321,32 @@ extern "C" mk_status mk_rope_write(const mk_kv_pool* pool, const mk_kv_rows* row
   if (heads > (1 << 20)) return MK_ERR_UNSUPPORTED;
   const bool vec = dense_vec(r->q, r->dtype) && dense_vec(r->out, r->dtype) && dense_vec(r->k, r->dtype) && dense_vec(r->v, r->dtype);
   const bool q8 = pool->kv_dtype == MK_KV_Q8;
-  RopeArgs a{*pool, *rows, r->q, r->out, r->k, r->v, p, r->parents, r->positions, r->hq, static_cast<int>(heads), 1, 0, 1, 0, 0, 0, 0, 1.f / static_cast<float>(pool->dh)};
+  RopeArgs a{*pool, *rows, r->q, r->out, r->k, r->v, p, r->parents, r->positions, r->hq, static_cast<int>(heads), 1, 1, 1, 1, 0, 0, 0, 1.f / static_cast<float>(pool->dh)};
   a.lanes_log2 = pool->dh == 64 ? 2 : pool->dh == 128 ? 3 : 4;
   const int groups = kBlock >> a.lanes_log2;  // of a block
-  // A head a group while that makes no more than four blocks an SM; with more rows four heads, of as many rows as
-  // they come to.
+  // A row a group while that makes no more than four blocks an SM.
   const bool many = rows->n_rows * heads > 608ll * groups;
-  const int per = many ? kPer : 1;
-  a.block_heads = static_cast<int>(heads < per * groups ? heads : per * groups);
-  a.block_rows = per * groups / a.block_heads;
-  if (!many) a.block_rows = 1;
-  if (a.block_rows > kMaxRows) a.block_rows = kMaxRows;
-  a.head_blocks = static_cast<int>((heads + a.block_heads - 1) / a.block_heads);
-  a.heads_inv = (1 << 20) / a.block_heads + 1;  // exact: pairs < 512, heads < 1024
-  const Kernel fn = many ? (r->dtype == MK_F32 ? pick<MK_F32, kPer>(q8, vec) : r->dtype == MK_F16 ? pick<MK_F16, kPer>(q8, vec) : pick<MK_BF16, kPer>(q8, vec))
+  a.head_blocks = static_cast<int>((heads + groups - 1) / groups);
+  a.block_heads = static_cast<int>((heads + a.head_blocks - 1) / a.head_blocks);
+  a.group_rows = groups / a.block_heads;
+  int block_rows = a.group_rows * (!many ? 1 : r->dtype == MK_F32 ? kPerF32 : kPer);
+  if (many) {  // as many batches a block as leave 304 blocks, two an SM, or, where shared memory ends before, a few times as many
+    const int64_t blocks = (rows->n_rows + block_rows - 1) / block_rows * a.head_blocks;
+    const int fit = kTable / 4 / (p.rot > 64 ? p.rot : 64) / block_rows, most = fit < kMaxRows / block_rows ? fit : kMaxRows / block_rows;
+    const int64_t waves = (blocks + 304ll * most - 1) / (304ll * most);
+    a.batches = static_cast<int>((blocks + 304 * waves - 1) / (304 * waves));
+    block_rows *= a.batches;
+  }
+  const Kernel fn = many ? (r->dtype == MK_F32 ? pick<MK_F32, kPerF32>(q8, vec) : r->dtype == MK_F16 ? pick<MK_F16, kPer>(q8, vec) : pick<MK_BF16, kPer>(q8, vec))
                          : (r->dtype == MK_F32 ? pick<MK_F32, 1>(q8, vec) : r->dtype == MK_F16 ? pick<MK_F16, 1>(q8, vec) : pick<MK_BF16, 1>(q8, vec));
-  const int64_t slab = (1ll << 30) / a.head_blocks / a.block_rows * a.block_rows;  // blocks of one launch stay below 2^31
+  const int64_t slab = (1ll << 30) / a.head_blocks / block_rows * block_rows;  // blocks of one launch stay below 2^31
   for (int64_t r0 = 0; r0 < rows->n_rows; r0 += slab) {
     a.row0 = static_cast<int>(r0);
     a.n = static_cast<int>(rows->n_rows - r0 < slab ? rows->n_rows - r0 : slab);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>((a.n + a.block_rows - 1) / a.block_rows) * a.head_blocks));
+    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>((a.n + block_rows - 1) / block_rows) * a.head_blocks));
     cfg.blockDim = dim3(kBlock);
-    cfg.dynamicSmemBytes = sizeof(float) * a.block_rows * p.rot;
+    cfg.dynamicSmemBytes = sizeof(float) * block_rows * p.rot;
     cfg.stream = static_cast<cudaStream_t>(stream);
     if (cudaLaunchKernelEx(&cfg, fn, a) != cudaSuccess) {
       cudaGetLastError();
