@@ -211,7 +211,7 @@ mk_status mk_rope_write(const mk_kv_pool* pool, const mk_kv_rows* rows, const mk
  * reached, -1 behind them; emitted [n_rows]: their greedy tokens, i.e. the accepted
  * drafts and one token more, -1 behind them; count [n_seqs]: their number (as
  * mk_step's counts; 0 for a sequence without rows). Rows of no sequence are left alone.
- * work: mk_tree_work_bytes() bytes, 256-byte aligned, as mk_attend's.
+ * work: mk_tree_work_bytes() bytes (0 for few logits), 256-byte aligned, as mk_attend's.
  * Errors: MK_ERR_INVALID, MK_ERR_UNSUPPORTED (vocab above 2^30), MK_ERR_CUDA.
  */
 typedef struct mk_tree_args {
@@ -227,7 +227,7 @@ typedef struct mk_tree_args {
     uint64_t work_bytes;
 } mk_tree_args;
 
-size_t mk_tree_work_bytes(int32_t n_rows, int32_t vocab);
+size_t mk_tree_work_bytes(const mk_kv_rows* rows, int32_t vocab);
 mk_status mk_tree_accept(const mk_kv_rows* rows, const mk_tree_args* args, void* stream);
 
 /* Layers of a pool that have their pages in common: pool is the first, and layer i

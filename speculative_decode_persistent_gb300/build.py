@@ -1,6 +1,7 @@
-"""In-tree build of libmk.so (nvcc, sm_103a only).
+"""In-tree build of libmk.so (nvcc, sm_103a only) and of the Python side of its
+operators, _bind (g++, against torch's headers).
 
-Each translation unit compiles in its own nvcc process, in parallel, then one
+Each translation unit compiles in its own process, in parallel, then one
 link step produces speculative_decode_persistent_gb300/libmk.so.
 """
 from __future__ import annotations
@@ -8,6 +9,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +20,8 @@ BUILD = os.path.join(HERE, "_build")
 SO = os.path.join(HERE, "libmk.so")
 SOURCES = ["mk_kernel.cu", "mk_api.cu", "mk_pack.cu", "ops/kv_rows.cu", "ops/kv_move.cu", "ops/rope_rows.cu", "ops/tree.cu",
            "ops/attend.cu", "ops/attend_f16.cu", "ops/attend_q8.cu", "ops/attend_tree_f16.cu", "ops/attend_tree_q8.cu"]
+BIND = os.path.join(HERE, "_bind.so")
+BIND_SOURCE = os.path.join(CSRC, "ops", "bind.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
@@ -29,6 +33,16 @@ def _stale(out: str, deps: list[str]) -> bool:
         return True
     t = os.path.getmtime(out)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _bind_command(out: str) -> list[str]:
+    import torch
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.abspath(NVCC)))
+    include = [INCLUDE, os.path.join(home, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in include), BIND_SOURCE, "-o", out,
+            f"-L{os.path.join(home, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -46,6 +60,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append(cmd)
 
+    tmp_bind = BIND + f".tmp{os.getpid()}"
+    bind = force or _stale(BIND, [BIND_SOURCE] + [h for h in headers if h.endswith(".h")])
+    if bind:
+        jobs.append(_bind_command(tmp_bind))
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -55,8 +74,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             if verbose or ptxas_info or r.returncode:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode:
-                raise RuntimeError("nvcc failed: " + " ".join(cmd))
-    if force or jobs or _stale(SO, objs):
+                raise RuntimeError("compiler failed: " + " ".join(cmd))
+    if bind:
+        os.replace(tmp_bind, BIND)
+    if force or _stale(SO, objs):
         tmp = SO + f".tmp{os.getpid()}"
         cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -22,6 +22,7 @@ namespace {
 constexpr int kBlock = 256;
 constexpr int kMaxSplit = 128;  // parts of a row
 constexpr int kSpan = 2048;     // logits of a part, at least
+constexpr int kMaxVocab = 1 << 30;  // indices of a row's parts stay within 32 bits
 constexpr int64_t kSmall = 1 << 16;
 
 // A logit and its index as one number that grows with the logit and falls with the
@@ -191,10 +192,10 @@ __global__ void __launch_bounds__(kWalkBlock) tree_small(const __grid_constant__
   const SeqView v = seq_view(a.rows, blockIdx.x);
   for (int j = warp; j < v.q_len; j += kWalkBlock / 32) {
     const uint64_t key = warp_max(scan<DT, VEC>(static_cast<const T*>(a.logits) + (v.r0 + j) * a.row_stride, 0, a.vocab, lane, 32));
-    if (lane == 0) (j < kNear ? near[j] : a.greedy[v.r0 + j]) = token_of(key);
+    if (lane == 0) near[j] = token_of(key);  // (no more rows than kNear)
   }
   __syncthreads();
-  if (warp == 0) walk(a, v, blockIdx.x, lane, [&](int j) { return j < kNear ? near[j] : a.greedy[v.r0 + j]; });
+  if (warp == 0) walk(a, v, blockIdx.x, lane, [&](int j) { return near[j]; });
 }
 
 // Parts of a row: about eight blocks an SM over all rows, each of at least kSpan logits.
@@ -205,11 +206,16 @@ int split_of(int n_rows, int vocab) {
 }
 int64_t part_bytes(int n_rows, int vocab) { return (static_cast<int64_t>(n_rows) * split_of(n_rows, vocab) * 8 + 255) / 256 * 256; }
 
+// One launch while the rows of a sequence (as many as max_q says) hold no more logits than kSmall. Its nodes' greedy tokens
+// stay in shared memory: no workspace.
+bool small(const mk_kv_rows& rows, int vocab) {
+  return rows.n_rows <= kNear && static_cast<int64_t>(rows.max_q) * vocab <= kSmall;
+}
+
 template <int DT>
 cudaError_t launch(const TreeArgs& a, bool vec, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  // One launch while the rows of a sequence (as many as max_q says) hold no more logits than kSmall.
-  if (static_cast<int64_t>(a.rows.max_q) * a.vocab <= kSmall) {
+  if (small(a.rows, a.vocab)) {
     cfg.gridDim = dim3(a.rows.n_seqs);
     cfg.blockDim = dim3(kWalkBlock);
     cfg.stream = stream;
@@ -234,9 +240,10 @@ cudaError_t launch(const TreeArgs& a, bool vec, cudaStream_t stream) {
 }  // namespace ops
 }  // namespace mk
 
-extern "C" size_t mk_tree_work_bytes(int32_t n_rows, int32_t vocab) {
-  if (n_rows < 0 || vocab <= 0 || vocab > (1 << 30)) return 0;
-  return static_cast<size_t>(mk::ops::part_bytes(n_rows, vocab)) + static_cast<size_t>(n_rows) * 4 + 256;
+extern "C" size_t mk_tree_work_bytes(const mk_kv_rows* rows, int32_t vocab) {
+  using namespace mk::ops;
+  if (check_rows(rows) != MK_OK || vocab <= 0 || vocab > kMaxVocab || small(*rows, vocab)) return 0;
+  return static_cast<size_t>(part_bytes(rows->n_rows, vocab)) + static_cast<size_t>(rows->n_rows) * 4 + 256;
 }
 
 extern "C" mk_status mk_tree_accept(const mk_kv_rows* rows, const mk_tree_args* t, void* stream) {
@@ -244,14 +251,14 @@ extern "C" mk_status mk_tree_accept(const mk_kv_rows* rows, const mk_tree_args* 
   const mk_status st = check_rows(rows);
   if (st != MK_OK) return st;
   if (!t || t->vocab <= 0 || t->dtype < MK_F32 || t->dtype > MK_BF16) return MK_ERR_INVALID;
-  if (t->vocab > (1 << 30)) return MK_ERR_UNSUPPORTED;  // (indices of a row's parts stay within 32 bits)
+  if (t->vocab > kMaxVocab) return MK_ERR_UNSUPPORTED;
   if (rows->n_seqs == 0) return MK_OK;
   if (!t->count) return MK_ERR_INVALID;
   if (rows->n_rows > 0) {
     if (!t->tokens || !t->logits || !t->path || !t->emitted || (reinterpret_cast<uintptr_t>(t->logits) & (elem_bytes(t->dtype) - 1)))
       return MK_ERR_INVALID;
-    if (!t->work || (reinterpret_cast<uintptr_t>(t->work) & 255u) || t->work_bytes < mk_tree_work_bytes(rows->n_rows, t->vocab))
-      return MK_ERR_INVALID;
+    const size_t need = mk_tree_work_bytes(rows, t->vocab);
+    if (need && (!t->work || (reinterpret_cast<uintptr_t>(t->work) & 255u) || t->work_bytes < need)) return MK_ERR_INVALID;
   }
   TreeArgs a{*rows, t->parents, t->tokens, t->logits, t->row_stride, t->vocab, 1, 0, t->path, t->count, t->emitted, nullptr, nullptr};
   a.split = split_of(rows->n_rows, t->vocab);

@@ -37,7 +37,7 @@ def _rope(ops, **kw):
 
 
 def _tree(ops, **kw):
-    t = ops.mk_tree_args(4096, 4096, 4096, 100, 100, 0, 4096, 4096, 4096, 4096, 1 << 30)
+    t = ops.mk_tree_args(4096, 4096, 4096, 100000, 100000, 0, 4096, 4096, 4096, 4096, 1 << 30)
     for k, v in kw.items():
         setattr(t, k, v)
     return t
@@ -107,12 +107,14 @@ def test_nothing_to_do_is_ok_without_a_device(ops):
 
 
 def test_work_bytes(ops):
-    w = ops.lib.mk_tree_work_bytes
-    assert w(-1, 10) == 0 and w(4, 0) == 0 and w(4, (1 << 30) + 1) == 0
+    w = lambda n, v, q: ops.lib.mk_tree_work_bytes(_rows(ops, n_rows=n, max_q=q), v)  # noqa: E731
+    assert w(-1, 10, 1) == 0 and w(4, 0, 1) == 0 and w(4, (1 << 30) + 1, 1) == 0
     for n in (0, 1, 7, 64, 1000, 1 << 20):
         for v in (1, 2047, 2048, 2049, 248320, 1 << 30):
-            parts = max(1, min(-(-v // 2048), max(1, -(-608 // max(n, 1))), 128))
-            assert w(n, v) >= n * (8 * parts + 4), (n, v)
+            for q in (1, 16, n):
+                few = n <= 1024 and q * v <= 1 << 16  # one launch, nothing to keep between two
+                parts = max(1, min(-(-v // 2048), max(1, -(-1216 // max(n, 1))), 128))
+                assert w(n, v, q) == 0 if few else w(n, v, q) >= n * (8 * parts + 4), (n, v, q)
 
 
 # -------------------------------------------------------- the rotation's table
