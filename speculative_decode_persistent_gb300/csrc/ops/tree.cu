@@ -109,6 +109,7 @@ template <int DT, bool VEC>
 __global__ void __launch_bounds__(kBlock) tree_top(const __grid_constant__ TreeArgs a) {
   using T = typename Elem<DT>::T;
   __shared__ uint64_t top[kBlock / 32];
+  asm volatile("griddepcontrol.launch_dependents;");  // (it waits for the end of this grid all the same)
   for (int row = blockIdx.y; row < a.rows.n_rows; row += gridDim.y) {
     const int begin = static_cast<int>(blockIdx.x) * a.span;
     uint64_t key = scan<DT, VEC>(static_cast<const T*>(a.logits) + row * a.row_stride, begin, min(a.vocab, begin + a.span),
@@ -122,7 +123,6 @@ __global__ void __launch_bounds__(kBlock) tree_top(const __grid_constant__ TreeA
     }
     __syncthreads();
   }
-  asm volatile("griddepcontrol.launch_dependents;");
 }
 
 // A warp walks a sequence's tree, 32 nodes at a time; greedy: its nodes' greedy tokens.
