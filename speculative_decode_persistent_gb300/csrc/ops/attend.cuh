@@ -1104,7 +1104,8 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
         const uint32_t gone = static_cast<uint32_t>(ms.raw_pages[rs]);
         const int end = partly ? wk.v.kv_len - b * kBN - key0 : nkeys;
         // A warp converts a box (16 tokens x kBox codes) at a time, 16 codes a
-        // lane and step; the warps take the boxes of all units in turn.
+        // lane and step; the warps take the boxes of all units in turn. (Single steps
+        // dealt out evenly take more address arithmetic: 84 -> 116 us for 4 x 16 rows.)
         constexpr int kBC = C::kBox / 16, kTok = 32 / kBC, kSteps = kPage / kTok;
         const int nbx = nsl * 64 / C::kBox, boxes = nkeys / kPage * nbx, inv = 256 / nbx + 1;
         const int cc = lane % kBC, tok0 = lane / kBC;

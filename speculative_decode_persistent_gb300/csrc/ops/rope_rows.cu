@@ -21,6 +21,7 @@
 // blocks as are resident, so that this is paid once. Each thread reads its 16 values of a
 // head before it writes them: out may be q.
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -89,6 +90,29 @@ __device__ __forceinline__ void put8(typename Elem<DT>::T* p, const float* x) {
     for (int i = 0; i < 4; ++i) w[i] = DT == MK_F16 ? pack_half2(x[2 * i], x[2 * i + 1]) : pack_bf162(x[2 * i], x[2 * i + 1]);
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+
+// A head's (mean x^2 + eps)^-1/2 where the squares leave 32 bits: of the values divided by a power of two near the
+// largest. `plain` where that is no number to divide by (0, infinite, NaN).
+__device__ __forceinline__ float norm_factor(const float (&x)[8], const float (&y)[8], bool in, int lanes, uint32_t mask, float inv_dh, float eps,
+                                             float plain) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    top = fmaxf(top, fmaxf(fabsf(x[i]), fabsf(y[i])));
+    if (x[i] != x[i] || y[i] != y[i]) top = INFINITY;
+  }
+  if (!in) top = 0.f;
+  for (int m = lanes >> 1; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, m));
+  if (!(top > 0.f && top < INFINITY)) return plain;
+  // 2^-e with 2^e near top, kept normal, as is its reciprocal
+  const float s = __uint_as_float(static_cast<uint32_t>(254 - min(max(static_cast<int>(__float_as_uint(top) >> 23), 1), 253)) << 23);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum += (x[i] * s) * (x[i] * s) + (y[i] * s) * (y[i] * s);
+  if (!in) sum = 0.f;
+  for (int m = lanes >> 1; m; m >>= 1) sum += __shfl_xor_sync(mask, sum, m);
+  return s * rsqrtf(fmaf(sum, inv_dh, eps * s * s));
 }
 
 template <int DT, bool Q8, bool VEC, int PER>
@@ -175,7 +199,8 @@ __global__ void __launch_bounds__(kBlock, 2) rope_write_kernel(const __grid_cons
   }
   __syncthreads();
   T* const out = static_cast<T*>(a.out.data) + (a.row0 + r0) * a.out.row_stride + head * a.out.head_stride + lo;
-  auto turn = [&](const Raw<DT>& rx, const Raw<DT>& ry, int row) {
+  // One head of one row. A head whose squares leave 32 bits is left (true) by the first call, and taken with `rare` set.
+  auto turn = [&](const Raw<DT>& rx, const Raw<DT>& ry, int row, auto rare) {
     const int token = row_token[row];
     float x[8], y[8];
     values8<DT>(rx, x);
@@ -202,7 +227,12 @@ __global__ void __launch_bounds__(kBlock, 2) rope_write_kernel(const __grid_cons
         sum += __shfl_xor_sync(mask, sum, 2);
         if (lanes > 4) sum += __shfl_xor_sync(mask, sum, 4);
         if (lanes > 8) sum += __shfl_xor_sync(mask, sum, 8);
-        const float f = rsqrtf(fmaf(sum, a.inv_dh, a.rope.eps));
+        float f = rsqrtf(fmaf(sum, a.inv_dh, a.rope.eps));
+        if constexpr (decltype(rare)::value) {
+          f = norm_factor(x, y, in, lanes, mask, a.inv_dh, a.rope.eps, f);
+        } else if (DT != MK_F16 && (!(sum < 3e38f) || (sum < 1e-30f && a.rope.eps < 1e-30f))) {  // (binary16's squares fit)
+          return true;
+        }
         const uint64_t f2 = pack2(f, f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -238,7 +268,7 @@ __global__ void __launch_bounds__(kBlock, 2) rope_write_kernel(const __grid_cons
         put8<DT, VEC>(o, x);
         put8<DT, VEC>(o + step, y);
       }
-      return;
+      return false;
     }
     const bool store = in && token >= 0;
     const int64_t e = ((static_cast<int64_t>(token / kPage) * hkv + head) * kPage + token % kPage) * dh + lo;
@@ -267,14 +297,21 @@ __global__ void __launch_bounds__(kBlock, 2) rope_write_kernel(const __grid_cons
         }
       }
     }
+    return false;
   };
-  for (int row = first; row < n_rows; row += PER * a.group_rows) {  // (whole groups)
+  uint64_t left = 0;  // the group's rows that were, by their number
+  for (int row = first, i = 0; row < n_rows; row += PER * a.group_rows, i += PER) {  // (whole groups)
     Batch then;
     if (PER > 1 && row + PER * a.group_rows < n_rows) then = fetch(row + PER * a.group_rows);
 #pragma unroll
     for (int u = 0; u < PER; ++u)
-      if (row + u * a.group_rows < n_rows) turn(now.x[u], now.y[u], row + u * a.group_rows);
+      if (row + u * a.group_rows < n_rows && turn(now.x[u], now.y[u], row + u * a.group_rows, std::false_type())) left |= 1ull << (i + u);
     if (PER > 1) now = then;
+  }
+  for (; left; left &= left - 1) {
+    const int row = first + (__ffsll(static_cast<long long>(left)) - 1) * a.group_rows;
+    const T* q = static_cast<const T*>(src.data) + (a.row0 + r0 + row) * src.row_stride + head * src.head_stride + lo;
+    turn(fetch8<DT, VEC>(q), fetch8<DT, VEC>(q + step), row, std::true_type());
   }
 }
 
@@ -332,7 +369,8 @@ extern "C" mk_status mk_rope_write(const mk_kv_pool* pool, const mk_kv_rows* row
   int block_rows = a.group_rows * (!many ? 1 : r->dtype == MK_F32 ? kPerF32 : kPer);
   if (many) {  // as many batches a block as leave 304 blocks, two an SM, or, where shared memory ends before, a few times as many
     const int64_t blocks = (rows->n_rows + block_rows - 1) / block_rows * a.head_blocks;
-    const int fit = kTable / 4 / (p.rot > 64 ? p.rot : 64) / block_rows, most = fit < kMaxRows / block_rows ? fit : kMaxRows / block_rows;
+    const int fit = kTable / 4 / (p.rot > 64 ? p.rot : 64), room = fit < kMaxRows ? fit : kMaxRows, rows_most = 64 * a.group_rows;
+    const int most = (room < rows_most ? room : rows_most) / block_rows;  // (64 rows a group: they are numbered in 64 bits)
     const int64_t waves = (blocks + 304ll * most - 1) / (304ll * most);
     a.batches = static_cast<int>((blocks + 304 * waves - 1) / (304 * waves));
     block_rows *= a.batches;

@@ -116,6 +116,12 @@ class KVPool:
         self.h = _bind.pool(k, v, k_scale, v_scale)
         self.tensors = (k, v, k_scale, v_scale)
 
+    device = property(lambda self: self.tensors[0].device)
+    q8 = property(lambda self: self.tensors[0].dtype == torch.int8)
+    n_pages = property(lambda self: self.tensors[0].shape[-4])
+    hkv = property(lambda self: self.tensors[0].shape[-3])
+    dh = property(lambda self: self.tensors[0].shape[-1])
+
 
 class KVLayers:
     """Layers of a paged pool that have their pages in common: the tensors of
@@ -127,6 +133,9 @@ class KVLayers:
     def __init__(self, k, v, k_scale=None, v_scale=None):
         self.h = _bind.layers(k, v, k_scale, v_scale)
         self.tensors = (k, v, k_scale, v_scale)
+
+    device, q8, n_pages, hkv, dh = KVPool.device, KVPool.q8, KVPool.n_pages, KVPool.hkv, KVPool.dh
+    n_layers = property(lambda self: self.tensors[0].shape[0])
 
 
 class Rope:
@@ -176,6 +185,9 @@ class KVRows:
         self.h = _bind.rows(row_start, kv_len, tables, n_rows, max_q)
         self.tensors, self.n_rows, self.max_q = (row_start, kv_len, tables), n_rows, max_q
 
+    device = property(lambda self: self.tensors[0].device)
+    n_seqs = property(lambda self: self.tensors[1].shape[0])
+
 
 def kv_write(pool: KVPool, rows: KVRows, k, v) -> None:
     """Store the new rows k, v [rows][kv heads][head dim] at their positions,
@@ -196,8 +208,8 @@ def rope_write(pool: KVPool, rows: KVRows, rope: Rope, q, k, v, parents=None, po
     """New rows into use in one pass: q [rows][query heads][head dim] and k
     [rows][kv heads][head dim] normalised (when rope has gains) and rotated by
     the rows' positions, q into out (made here unless given; it may be q
-    itself; rows of no sequence are left as they are, undefined when it is
-    made here), k and v into the pool as by kv_write. A row's position is
+    itself, and overlaps no input otherwise; rows of no sequence are left as they
+    are, undefined when it is made here), k and v into the pool as by kv_write. A row's position is
     positions[row], or that of its slot; for nodes of trees (parents, as for
     attend) the tree's first position plus the node's depth. All tensors are
     of one type; q, k, v may be slices of one projection's output. Two rows of
@@ -216,7 +228,9 @@ def attend(pool: KVPool, rows: KVRows, q, scale=None, window: int = 0, sinks: in
     drafts: parents[row] is the row's parent, an index into its sequence's rows
     before its own, or -1 where the node follows the cached tokens directly; a
     node sees the tokens before the tree, its ancestors and itself, and windows
-    count positions, the tree's first slot plus a node's depth. Returns out, like q (made here unless given; it may be q or gate itself; rows of
+    count positions, the tree's first slot plus a node's depth (for drafts: the
+    time of the tree's own tokens grows with its nodes times their depth).
+    Returns out, like q (made here unless given; it may be q or gate itself; rows of
     no sequence are left as they are, undefined when it is made here)."""
     return _bind.attend(pool.h, rows.h, q, scale, window, sinks, gate, out, parents)
 

@@ -185,6 +185,32 @@ def test_rope_norm_of_small_and_zero_heads(ops):
     assert_within(got[keep], want[keep], rounded(b, want, torch.float32)[keep])
 
 
+@pytest.mark.parametrize("dh", [64, 192, 256])
+def test_rope_norm_beyond_the_squares_of_32_bits(ops, dh):
+    """Heads whose squares overflow, or with a small eps vanish, in 32 bits: normalised all the same."""
+    c = TreeCase([(9, 9)], 2, 1, dh, "f16", "f32", seed=18, pad_rows=0)
+    c.q[0] *= 1e19
+    c.q[1] *= 1e37
+    c.q[2, 1] = 3e38
+    c.q[3] *= 1e-20
+    c.q[4] *= 1e-36
+    c.q[5, 0, 1:] = 0
+    c.q[6, 0, 3], c.q[7, 1, 2] = math.inf, math.nan
+    c.q[8] = 0
+    clean = torch.where(torch.isfinite(c.q), c.q, torch.ones_like(c.q))
+    for eps in (EPS, 1e-38, 0.0):
+        gain = torch.rand(dh, device="cuda") + 0.5
+        rope = ops.Rope(64, 1e4, gain, gain, eps)
+        pool, rows = c.ops()
+        got = ops.rope_write(pool, rows, rope, c.q, c.new_k, c.new_v)
+        want, b = turned(clean, list(range(9)), 64, freqs(64, 1e4), gain, eps)
+        keep = torch.ones(9, 2, dtype=torch.bool, device="cuda")
+        keep[6, 0] = keep[7, 1] = keep[8] = False
+        assert_within(got[keep], want[keep], rounded(b, want, torch.float32)[keep])
+        assert bool(torch.isnan(got[6, 0]).any()) and bool(torch.isnan(got[7, 1]).all())
+        assert bool(torch.isnan(got[8]).all()) if eps == 0 else not got[8].any()
+
+
 def test_rope_write_many_rows(ops):
     """More rows than one head a group is for, an odd number of heads among the groups."""
     c = TreeCase([(700, 700), (333, 1200)], 7, 2, 256, "f16", "f16", seed=9, kind="chain")
