@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(256) attend_join(const AttendParams a) {
     if (r < j.rows) {
       // A batch of parts, the first together with the references and sums of all (a lane's k is `lane`): one wait for
       // memory instead of two.
-      constexpr int kBatch = 4;
+      constexpr int kBatch = 8;
       const int k0 = share == 1 ? 0 : warp;
       auto slot_of = [&](int k) { return k ? 2 * (j.w0 + k) : j.slot0; };
       float2 y[kBatch][kPer / 2];
