@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(256) attend_join(const AttendParams a) {
     if (r < j.rows) {
       // A batch of parts, the first together with the references and sums of all (a lane's k is `lane`): one wait for
       // memory instead of two.
-      constexpr int kBatch = 8;
+      constexpr int kBatch = 4;
       const int k0 = share == 1 ? 0 : warp;
       auto slot_of = [&](int k) { return k ? 2 * (j.w0 + k) : j.slot0; };
       float2 y[kBatch][kPer / 2];
@@ -574,6 +574,27 @@ __global__ void __launch_bounds__(256) attend_join(const AttendParams a) {
     }
     if (share == 1) __syncwarp(); else __syncthreads();
   }
+}
+
+// A lane's eight bf16 values of a query row as binary16, for lanes `group`, which hold the row: times a power of two that
+// brings the row's largest value to [2^14, 2^15), exact for what is at least 2^-31 of it, to 2^-25 for the rest (2^-39 of
+// the largest); infinite and NaN values stay (magnitudes compared as integers; a row's lanes in one reduction). Returns the
+// power that the row was divided by.
+__device__ __forceinline__ int half_queries(uint32_t (&o)[4], uint32_t group) {
+  float x[8];
+  uint32_t top2 = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = __uint_as_float(o[j] << 16);
+    x[2 * j + 1] = __uint_as_float(o[j] & 0xffff0000u);
+    top2 = __vmaxu2(top2, o[j] & 0x7fff7fffu);
+  }
+  const uint32_t mx = __reduce_max_sync(group, max(top2 & 0xffffu, top2 >> 16));
+  const int e = max(static_cast<int>(mx >> 7) - (127 + 14), -126);  // at most 114; 2^e and 2^-e are normal
+  const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = pack_half2(x[2 * j] * f, x[2 * j + 1] * f);
+  return e;
 }
 
 // The worker's segments, every warp its part. LARGE: once more, from segment `first` on, with large q8 values.
@@ -1207,54 +1228,89 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
     };
     constexpr int kLPR = NS == 3 ? 32 : 8 * NS;  // lanes per row of Q
     constexpr int kRPP = 32 / kLPR;              // rows per warp and pass
+    [[maybe_unused]] constexpr int kPass = (128 + kPrep * kRPP - 1) / (kPrep * kRPP), kBatch = kPass < 11 ? kPass : 11;
     const int ch = lane % kLPR, sub = lane / kLPR;
+    const uint32_t row_lanes = kLPR == 32 ? 0xffffffffu : ((1u << kLPR % 32) - 1) << (sub * kLPR);
     while (ok && take()) {
-      // Q of the tile, once the products of the segment before no longer read it: every row's copy into its place under
-      // way at once, then each lane converts the pieces that it copied. (In registers, eleven rows at a time in
-      // unrolled code, a tile of 256 rows took 6.7 us.)
+      // Q of the tile
       const int rows = min(128, wk.t.rows - rank * 128);
-      if (wk.seg + shift > 0) ok = wait(ms.q_free, (wk.seg + shift - 1) & 1);
-      if (!ok) break;
-      auto place = [&](int r) { return sq + (ch / 8) * 16384 + r * 128 + (((ch % 8) ^ (r & 7)) << 4); };
-#pragma unroll 2
-      for (int r = pw * kRPP + sub; r < rows; r += kPrep * kRPP) {
-        if (kLPR != 8 * NS && ch >= 8 * NS) continue;
-        const RowOf at = row_of(wk.t, rank * 128 + r, a.G, a.g_inv);
-        const uint16_t* p = static_cast<const uint16_t*>(a.q.data) + (wk.v.r0 + at.tok) * a.q.row_stride +
-                            (wk.h * a.G + at.head) * a.q.head_stride + ch * 8;
-        if (a.vq) {
-          cp_async16(smem_u32(place(r)), p);
-        } else {
-          uint32_t o[4];
+      if constexpr (Q8) {
+        // The first rows are fetched before the products of the segment before are known to no longer read it, and stored
+        // after that. (The other way costs the conversion of codes, which sets the pace here, registers: 2 % of the time.)
+#pragma unroll 1
+        for (int pass = 0; pass < kPass; pass += kBatch) {
+          // Addresses are clamped to valid rows and columns rather than the loads
+          // made conditional: all of a batch are in flight at once.
+          uint32_t o[kBatch][4];
+          auto row_ptr = [&](int t) {
+            const int r = min(((pass + t) * kPrep + pw) * kRPP + sub, max(rows, 1) - 1);
+            const RowOf at = row_of(wk.t, min(rank * 128 + r, wk.t.rows - 1), a.G, a.g_inv);
+            return static_cast<const uint16_t*>(a.q.data) + (wk.v.r0 + at.tok) * a.q.row_stride +
+                   (wk.h * a.G + at.head) * a.q.head_stride + min(ch, 8 * NS - 1) * 8;
+          };
+          if (a.vq) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = p[2 * j] | static_cast<uint32_t>(p[2 * j + 1]) << 16;
-          *reinterpret_cast<uint4*>(place(r)) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int t = 0; t < kBatch; ++t) {
+              if (t >= 2 && (pass + t) * kPrep * kRPP >= rows) break;
+              const uint4 x = __ldg(reinterpret_cast<const uint4*>(row_ptr(t)));
+              o[t][0] = x.x; o[t][1] = x.y; o[t][2] = x.z; o[t][3] = x.w;
+            }
+          } else {
+#pragma unroll
+            for (int t = 0; t < kBatch; ++t) {
+              const uint16_t* qp = row_ptr(t);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[t][j] = qp[2 * j] | static_cast<uint32_t>(qp[2 * j + 1]) << 16;
+            }
+          }
+          if (pass == 0 && wk.seg + shift > 0) ok = wait(ms.q_free, (wk.seg + shift - 1) & 1);
+#pragma unroll
+          for (int t = 0; t < kBatch; ++t) {
+            const int r0 = ((pass + t) * kPrep + pw) * kRPP, r = r0 + sub;
+            if (r0 >= rows) break;  // whole warps
+            int e = 0;
+            if (a.dtype == MK_BF16) e = half_queries(o[t], row_lanes);
+            if (r < rows && ch < 8 * NS)
+              *reinterpret_cast<uint4*>(sq + (ch / 8) * 16384 + r * 128 + (((ch % 8) ^ (r & 7)) << 4)) =
+                  make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
+            if (ch == 0 && r < rows) ms.qe[(wk.seg + shift) % 3][r] = static_cast<int8_t>(e);
+          }
         }
-        if (ch == 0) ms.qe[(wk.seg + shift) % 3][r] = 0;
-      }
-      cp_async_wait();
-      if (a.dtype == MK_BF16) {
-        // the row times a power of two that brings its largest value to [2^14, 2^15): exact for what is at least
-        // 2^-31 of it, to 2^-25 for the rest (2^-39 of the largest); infinite and NaN values stay
-        // (magnitudes compared as integers; a row's lanes in one reduction)
+        if (!ok) break;
+      } else {
+        // Once the products of the segment before no longer read it: every row's copy into its place under way at once,
+        // then each lane converts the pieces that it copied (4,096-row prompt: 166 -> 162 us).
+        if (wk.seg + shift > 0) ok = wait(ms.q_free, (wk.seg + shift - 1) & 1);
+        if (!ok) break;
+        auto place = [&](int r) { return sq + (ch / 8) * 16384 + r * 128 + (((ch % 8) ^ (r & 7)) << 4); };
 #pragma unroll 2
-        for (int r0 = pw * kRPP; r0 < rows; r0 += kPrep * kRPP) {
-          const int r = r0 + sub;
-          const bool mine = r < rows && (kLPR == 8 * NS || ch < 8 * NS);
-          const uint4 w = mine ? *reinterpret_cast<const uint4*>(place(r)) : make_uint4(0, 0, 0, 0);
-          const uint32_t o[4] = {w.x, w.y, w.z, w.w};
-          uint32_t top2 = 0;
+        for (int r = pw * kRPP + sub; r < rows; r += kPrep * kRPP) {
+          if (kLPR != 8 * NS && ch >= 8 * NS) continue;
+          const RowOf at = row_of(wk.t, rank * 128 + r, a.G, a.g_inv);
+          const uint16_t* p = static_cast<const uint16_t*>(a.q.data) + (wk.v.r0 + at.tok) * a.q.row_stride +
+                              (wk.h * a.G + at.head) * a.q.head_stride + ch * 8;
+          if (a.vq) {
+            cp_async16(smem_u32(place(r)), p);
+          } else {
+            uint32_t o[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) top2 = __vmaxu2(top2, o[j] & 0x7fff7fffu);
-          const uint32_t group = kLPR == 32 ? 0xffffffffu : ((1u << kLPR % 32) - 1) << (sub * kLPR);
-          const uint32_t mx = __reduce_max_sync(group, max(top2 & 0xffffu, top2 >> 16));
-          const int e = max(static_cast<int>(mx >> 7) - (127 + 14), -126);  // at most 114; 2^e and 2^-e are normal
-          const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          uint32_t h[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) h[j] = pack_half2(__uint_as_float(o[j] << 16) * f, __uint_as_float(o[j] & 0xffff0000u) * f);
-          if (mine) *reinterpret_cast<uint4*>(place(r)) = make_uint4(h[0], h[1], h[2], h[3]);
-          if (mine && ch == 0) ms.qe[(wk.seg + shift) % 3][r] = static_cast<int8_t>(e);
+            for (int j = 0; j < 4; ++j) o[j] = p[2 * j] | static_cast<uint32_t>(p[2 * j + 1]) << 16;
+            *reinterpret_cast<uint4*>(place(r)) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          if (ch == 0) ms.qe[(wk.seg + shift) % 3][r] = 0;
+        }
+        cp_async_wait();
+        if (a.dtype == MK_BF16) {
+#pragma unroll 2
+          for (int r0 = pw * kRPP; r0 < rows; r0 += kPrep * kRPP) {
+            const int r = r0 + sub;
+            const bool mine = r < rows && (kLPR == 8 * NS || ch < 8 * NS);
+            const uint4 w = mine ? *reinterpret_cast<const uint4*>(place(r)) : make_uint4(0, 0, 0, 0);
+            uint32_t o[4] = {w.x, w.y, w.z, w.w};
+            const int e = half_queries(o, row_lanes);
+            if (mine) *reinterpret_cast<uint4*>(place(r)) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (mine && ch == 0) ms.qe[(wk.seg + shift) % 3][r] = static_cast<int8_t>(e);
+          }
         }
       }
       fence_async_shared();
