@@ -500,7 +500,7 @@ template <int NS, int CG>
 __global__ void __launch_bounds__(256) attend_join(const AttendParams a) {
   constexpr int DH = NS * 64, M = 128 * CG, kPer = DH / 32;
   __shared__ float sums[8][DH + 4];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched early: the parts are written from here on
+  wait_for_previous();  // the parts are written from here on
   const JoinInfo j = a.join[blockIdx.x];
   if (j.w0 < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -1402,12 +1402,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tensormap_prefetch(&tv);
   }
   if (warp == kWarpMma) tmem_alloc<CG>(smem_u32(&ms.tmem), 512);
+  wait_for_previous();
   find_start<C::M, TREE>(a, reinterpret_cast<int*>(ring), &ms.start, blockIdx.x / CG, rank == 0);
   fence_async_shared();  // the scratch lay where tensor copies go
   meet();
   tc_fence_after();
   const uint32_t tm = ms.tmem;
-  asm volatile("griddepcontrol.launch_dependents;");
+  let_next_start();  // attend_join
   attend_pass<NS, Q8, CG, TREE, false>(a, tk, tv, smem, tm);
   if constexpr (Q8 && CG == 2) {  // both blocks of a pair go on alike, even if the pool changes under the kernel
     __syncthreads();
@@ -1465,27 +1466,20 @@ cudaError_t launch_attend(AttendParams a, const CUtensorMap& tk, const CUtensorM
   a.workers = resident_workers<NS, Q8, CG, TREE>(device);
   if (!a.workers) return cudaErrorInvalidDevice;
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim = {CG, 1, 1};
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(a.workers * CG);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel<NS, Q8, CG, TREE>, a, tk, tv);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t jc{};
-  cudaLaunchAttribute ja[1];
-  ja[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  ja[0].val.programmaticStreamSerializationAllowed = 1;
-  jc.gridDim = dim3(a.workers, kJoinSplit);
-  jc.blockDim = dim3(256);
-  jc.stream = stream;
-  jc.attrs = ja;
-  jc.numAttrs = 1;
-  return cudaLaunchKernelEx(&jc, attend_join<NS, CG>, a);
+  return launch_early(attend_join<NS, CG>, dim3(a.workers, kJoinSplit), dim3(256), 0, stream, a);
 }
 
 template <bool Q8, bool TREE>

@@ -25,6 +25,7 @@ struct CopyArgs {
 
 template <int U>
 __global__ void __launch_bounds__(kCopyBlock) kv_copy_kernel(const __grid_constant__ CopyArgs a) {
+  wait_for_previous();
   const int64_t layer = static_cast<int64_t>(blockIdx.z) * a.l.layer_stride;
   const bool q8 = a.l.pool.kv_dtype == MK_KV_Q8;
   int chunk = blockIdx.x;
@@ -77,6 +78,7 @@ __global__ void __launch_bounds__(kThreads) kv_keep_kernel(const __grid_constant
   static_assert(kTokens <= kThreads && kTokens % 32 == 0, "a thread looks at one entry");
   __shared__ int from[3][kTokens], to[3][kTokens];
   __shared__ uint32_t ascends[3][kTokens / 32];
+  wait_for_previous();
   const int s = blockIdx.y, tid = threadIdx.x;
   const SeqView v = seq_view(a.rows, s);
   const int base = v.kv_len - v.q_len, hkv = a.l.pool.hkv, n_pages = a.l.pool.n_pages;
@@ -213,11 +215,8 @@ extern "C" mk_status mk_kv_copy(const mk_kv_layers* layers, const int32_t* src, 
   if (2 * (chunks + scale_chunks) > 0x7fffffffll) return MK_ERR_UNSUPPORTED;
   a.chunks = static_cast<int>(chunks);
   a.scale_chunks = static_cast<int>(scale_chunks);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * (chunks + scale_chunks)), n < 65535 ? n : 65535, layers->n_layers);
-  cfg.blockDim = dim3(kCopyBlock);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  return launched(cudaLaunchKernelEx(&cfg, big ? kv_copy_kernel<4> : kv_copy_kernel<1>, a));
+  const dim3 grid(static_cast<unsigned>(2 * (chunks + scale_chunks)), n < 65535 ? n : 65535, layers->n_layers);
+  return launched(launch_early(big ? kv_copy_kernel<4> : kv_copy_kernel<1>, grid, dim3(kCopyBlock), 0, static_cast<cudaStream_t>(stream), a));
 }
 
 extern "C" mk_status mk_kv_keep(const mk_kv_layers* layers, const mk_kv_rows* rows, const int32_t* keep, int32_t* kv_len, void* stream) {
@@ -237,9 +236,6 @@ extern "C" mk_status mk_kv_keep(const mk_kv_layers* layers, const mk_kv_rows* ro
   const int64_t data = 2ll * p.hkv * a.pieces, columns = data + (q8 ? 2ll * p.hkv : 0);
   if (columns > (1 << 24)) return MK_ERR_UNSUPPORTED;
   a.data = static_cast<int>(data);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(columns), rows->n_seqs, layers->n_layers);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  return launched(cudaLaunchKernelEx(&cfg, wide ? kv_keep_kernel<16> : kv_keep_kernel<4>, a));
+  const dim3 grid(static_cast<unsigned>(columns), rows->n_seqs, layers->n_layers);
+  return launched(launch_early(wide ? kv_keep_kernel<16> : kv_keep_kernel<4>, grid, dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a));
 }

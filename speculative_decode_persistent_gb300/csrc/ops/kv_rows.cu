@@ -62,6 +62,7 @@ __device__ __forceinline__ int64_t pool_elem(const RowsArgs& a, int token_row, c
 template <int DT, bool Q8, bool VEC>
 __global__ void __launch_bounds__(kBlock, 5) kv_write_kernel(const RowsArgs a) {
   using T = typename Elem<DT>::T;
+  wait_for_previous();
   const Where w = where(a);
   const int half = a.pool.dh / 2;
   const T* k = static_cast<const T*>(a.k.data) + w.r * a.k.row_stride + w.head * a.k.head_stride + w.dim;
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(kBlock, 5) kv_write_kernel(const RowsArgs a) {
 template <int DT, bool Q8, bool VEC>
 __global__ void __launch_bounds__(kBlock) kv_read_kernel(const RowsArgs a) {
   using T = typename Elem<DT>::T;
+  wait_for_previous();
   const Where w = where(a);
   const int t = w.live ? token_row(a.rows, a.pool.n_pages, static_cast<int>(w.r)) : -2;
   if (t == -2) return;
@@ -165,11 +167,8 @@ mk_status run(const mk_kv_pool* pool, const mk_kv_rows* rows, const mk_dense* k,
     RowsArgs a{*pool, *rows, *k, *v, static_cast<int>(r),
                static_cast<int>(rows->n_rows - r < slab ? rows->n_rows - r : slab), static_cast<uint32_t>(per_row),
                static_cast<uint32_t>((1ll << 32) / per_row)};
-    cudaLaunchConfig_t cfg{};  // (the launch's own status: an error that an earlier call left is not this one's)
-    cfg.gridDim = dim3(static_cast<unsigned>((a.n * per_row + kBlock - 1) / kBlock));
-    cfg.blockDim = dim3(kBlock);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    if (cudaLaunchKernelEx(&cfg, fn, a) != cudaSuccess) {
+    const dim3 grid(static_cast<unsigned>((a.n * per_row + kBlock - 1) / kBlock));
+    if (launch_early(fn, grid, dim3(kBlock), 0, static_cast<cudaStream_t>(stream), a) != cudaSuccess) {
       cudaGetLastError();
       return MK_ERR_CUDA;
     }

@@ -118,6 +118,7 @@ __device__ __forceinline__ float norm_factor(const float (&x)[8], const float (&
 template <int DT, bool Q8, bool VEC, int PER>
 __global__ void __launch_bounds__(kBlock, 2) rope_write_kernel(const __grid_constant__ RopeArgs a) {
   using T = typename Elem<DT>::T;
+  wait_for_previous();
   __shared__ int row_token[kMaxRows], row_pos[kMaxRows];  // token: -2 for rows of no sequence
   extern __shared__ __align__(16) float table[];          // [rows of the block][2][rot / 2]: cosines, sines
   const int tid = threadIdx.x, lanes = 1 << a.lanes_log2, c = tid & (lanes - 1), group = tid >> a.lanes_log2;
@@ -381,12 +382,8 @@ extern "C" mk_status mk_rope_write(const mk_kv_pool* pool, const mk_kv_rows* row
   for (int64_t r0 = 0; r0 < rows->n_rows; r0 += slab) {
     a.row0 = static_cast<int>(r0);
     a.n = static_cast<int>(rows->n_rows - r0 < slab ? rows->n_rows - r0 : slab);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>((a.n + block_rows - 1) / block_rows) * a.head_blocks));
-    cfg.blockDim = dim3(kBlock);
-    cfg.dynamicSmemBytes = sizeof(float) * block_rows * p.rot;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    if (cudaLaunchKernelEx(&cfg, fn, a) != cudaSuccess) {
+    const dim3 grid(static_cast<unsigned>(static_cast<int64_t>((a.n + block_rows - 1) / block_rows) * a.head_blocks));
+    if (launch_early(fn, grid, dim3(kBlock), sizeof(float) * block_rows * p.rot, static_cast<cudaStream_t>(stream), a) != cudaSuccess) {
       cudaGetLastError();
       return MK_ERR_CUDA;
     }

@@ -109,7 +109,8 @@ template <int DT, bool VEC>
 __global__ void __launch_bounds__(kBlock) tree_top(const __grid_constant__ TreeArgs a) {
   using T = typename Elem<DT>::T;
   __shared__ uint64_t top[kBlock / 32];
-  asm volatile("griddepcontrol.launch_dependents;");  // (it waits for the end of this grid all the same)
+  let_next_start();  // tree_walk
+  wait_for_previous();
   for (int row = blockIdx.y; row < a.rows.n_rows; row += gridDim.y) {
     const int begin = static_cast<int>(blockIdx.x) * a.span;
     uint64_t key = scan<DT, VEC>(static_cast<const T*>(a.logits) + row * a.row_stride, begin, min(a.vocab, begin + a.span),
@@ -168,8 +169,8 @@ constexpr int kWalkBlock = 512, kNear = 1024;  // nodes whose greedy tokens are 
 __global__ void __launch_bounds__(kWalkBlock) tree_walk(const __grid_constant__ TreeArgs a) {
   __shared__ int near[kNear];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  wait_for_previous();  // the parts are there from here on
   const SeqView v = seq_view(a.rows, blockIdx.x);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there from here on
   for (int j = warp; j < v.q_len; j += kWalkBlock / 32) {
     uint64_t key = 0;
     for (int p = lane; p < a.split; p += 32) {
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(kWalkBlock) tree_small(const __grid_constant__
   using T = typename Elem<DT>::T;
   __shared__ int near[kNear];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  wait_for_previous();
   const SeqView v = seq_view(a.rows, blockIdx.x);
   for (int j = warp; j < v.q_len; j += kWalkBlock / 32) {
     const uint64_t key = warp_max(scan<DT, VEC>(static_cast<const T*>(a.logits) + (v.r0 + j) * a.row_stride, 0, a.vocab, lane, 32));
@@ -215,26 +217,11 @@ bool small(const mk_kv_rows& rows, int vocab) {
 
 template <int DT>
 cudaError_t launch(const TreeArgs& a, bool vec, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg{};
-  if (small(a.rows, a.vocab)) {
-    cfg.gridDim = dim3(a.rows.n_seqs);
-    cfg.blockDim = dim3(kWalkBlock);
-    cfg.stream = stream;
-    return cudaLaunchKernelEx(&cfg, vec ? tree_small<DT, true> : tree_small<DT, false>, a);
-  }
-  cfg.gridDim = dim3(a.split, a.rows.n_rows < 65535 ? a.rows.n_rows : 65535);
-  cfg.blockDim = dim3(kBlock);
-  cfg.stream = stream;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, vec ? tree_top<DT, true> : tree_top<DT, false>, a);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(a.rows.n_seqs);
-  cfg.blockDim = dim3(kWalkBlock);
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_walk, a);
+  if (small(a.rows, a.vocab))
+    return launch_early(vec ? tree_small<DT, true> : tree_small<DT, false>, dim3(a.rows.n_seqs), dim3(kWalkBlock), 0, stream, a);
+  const dim3 grid(a.split, a.rows.n_rows < 65535 ? a.rows.n_rows : 65535);
+  const cudaError_t e = launch_early(vec ? tree_top<DT, true> : tree_top<DT, false>, grid, dim3(kBlock), 0, stream, a);
+  return e != cudaSuccess ? e : launch_early(tree_walk, dim3(a.rows.n_seqs), dim3(kWalkBlock), 0, stream, a);
 }
 
 }  // namespace
