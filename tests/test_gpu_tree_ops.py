@@ -331,6 +331,22 @@ def test_unseen_nodes_may_hold_anything(ops, kv):
     assert not torch.isfinite(out[own_key]).any()
 
 
+@pytest.mark.parametrize("seqs,hq,hkv,dh,kv", [([(64, 30000)], 24, 4, 256, "f16"), ([(64, 52000)], 24, 4, 256, "q8"), ([(100, 100000)], 8, 4, 64, "f16"),
+                                               ([(45, 70001)], 12, 2, 192, "f16")])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 5), (20000, 0)])
+def test_tiles_that_share_a_far_context(ops, seqs, hq, hkv, dh, kv, window, sinks):
+    """Contexts beyond the L2 cache, several tiles of one sequence: all tiles are cut at the same blocks, into more
+    pieces than a narrow window has blocks."""
+    c = TreeCase(seqs, hq, hkv, dh, kv, "f16", seed=19)
+    check_tree(ops, c, window, sinks)
+    if not window:
+        from ops_helpers import Case
+        pool, rows = c.ops()
+        out = ops.attend(pool, rows, c.q)
+        want, bound = Case.attend_ref(c)
+        assert_within(out[:c.rows_used], want, bound)
+
+
 def test_nodes_without_pages_or_slots(ops):
     c = TreeCase([(20, 150), (30, 40)], 4, 2, 64, "f16", "f16", seed=10)
     c.tables[0, 2], c.tables[0, 8], c.tables[1, 0], c.tables[1, 1] = -1, c.n_pages, -7, -1

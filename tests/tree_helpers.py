@@ -58,8 +58,8 @@ class TreeCase(Case):
             if base + j < 0:
                 continue  # a row without a slot sees nothing
             pos = base + len(line) - 1
-            for t in range(max(base, 0)):
-                see[j, t] = not window or pos - t < window or t < sinks
+            t = torch.arange(max(base, 0))
+            see[j, :max(base, 0)] = (pos - t < window) | (t < sinks) if window else True
             for depth, n in enumerate(line):
                 if base + n >= 0:
                     see[j, base + n] = not window or pos - (base + depth) < window or base + depth < sinks
