@@ -1,7 +1,10 @@
 // Moves of cached tokens within the pool, in all layers of one call: whole pages
 // (a prefix for another sequence) and kept tokens (the accepted path of a tree of
 // drafts, or a context that loses old tokens). Nothing is computed: both are bound by
-// HBM traffic when much moves, by the launch when little does.
+// HBM traffic when much moves, by the launch when little does. Measured: 3 x 256 pages in 17
+// layers (binary16, 1.14 GB) copied in 168 us, 6.8 TB/s, the copy rate; 8,176 of 23,000 tokens moved
+// in 17 layers (q8, 605 MB) in 130 us, 4.6 TB/s (a column's batches follow each other: the latency
+// of 64 of them); the paths of four trees in 17 layers in 5 us.
 #include <cuda_runtime.h>
 
 #include "ops_internal.cuh"

@@ -20,6 +20,11 @@
 // sines and cosines once for all heads, in shared memory; with many rows there are as many
 // blocks as are resident, so that this is paid once. Each thread reads its 16 values of a
 // head before it writes them: out may be q.
+//
+// Bound and measured. Many rows: 8,192 rows of 24 + 4 + 4 heads of 256 (bf16, 268 MB) in 49 us,
+// 5.4 TB/s; ncu has 57 % of the issue slots busy and 16 warps an SM, which wait on their own
+// arithmetic and on shared memory. Few rows: the launch and three dependent loads of the lookup
+// (64 rows into a q8 pool with their reading back, two calls: 11 us).
 #include <cmath>
 #include <type_traits>
 
