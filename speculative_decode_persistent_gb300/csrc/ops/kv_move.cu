@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kCopyBlock) kv_copy_kernel(const __grid_consta
 // block meets, all are written. What later entries read lies behind everything that
 // earlier ones write, so columns need no order among blocks, and the next batch is read
 // while this one is on its way. LANES lanes of 16 bytes take a token: 4 in long lists
-// (128 entries a batch, narrow columns, many blocks), 16 in short ones (32 entries).
+// (128 entries a batch, narrow columns, many blocks), 16 in shorter ones (32 entries).
 constexpr int kThreads = 128, kDeep = 4;  // threads of a block, tokens that a thread moves at a time
 
 struct KeepArgs {
@@ -211,8 +211,9 @@ extern "C" mk_status mk_kv_copy(const mk_kv_layers* layers, const int32_t* src, 
   const mk_kv_pool& p = layers->pool;
   const bool q8 = p.kv_dtype == MK_KV_Q8;
   CopyArgs a{*layers, src, dst, n, 0, 0, static_cast<int64_t>(p.hkv) * kPage * p.dh * (q8 ? 1 : 2), static_cast<int64_t>(p.hkv) * p.dh};
-  // 16 KB a block, or 4 KB where that leaves SMs without two blocks
-  const bool big = a.page_bytes * 2 * n * layers->n_layers >= (304ll << 14);
+  // 16 KB a block, or 4 KB where that leaves SMs without a block (64 KB a pair of pages: 8 pairs 1.6 against 1.4 us, 32
+  // pairs 1.7 both, 76 pairs 2.0 against 2.5, 1,000 pairs 21 against 26)
+  const bool big = a.page_bytes * 2 * n * layers->n_layers >= (152ll << 14);
   const int64_t span = kCopyBlock * 16 * (big ? 4 : 1);
   const int64_t chunks = (a.page_bytes + span - 1) / span, scale_chunks = q8 ? (a.scale_bytes + span - 1) / span : 0;
   if (2 * (chunks + scale_chunks) > 0x7fffffffll) return MK_ERR_UNSUPPORTED;
@@ -231,8 +232,10 @@ extern "C" mk_status mk_kv_keep(const mk_kv_layers* layers, const mk_kv_rows* ro
   if (!keep && rows->n_rows > 0) return MK_ERR_INVALID;
   const mk_kv_pool& p = layers->pool;
   const bool q8 = p.kv_dtype == MK_KV_Q8;
-  // short lists (drafts) in wide columns, long ones in narrow: the more blocks the more is on its way
-  const bool wide = rows->n_rows <= 32ll * rows->n_seqs;
+  // Short lists (drafts) in wide columns, long ones in narrow: the more blocks the more is on its way. (Half of four
+  // sequences' rows kept in 17 layers: 16 rows 2.6 against 6.6 us, 128 rows 7.1 against 10, 512 rows 26 against 28; 8,192 of
+  // 23,000 tokens 145 in columns twice as wide and 166 in whole rows against 132.)
+  const bool wide = rows->n_rows <= 512ll * rows->n_seqs;
   const int width = 16 * (wide ? 16 : 4);
   KeepArgs a{*layers, *rows, keep, kv_len, p.dh * (q8 ? 1 : 2), 0, 0};
   a.pieces = (a.row_bytes + width - 1) / width;
