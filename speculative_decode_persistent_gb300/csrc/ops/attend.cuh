@@ -267,7 +267,7 @@ struct Walk {
   // so that a load ahead is waited for only where has_page() looks at it.
   __device__ __forceinline__ int entry(int b, int i) const {
     const int e = b * (kBN / kPage) + i;
-    return e < a->rows.table_stride ? __ldg(a->rows.tables + static_cast<int64_t>(s) * a->rows.table_stride + e) : -1;
+    return e < a->rows.table_stride ? a->rows.tables[static_cast<int64_t>(s) * a->rows.table_stride + e] : -1;
   }
   __device__ __forceinline__ bool has_page(int entry) const { return entry >= 0 && entry < a->pool.n_pages; }
 };
@@ -1300,7 +1300,7 @@ __device__ __forceinline__ void attend_pass(const AttendParams& a, const CUtenso
 #pragma unroll
             for (int t = 0; t < kBatch; ++t) {
               if (t >= 2 && (pass + t) * kPrep * kRPP >= rows) break;
-              const uint4 x = __ldg(reinterpret_cast<const uint4*>(row_ptr(t)));
+              const uint4 x = *reinterpret_cast<const uint4*>(row_ptr(t));
               o[t][0] = x.x; o[t][1] = x.y; o[t][2] = x.z; o[t][3] = x.w;
             }
           } else {

@@ -3,7 +3,7 @@
 // drafts, or a context that loses old tokens). Nothing is computed: both are bound by
 // HBM traffic when much moves, by the launch when little does. Measured: 3 x 256 pages in 17
 // layers (binary16, 1.14 GB) copied in 168 us, 6.8 TB/s, the copy rate; 8,176 of 23,000 tokens moved
-// in 17 layers (q8, 605 MB) in 130 us, 4.6 TB/s (a column's batches follow each other: the latency
+// in 17 layers (q8, 605 MB) in 128 us, 4.7 TB/s (a column's batches follow each other: the latency
 // of 64 of them); the paths of four trees in 17 layers in 5 us.
 #include <cuda_runtime.h>
 
@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kCopyBlock) kv_copy_kernel(const __grid_consta
                         (scales ? layer / 16 : q8 ? layer : 2 * layer);
   const int64_t at = static_cast<int64_t>(chunk) * (kCopyBlock * 16 * U) + threadIdx.x * 16;
   for (int pair = blockIdx.y; pair < a.n; pair += gridDim.y) {
-    const int s = __ldg(a.src + pair), d = __ldg(a.dst + pair);
+    const int s = a.src[pair], d = a.dst[pair];
     if (s < 0 || s >= a.l.pool.n_pages || d < 0 || d >= a.l.pool.n_pages) continue;
     const uint8_t* from = base + s * bytes;
     uint8_t* to = base + d * bytes;
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kCopyBlock) kv_copy_kernel(const __grid_consta
 // through the whole list, a batch of entries at a time: all of a batch are read, the
 // block meets, all are written. What later entries read lies behind everything that
 // earlier ones write, so columns need no order among blocks, and the next batch is read
-// while this one is on its way. LANES lanes of 16 bytes take a token: 4 in long lists
+// while this one is on its way: its pages were looked up a batch before, its list's entries read two before. LANES lanes of 16 bytes take a token: 4 in long lists
 // (128 entries a batch, narrow columns, many blocks), 16 in shorter ones (32 entries).
 constexpr int kThreads = 128, kDeep = 4;  // threads of a block, tokens that a thread moves at a time
 
@@ -75,8 +75,10 @@ struct KeepArgs {
   int row_bytes, pieces, data;  // bytes of a head's row, columns of it; columns of a layer that are K's and V's
 };
 
+// (Eight blocks an SM: without the limit the narrow one took 56 registers and spilled, 138 against 135 us; looked up behind
+// the loads of the next batch, 149 against 128.)
 template <int LANES>
-__global__ void __launch_bounds__(kThreads) kv_keep_kernel(const __grid_constant__ KeepArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) kv_keep_kernel(const __grid_constant__ KeepArgs a) {
   constexpr int kTokens = kThreads * kDeep / LANES;  // entries of a batch
   static_assert(kTokens <= kThreads && kTokens % 32 == 0, "a thread looks at one entry");
   __shared__ int from[3][kTokens], to[3][kTokens];
@@ -98,21 +100,25 @@ __global__ void __launch_bounds__(kThreads) kv_keep_kernel(const __grid_constant
   const bool mine = scales || at16 < bytes;
   if (!scales) p += at16;
 
-  // Batch b of the list: rows of a head that its entries come from and go to (-1: does not move), and which entries follow
+  struct Entry {
+    int k, before;
+  };
+  // a thread's entry of batch b of the list, and the one before it
+  auto entry = [&](int b) {
+    const int i = b * kTokens + tid;
+    return tid < kTokens && i < v.q_len ? Entry{a.keep[v.r0 + i], i ? a.keep[v.r0 + i - 1] : -1} : Entry{-1, -1};
+  };
+  // Batch b, whose entries are e: rows of a head that they come from and go to (-1: does not move), and which entries follow
   // the one before.
-  auto look = [&](int b, int buf) {
+  auto look = [&](int b, int buf, Entry e) {
     if (tid >= kTokens) return;
     const int i = b * kTokens + tid;
     int f = -1, t = -1;
-    bool good = false;
-    if (i < v.q_len) {
-      const int k = __ldg(a.keep + v.r0 + i), before = i ? __ldg(a.keep + v.r0 + i - 1) : -1;
-      good = k < v.q_len && k > max(before, -1);
-      if (good && k != i) {
-        f = token_at(a.rows, n_pages, s, base + k);
-        t = token_at(a.rows, n_pages, s, base + i);
-        if (f < 0 || t < 0) f = -1;
-      }
+    const bool good = e.k < v.q_len && e.k > max(e.before, -1);
+    if (good && e.k != i) {
+      f = token_at(a.rows, n_pages, s, base + e.k);
+      t = token_at(a.rows, n_pages, s, base + i);
+      if (f < 0 || t < 0) f = -1;
     }
     from[buf][tid] = f < 0 ? -1 : f / kPage * (hkv * kPage) + f % kPage;  // (below 2^31: check_pool)
     to[buf][tid] = t < 0 ? -1 : t / kPage * (hkv * kPage) + t % kPage;
@@ -166,8 +172,9 @@ __global__ void __launch_bounds__(kThreads) kv_keep_kernel(const __grid_constant
         if (t.d[u] >= 0) *reinterpret_cast<uint4*>(p + static_cast<int64_t>(t.d[u]) * bytes) = t.x[u];
     }
   };
-  look(0, 0);
-  look(1, 1);
+  look(0, 0, entry(0));
+  look(1, 1, entry(1));
+  Entry ahead = entry(2);
   __syncthreads();
   Batch now = load(0);
   int count = now.n;
@@ -178,8 +185,9 @@ __global__ void __launch_bounds__(kThreads) kv_keep_kernel(const __grid_constant
     Batch then;
     then.n = 0;
     if (more) {
+      look(b + 2, after, ahead);  // (its buffer was read two batches ago)
       then = load(next);
-      look(b + 2, after);  // (its buffer was read two batches ago)
+      ahead = entry(b + 3);
     }
     __syncthreads();  // every thread has read batch b
     store(now);

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kBlock) kv_read_kernel(const RowsArgs a) {
       if (!Q8) {
         load8<MK_F16, true>(static_cast<const __half*>(pool) + e, x[i]);
       } else {
-        const uint2 c = __ldg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(pool) + e));
+        const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(pool) + e);
         const float d = __half2float(static_cast<const __half*>(i < 2 ? a.pool.k_scale : a.pool.v_scale)[e / 32]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {  // 2^23 + (code + 128) by a byte move: integer conversions run at a quarter of the rate

@@ -59,7 +59,9 @@ inline bool dense_vec(const mk_dense& d, int dtype) {
 // ------------------------------------------------------------ early launches
 // Kernels are launched while the one before them in the stream ends: their launch overlaps its end (tree of 8 nodes over
 // 4K tokens 20.5 -> 17.5 us a call, 64 rotated rows 11.9 -> 10.5). The first thing every thread does with memory that
-// others use is to wait for that end, so a kernel is over only after all those before it. A kernel lets the next one in
+// others use is to wait for that end, so a kernel is over only after all those before it. What it reads then it reads with
+// ordinary loads, which the wait orders: read-only ones (ld.global.nc) promise the right value only of memory that nothing
+// writes while the kernel runs, and it runs while the one before still writes. A kernel lets the next one in
 // before its end only where that is its own second part: another kernel's blocks, placed among those still running,
 // would lie unevenly on the SMs (kept tokens 132 -> 152 us).
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
@@ -88,16 +90,16 @@ struct SeqView {
 };
 __device__ __forceinline__ SeqView seq_view(const mk_kv_rows& m, int s) {
   SeqView v;
-  v.r0 = clampi(__ldg(m.row_start + s), 0, m.n_rows);
-  v.q_len = clampi(__ldg(m.row_start + s + 1), v.r0, m.n_rows) - v.r0;
-  v.kv_len = clampi(__ldg(m.kv_len + s), 0, m.table_stride * kPage);
+  v.r0 = clampi(m.row_start[s], 0, m.n_rows);
+  v.q_len = clampi(m.row_start[s + 1], v.r0, m.n_rows) - v.r0;
+  v.kv_len = clampi(m.kv_len[s], 0, m.table_stride * kPage);
   return v;
 }
 
 // Token row (page * 16 + slot) of position pos of sequence s, -1 when it has none.
 __device__ __forceinline__ int token_at(const mk_kv_rows& m, int n_pages, int s, int pos) {
   if (pos < 0 || pos >= m.table_stride * kPage) return -1;
-  const int page = __ldg(m.tables + static_cast<int64_t>(s) * m.table_stride + pos / kPage);
+  const int page = m.tables[static_cast<int64_t>(s) * m.table_stride + pos / kPage];
   return page >= 0 && page < n_pages ? page * kPage + pos % kPage : -1;
 }
 
@@ -106,7 +108,7 @@ __device__ __forceinline__ int seq_of_row(const mk_kv_rows& m, int r, SeqView& v
   int lo = 0, hi = m.n_seqs;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(m.row_start + mid + 1) > r) hi = mid; else lo = mid + 1;
+    if (m.row_start[mid + 1] > r) hi = mid; else lo = mid + 1;
   }
   if (lo >= m.n_seqs) return -1;
   v = seq_view(m, lo);
@@ -123,7 +125,7 @@ __device__ __forceinline__ int token_row(const mk_kv_rows& m, int n_pages, int r
 // A node's parent in a tree of drafts (parents: of its sequence's rows), -1 for none: only a node before it can be one,
 // so every walk towards the root ends.
 __device__ __forceinline__ int parent_of(const int32_t* parents, int node) {
-  const int p = __ldg(parents + node);
+  const int p = parents[node];
   return p >= 0 && p < node ? p : -1;
 }
 
@@ -156,7 +158,7 @@ __device__ __forceinline__ void load8(const typename Elem<DT>::T* p, float* x) {
   if (VEC) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-      reinterpret_cast<uint4*>(t)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      reinterpret_cast<uint4*>(t)[i] = reinterpret_cast<const uint4*>(p)[i];
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = p[i];

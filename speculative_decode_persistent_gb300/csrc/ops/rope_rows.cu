@@ -67,7 +67,7 @@ __device__ __forceinline__ Raw<DT> fetch8(const typename Elem<DT>::T* p) {
   Raw<DT> r;
   if (VEC) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) r.w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
   } else {
     alignas(16) typename Elem<DT>::T t[8];
 #pragma unroll
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kBlock, 2) rope_write_kernel(const __grid_cons
       token = token_at(a.rows, a.pool.n_pages, seq, at);
       pos = at;
       if (a.positions) {
-        pos = __ldg(a.positions + row);
+        pos = a.positions[row];
       } else if (a.parents) {
         pos = at - node;
         for (int n = parent_of(a.parents + v.r0, node); n >= 0; n = parent_of(a.parents + v.r0, n)) ++pos;
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kBlock, 2) rope_write_kernel(const __grid_cons
   if (h0 < a.hq + hkv) {  // (a block of v alone turns nothing)
     for (int i = tid; i < n_rows * half; i += kBlock) {
       const int r = i / half, j = i - r * half;
-      const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(row_pos[r])) * __ldg(a.rope.turns + j);
+      const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(row_pos[r])) * a.rope.turns[j];
       float sn, cs;
       sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
       table[r * rot + j] = cs;
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(kBlock, 2) rope_write_kernel(const __grid_cons
   if (gain) {
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
-      const ulonglong2 g0 = __ldg(reinterpret_cast<const ulonglong2*>(gain + lo + 2 * i));
-      const ulonglong2 g1 = __ldg(reinterpret_cast<const ulonglong2*>(gain + lo + step + 2 * i));
+      const ulonglong2 g0 = *reinterpret_cast<const ulonglong2*>(gain + lo + 2 * i);
+      const ulonglong2 g1 = *reinterpret_cast<const ulonglong2*>(gain + lo + step + 2 * i);
       gx[i] = g0.x; gx[i + 1] = g0.y;
       gy[i] = g1.x; gy[i + 1] = g1.y;
     }

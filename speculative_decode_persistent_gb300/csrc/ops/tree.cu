@@ -79,7 +79,7 @@ __device__ __forceinline__ uint64_t scan(const typename Elem<DT>::T* x, int begi
   };
   auto get = [&](int j, float* y) {
     if (VEC) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(x + j));
+      const uint4 w = *reinterpret_cast<const uint4*>(x + j);
 #pragma unroll
       for (int k = 0; k < kV; ++k) y[k] = Elem<DT>::get(reinterpret_cast<const T*>(&w)[k]);
     } else {
@@ -145,7 +145,7 @@ __device__ __forceinline__ void walk(const TreeArgs& a, const SeqView& v, int se
   auto fetch = [&](int j) {
     if (j < v.q_len) {
       parent = a.parents ? parent_of(a.parents + v.r0, j) : j - 1;
-      tok = __ldg(a.tokens + v.r0 + j);
+      tok = a.tokens[v.r0 + j];
     }
   };
   fetch(1 + lane);
