@@ -97,10 +97,11 @@ __device__ __forceinline__ void put8(typename Elem<DT>::T* p, const float* x) {
   }
 }
 
-// A head's (mean x^2 + eps)^-1/2 where the squares leave 32 bits: of the values divided by a power of two near the
-// largest. `plain` where that is no number to divide by (0, infinite, NaN).
-__device__ __forceinline__ float norm_factor(const float (&x)[8], const float (&y)[8], bool in, int lanes, uint32_t mask, float inv_dh, float eps,
-                                             float plain) {
+// A head's (mean x^2 + eps)^-1/2 where the squares leave 32 bits, in two factors (their product may leave them too): the
+// power of two that brings the largest value to [1, 4), and the rest. 1 and `plain` where there is no such power (0, infinite,
+// NaN), and where eps is so far above the squares that it leaves 32 bits with them: then `plain` is eps's alone.
+__device__ __forceinline__ float2 norm_factors(const float (&x)[8], const float (&y)[8], bool in, int lanes, uint32_t mask, float inv_dh, float eps,
+                                               float plain) {
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -109,7 +110,7 @@ __device__ __forceinline__ float norm_factor(const float (&x)[8], const float (&
   }
   if (!in) top = 0.f;
   for (int m = lanes >> 1; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, m));
-  if (!(top > 0.f && top < INFINITY)) return plain;
+  if (!(top > 0.f && top < INFINITY)) return make_float2(1.f, plain);
   // 2^-e with 2^e near top, kept normal, as is its reciprocal
   const float s = __uint_as_float(static_cast<uint32_t>(254 - min(max(static_cast<int>(__float_as_uint(top) >> 23), 1), 253)) << 23);
   float sum = 0.f;
@@ -117,7 +118,8 @@ __device__ __forceinline__ float norm_factor(const float (&x)[8], const float (&
   for (int i = 0; i < 8; ++i) sum += (x[i] * s) * (x[i] * s) + (y[i] * s) * (y[i] * s);
   if (!in) sum = 0.f;
   for (int m = lanes >> 1; m; m >>= 1) sum += __shfl_xor_sync(mask, sum, m);
-  return s * rsqrtf(fmaf(sum, inv_dh, eps * s * s));
+  const float e = eps * s * s;
+  return e < INFINITY ? make_float2(s, rsqrtf(fmaf(sum, inv_dh, e))) : make_float2(1.f, plain);
 }
 
 template <int DT, bool Q8, bool VEC, int PER>
@@ -235,15 +237,22 @@ __global__ void __launch_bounds__(kBlock, 2) rope_write_kernel(const __grid_cons
         if (lanes > 8) sum += __shfl_xor_sync(mask, sum, 8);
         float f = rsqrtf(fmaf(sum, a.inv_dh, a.rope.eps));
         if constexpr (decltype(rare)::value) {
-          f = norm_factor(x, y, in, lanes, mask, a.inv_dh, a.rope.eps, f);
+          const float2 sf = norm_factors(x, y, in, lanes, mask, a.inv_dh, a.rope.eps, f);
+          const uint64_t p2 = pack2(sf.x, sf.x);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x2[i] = mul2(x2[i], p2);
+            y2[i] = mul2(y2[i], p2);
+          }
+          f = sf.y;
         } else if (DT != MK_F16 && (!(sum < 3e38f) || (sum < 1e-30f && a.rope.eps < 1e-30f))) {  // (binary16's squares fit)
           return true;
         }
         const uint64_t f2 = pack2(f, f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x2[i] = mul2(x2[i], mul2(f2, gx[i]));
-          y2[i] = mul2(y2[i], mul2(f2, gy[i]));
+          x2[i] = mul2(mul2(x2[i], f2), gx[i]);  // (x f is at most dh^1/2; f g may leave 32 bits)
+          y2[i] = mul2(mul2(y2[i], f2), gy[i]);
         }
       }
       if (turns) {
