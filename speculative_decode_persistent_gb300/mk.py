@@ -241,6 +241,7 @@ class Engine:
         self.max_seqs = max_seqs
         self.n_slots = n_state_slots
         self.n_gdn = sum(1 for k in model["kinds"] if k == 0)
+        self.n_kv = sum(1 for k in model["kinds"] if k == 1) + self.layout.has_mtp
         self.conv_ch = 2 * model["hk"] * model["dk"] + model["hv"] * model["dv"]
 
     # ---------------------------------------------------------------- state
@@ -254,8 +255,7 @@ class Engine:
 
     def kv_views(self):
         m, torch = self.model, self.torch
-        n_kv = sum(1 for k in m["kinds"] if k == 1) + (1 if self.layout.has_mtp else 0)
-        shape = (n_kv, self.layout.n_pages, m["hkv"], 16, m["dh"])
+        shape = (self.n_kv, self.layout.n_pages, m["hkv"], 16, m["dh"])
         n = int(np.prod(shape))
         if self.layout.kv_dtype == MK_KV_Q8:
             sshape = shape[:-1] + (m["dh"] // 32,)
@@ -327,7 +327,7 @@ class Engine:
         if len(free) < n:
             raise MkError(-3, "clone_sequence (no free pages)")
         new = np.array(free[:n], np.int32)
-        if n and src != dst:
+        if n and self.n_kv and src != dst:
             from . import ops
             self._before_current()
             ops.kv_copy(self.kv_layers(), *(torch.from_numpy(a.astype(np.int32)).to(self.device) for a in (info["pages"], new)))
@@ -355,7 +355,8 @@ class Engine:
         return ops.KVPool(*(views[n][layer] for n in names))
 
     def kv_layers(self):
-        """All KV layers of the pool as an ops.KVLayers: for ops.kv_copy, kv_keep."""
+        """All KV layers of the pool (refused when the model has none) as an
+        ops.KVLayers: for ops.kv_copy, kv_keep."""
         from . import ops
         views = self.kv_views()
         return ops.KVLayers(*(views[n] for n in (("kq", "vq", "ks", "vs") if self.layout.kv_dtype == MK_KV_Q8 else ("k", "v"))))
@@ -374,7 +375,7 @@ class Engine:
         if not 0 <= new_rows <= info["length"] or any(not a < b < new_rows for a, b in zip([-1] + keep, keep)):
             raise MkError(-1, "seq_keep (0 to length rows, ascending indices among them)")
         length = info["length"] - new_rows + len(keep)
-        if new_rows:
+        if new_rows and self.n_kv:
             self._before_current()
             rows = self.seq_rows([seq], [new_rows])
             entries = torch.tensor(keep + [-1] * (new_rows - len(keep)), dtype=torch.int32, device=self.device)
@@ -411,9 +412,8 @@ class Engine:
         seq_set or as seq_get gives it; zero when not given. A refused load
         leaves everything as it was."""
         from . import ops
-        torch, m = self.torch, self.model
-        n_kv = sum(1 for x in m["kinds"] if x == 1) + (1 if self.layout.has_mtp else 0)
-        if k.dim() != 4 or k.shape != v.shape or k.shape[0] != n_kv:
+        torch = self.torch
+        if k.dim() != 4 or k.shape != v.shape or k.shape[0] != self.n_kv:
             raise MkError(-1, "seq_load (k, v [kv layers][tokens][kv heads][head dim])")
         if not 0 <= seq < self.max_seqs:
             raise MkError(-1, "seq_load (sequence)")
@@ -442,7 +442,7 @@ class Engine:
         if n:
             dev = [torch.tensor(x, dtype=torch.int32, device=self.device) for x in ([0, n], [n], [pages])]
             rows = ops.KVRows(*dev, n_rows=n)
-            for i in range(n_kv):
+            for i in range(self.n_kv):
                 ops.kv_write(self.kv_pool(i), rows, k[i], v[i])
         Sv, Cv = self.state_views()
         if Sv is not None:
@@ -458,12 +458,11 @@ class Engine:
         from . import ops
         torch, m = self.torch, self.model
         n = self.seq_get(seq)["length"]
-        n_kv = sum(1 for x in m["kinds"] if x == 1) + (1 if self.layout.has_mtp else 0)
-        k, v = (torch.empty((n_kv, n, m["hkv"], m["dh"]), dtype=dtype or torch.float16, device=self.device) for _ in "kv")
+        k, v = (torch.empty((self.n_kv, n, m["hkv"], m["dh"]), dtype=dtype or torch.float16, device=self.device) for _ in "kv")
         if n:
             self._before_current()
             rows = self.seq_rows([seq], [n])
-            for i in range(n_kv):
+            for i in range(self.n_kv):
                 ops.kv_read(self.kv_pool(i), rows, out=(k[i], v[i]))
             self._after_current()
         return k, v

@@ -1,0 +1,54 @@
+"""An engine's cached contexts copied and thinned out (Engine.clone_sequence, seq_keep): models without KV
+layers, the recurrent state of what is kept, calls beside the engine's own stream."""
+import os
+import sys
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+
+@pytest.fixture(scope="module")
+def mk():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from speculative_decode_persistent_gb300 import mk as m
+    return m
+
+
+def _engine(mk, kinds=None, **kw):
+    from gen import configs
+    from gen.synth import make_weights
+    model = dict(configs.TINY, **({} if kinds is None else {"kinds": kinds}))
+    return mk.Engine(model, make_weights(model, 0), 0, 16, **kw)
+
+
+def _decode(eng, seq, n, token=11):
+    got = []
+    for _ in range(n):
+        out, _ = eng.step([token], [eng.seq_get(seq)["length"]], [seq])
+        eng.commit([seq], [1])
+        token = int(out[0])
+        got.append(token)
+    return got
+
+
+def test_models_without_kv_layers(mk):
+    """Recurrent layers only: a sequence has pages and a state, and no layer keeps K and V."""
+    eng = _engine(mk, [0, 0, 0, 0])
+    eng.seq_new(0)
+    for i, t in enumerate((5, 6, 7)):
+        eng.step([t], [i], [0])
+        eng.commit([0], [1])
+    eng.clone_sequence(0, 1)
+    a, b = eng.seq_get(0), eng.seq_get(1)
+    assert b["length"] == a["length"] == 3 and torch.equal(a["S"], b["S"]) and torch.equal(a["conv"], b["conv"])
+    eng.clone_sequence(1, 1)
+    assert eng.seq_keep(1, 2, [0]) == 2 and eng.seq_get(1)["length"] == 2
+    assert eng.seq_keep(1, 0, []) == 2
+    eng.clone_sequence(0, 1)
+    assert _decode(eng, 0, 4) == _decode(eng, 1, 4)
+    eng.close()
