@@ -278,6 +278,7 @@ class Engine:
         Sv, Cv = self.state_views()
         if Sv is None:
             S = conv = None
+        self._before_current()
         if S is not None:
             Sv[seq, 0].copy_(self._tensor(S))
         if conv is not None:
@@ -306,6 +307,7 @@ class Engine:
         """Install an empty sequence (no cached token) with a zero recurrent state."""
         Sv, Cv = self.state_views()
         if Sv is not None:
+            self._before_current()
             Sv[seq, 0].zero_()
             Cv[seq, 0].zero_()
             self.torch.cuda.synchronize(self.device)
@@ -327,9 +329,9 @@ class Engine:
         if len(free) < n:
             raise MkError(-3, "clone_sequence (no free pages)")
         new = np.array(free[:n], np.int32)
+        self._before_current()
         if n and self.n_kv and src != dst:
             from . import ops
-            self._before_current()
             ops.kv_copy(self.kv_layers(), *(torch.from_numpy(a.astype(np.int32)).to(self.device) for a in (info["pages"], new)))
         elif n:  # onto pages that may be its own: all are read before one is written
             si = torch.as_tensor(info["pages"].astype(np.int64), device=self.device)
@@ -375,8 +377,8 @@ class Engine:
         if not 0 <= new_rows <= info["length"] or any(not a < b < new_rows for a, b in zip([-1] + keep, keep)):
             raise MkError(-1, "seq_keep (0 to length rows, ascending indices among them)")
         length = info["length"] - new_rows + len(keep)
+        self._before_current()
         if new_rows and self.n_kv:
-            self._before_current()
             rows = self.seq_rows([seq], [new_rows])
             entries = torch.tensor(keep + [-1] * (new_rows - len(keep)), dtype=torch.int32, device=self.device)
             ops.kv_keep(self.kv_layers(), rows, entries)

@@ -52,3 +52,46 @@ def test_models_without_kv_layers(mk):
     eng.clone_sequence(0, 1)
     assert _decode(eng, 0, 4) == _decode(eng, 1, 4)
     eng.close()
+
+
+def test_copies_come_after_the_engines_work(mk):
+    """The engine on a stream of its own, the calls on the default one: the states that they copy are those that the
+    work queued there leaves, also where no K and V move."""
+    s = torch.cuda.Stream()
+    eng = _engine(mk, stream=s)
+    eng.seq_new(0)
+    eng.step([5, 6, 7, 8], [0, 1, 2, 3], [0] * 4, [1, 1, 1, 2])
+    assert eng.seq_get(0)["slot"] != 0
+
+    def later(seq, x):  # the committed state changes on the engine's stream, a tenth of a second from now
+        slot = eng.seq_get(seq)["slot"]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(200_000_000)
+            for t in eng.state_views():
+                t[seq, slot].fill_(x)
+
+    def all_are(seq, x):
+        info = eng.seq_get(seq)
+        return info["slot"] == 0 and bool((info["S"] == x).all()) and bool((info["conv"] == x).all())
+
+    later(0, 2.0)
+    assert eng.seq_keep(0, 0, []) == 4 and all_are(0, 2.0)
+    later(0, 3.0)
+    eng.clone_sequence(0, 0)
+    assert eng.seq_get(0)["length"] == 4 and all_are(0, 3.0)
+    later(0, 4.0)
+    eng.clone_sequence(0, 1)
+    assert all_are(1, 4.0)
+    S, conv = (torch.full_like(eng.seq_get(1)[x], 6.0) for x in ("S", "conv"))
+    later(1, 7.0)
+    eng.seq_set(1, 4, eng.seq_get(1)["pages"], S, conv)
+    assert all_are(1, 6.0)
+    later(1, 8.0)
+    eng.seq_new(1)
+    assert all_are(1, 0.0)
+    eng.seq_new(2)  # nothing cached: no pages to copy either
+    later(2, 5.0)
+    eng.clone_sequence(2, 3)
+    assert eng.seq_get(3)["length"] == 0 and all_are(3, 5.0)
+    eng.close()
