@@ -290,6 +290,20 @@ class Engine:
     def _tensor(self, x):
         return x.detach() if self.torch.is_tensor(x) else self.torch.from_numpy(np.ascontiguousarray(x, np.float32))
 
+    def _states(self, what, S, conv):
+        """S and conv of a sequence as fp32 tensors on the device, checked; None where not given."""
+        out = []
+        for x, view in zip((S, conv), self.state_views()):
+            if x is not None and view is not None:
+                try:
+                    x = self._tensor(x).to(self.device, self.torch.float32)
+                except (TypeError, ValueError, RuntimeError):
+                    raise MkError(-1, f"{what} (the recurrent state is numbers)") from None
+                if x.shape != view.shape[2:]:
+                    raise MkError(-1, f"{what} (shape of the recurrent state)")
+            out.append(x)
+        return out
+
     def seq_get(self, seq: int):
         n = self.layout.max_pages_per_seq
         length, npg, slot = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
@@ -363,30 +377,32 @@ class Engine:
         views = self.kv_views()
         return ops.KVLayers(*(views[n] for n in (("kq", "vq", "ks", "vs") if self.layout.kv_dtype == MK_KV_Q8 else ("k", "v"))))
 
-    def seq_keep(self, seq: int, new_rows: int, keep):
+    def seq_keep(self, seq: int, new_rows: int, keep, S=None, conv=None):
         """Keep some of a committed sequence's last new_rows cached tokens (the
         accepted path of a tree of drafts, say): keep lists them, ascending,
         as indices among those rows; they move up behind the tokens before, in
         all KV layers, the length shrinks, and pages wholly behind it return to
-        the pool. The committed recurrent state stays what it is; a pending
-        step is dropped. Returns the new length."""
+        the pool; a pending step is dropped. S, conv: the recurrent state that
+        belongs to the kept tokens, as in seq_load. Where not given, the
+        committed one stays, which has seen the dropped tokens too: right for
+        a context that loses old tokens, but after rejected drafts the next
+        step would go on from a state that no text gives. A refused call
+        leaves everything as it was. Returns the new length."""
         from . import ops
         torch = self.torch
         info = self.seq_get(seq)
         new_rows, keep = int(new_rows), [int(k) for k in keep]
         if not 0 <= new_rows <= info["length"] or any(not a < b < new_rows for a, b in zip([-1] + keep, keep)):
             raise MkError(-1, "seq_keep (0 to length rows, ascending indices among them)")
+        state = self._states("seq_keep", S, conv)
         length = info["length"] - new_rows + len(keep)
         self._before_current()
         if new_rows and self.n_kv:
             rows = self.seq_rows([seq], [new_rows])
             entries = torch.tensor(keep + [-1] * (new_rows - len(keep)), dtype=torch.int32, device=self.device)
             ops.kv_keep(self.kv_layers(), rows, entries)
-        Sv, Cv = self.state_views()
-        if Sv is not None and info["slot"]:
-            Sv[seq, 0].copy_(Sv[seq, info["slot"]])
-            Cv[seq, 0].copy_(Cv[seq, info["slot"]])
-        self.seq_set(seq, length, info["pages"][:-(-length // 16)])
+        state = [info[n] if x is None else x for n, x in zip(("S", "conv"), state)]
+        self.seq_set(seq, length, info["pages"][:-(-length // 16)], *state)
         return length
 
     def seq_rows(self, seqs, new_rows):
@@ -419,16 +435,7 @@ class Engine:
             raise MkError(-1, "seq_load (k, v [kv layers][tokens][kv heads][head dim])")
         if not 0 <= seq < self.max_seqs:
             raise MkError(-1, "seq_load (sequence)")
-        state = []
-        for x, view in zip((S, conv), self.state_views()):
-            if x is not None and view is not None:
-                try:
-                    x = self._tensor(x).to(self.device, torch.float32)
-                except (TypeError, ValueError, RuntimeError):
-                    raise MkError(-1, "seq_load (the recurrent state is numbers)") from None
-                if x.shape != view.shape[2:]:
-                    raise MkError(-1, "seq_load (shape of the recurrent state)")
-            state.append(x)
+        state = self._states("seq_load", S, conv)
         used = set()
         for s in range(self.max_seqs):
             if s != seq:

@@ -95,3 +95,55 @@ def test_copies_come_after_the_engines_work(mk):
     eng.clone_sequence(2, 3)
     assert eng.seq_get(3)["length"] == 0 and all_are(3, 5.0)
     eng.close()
+
+
+def test_kept_tokens_with_their_state(mk):
+    """After rejected tokens the state of the kept ones goes in with them, and the sequence goes on as one that never
+    saw the others."""
+    eng = _engine(mk)
+    want = None
+    for seq, texts in ((0, (5, 6)), (1, (5, 6, 7, 8))):
+        eng.seq_new(seq)
+        for i, t in enumerate(texts):
+            eng.step([t], [i], [seq])
+            eng.commit([seq], [1])
+            if i == 1:
+                S, conv = (eng.seq_get(seq)[x].clone() for x in ("S", "conv"))
+        if seq == 0:
+            eng.clone_sequence(0, 2)
+            eng.clone_sequence(0, 3)
+            want = _decode(eng, 0, 6)
+    assert eng.seq_keep(1, 2, [], S, conv) == 2
+    assert torch.equal(eng.seq_get(1)["S"], S) and torch.equal(eng.seq_get(1)["conv"], conv)
+    assert _decode(eng, 1, 6) == want
+    # the second of two drafts beside each other was right: its K and V lie one slot too far, its state is given from the host
+    eng.step([9], [2], [2])
+    eng.commit([2], [1])
+    eng.step([9], [2], [3])
+    eng.commit([3], [1])
+    S, conv = eng.seq_get(3)["S"].cpu(), eng.seq_get(3)["conv"].cpu().numpy()
+    k, v = eng.seq_kv(2)
+    eng.seq_load(4, torch.cat([k[:, :2], k[:, 1:2], k[:, 2:]], 1), torch.cat([v[:, :2], v[:, 1:2], v[:, 2:]], 1))
+    assert eng.seq_keep(4, 2, [1], S, conv) == 3
+    assert all(torch.equal(a, b) for a, b in zip(eng.seq_kv(4), (k, v)))
+    assert _decode(eng, 4, 6) == _decode(eng, 3, 6)
+    eng.close()
+
+
+def test_a_refused_keep_leaves_everything(mk):
+    eng = _engine(mk)
+    eng.seq_new(0)
+    eng.step([5, 6, 7, 8], [0, 1, 2, 3], [0] * 4, [1, 1, 1, 2])
+    info, (k, v) = eng.seq_get(0), eng.seq_kv(0)
+    S, conv = info["S"].clone(), info["conv"].clone()
+    for args in ((5, [0]), (2, [2]), (2, [1, 0]), (2, [0], S[None]), (2, [0], S, conv[1:]), (2, [0], "x"), (2, [0], S, [["x"]])):
+        with pytest.raises(mk.MkError) as e:
+            eng.seq_keep(0, *args)
+        assert e.value.status == -1
+        now = eng.seq_get(0)
+        assert now["length"] == 4 and torch.equal(now["S"], S) and torch.equal(now["conv"], conv)
+        assert all(torch.equal(a, b) for a, b in zip(eng.seq_kv(0), (k, v)))
+    # one of the two alone: the other stays
+    assert eng.seq_keep(0, 1, [], None, conv * 2) == 3
+    assert torch.equal(eng.seq_get(0)["S"], S) and torch.equal(eng.seq_get(0)["conv"], conv * 2)
+    eng.close()
