@@ -223,13 +223,15 @@ PyObject* make_pool(PyObject* const* a) {
     no(LAYERS ? "k and v are [layers][pages][kv heads][16][head dim] of one type" : "k and v are [pages][kv heads][16][head dim] of one type");
   const int64_t pages = k.size(o), heads = k.size(1 + o), dh = k.size(3 + o), n = LAYERS ? k.size(0) : 1;
   const int64_t layer = LAYERS && n > 1 ? k.stride(0) : 0;
-  // each layer contiguous, all tensors' layers equally far apart
-  auto packed = [&](const at::Tensor& t, int64_t last, int64_t per) {
+  // each layer contiguous (by torch's rule: strides of dimensions of size 1 say nothing), all tensors' layers equally far apart
+  auto packed = [&](const at::Tensor& t, int64_t per) {
     if (!LAYERS) return t.is_contiguous();
-    if (pages && heads && last && (t.stride(4) != 1 || t.stride(3) != last || t.stride(2) != kPage * last || t.stride(1) != heads * kPage * last)) return false;
+    int64_t want = 1;
+    for (int d = 4; d >= 1; want *= t.size(d--))
+      if (t.numel() && t.size(d) != 1 && t.stride(d) != want) return false;
     return n == 1 || (t.stride(0) * per == layer && layer >= pages * heads * kPage * dh && layer % 256 == 0);
   };
-  if (!packed(k, dh, 1) || !packed(v, dh, 1)) no(LAYERS ? "contiguous layers, equally far apart in all tensors" : "contiguous tensors");
+  if (!packed(k, 1) || !packed(v, 1)) no(LAYERS ? "contiguous layers, equally far apart in all tensors" : "contiguous tensors");
   const int device = cuda_index(k);
   if (!on(v, device)) no("one device");
   if (n > INT32_MAX || pages > INT32_MAX || heads > INT32_MAX || dh > INT32_MAX) throw Refusal{MK_ERR_UNSUPPORTED, name};
@@ -243,7 +245,7 @@ PyObject* make_pool(PyObject* const* a) {
         const at::Tensor& s = tensor(a[2 + i], name);
         fits = s.dim() == 4 + o && half_type(s.scalar_type()) && (!LAYERS || s.size(0) == n) && s.size(o) == pages && s.size(1 + o) == heads &&
                s.size(2 + o) == kPage && s.size(3 + o) == dh / 32 && on(s, device);
-        if (fits && !packed(s, dh / 32, 32)) no(LAYERS ? "contiguous layers, equally far apart in all tensors" : "contiguous scales");
+        if (fits && !packed(s, 32)) no(LAYERS ? "contiguous layers, equally far apart in all tensors" : "contiguous scales");
         (i ? p.v_scale : p.k_scale) = s.data_ptr();
       }
       if (!fits) no("an int8 pool needs binary16 scales, of the pool's shape with head dim / 32");

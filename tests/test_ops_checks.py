@@ -1,0 +1,41 @@
+"""The checks of the pool operators' Python calls, each shown by its own message: a call with one fault alone is
+refused for that fault. (CPU: what is asked of devices comes last.)"""
+import os
+import sys
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+sys.path.insert(0, os.path.join(ROOT, "tests"))
+
+
+@pytest.fixture(scope="module")
+def ops():
+    from speculative_decode_persistent_gb300 import build as b
+    b.build()
+    from speculative_decode_persistent_gb300 import ops as o
+    return o
+
+
+def h(*s):
+    return torch.zeros(s, dtype=torch.float16)
+
+
+def i(*s):
+    return torch.zeros(s, dtype=torch.int32)
+
+
+def test_layers_contiguous_by_torchs_rule(ops):
+    """Strides of dimensions of size 1 say nothing, in a KVLayers as in a KVPool."""
+    for views in ([h(3, 4, 16, 1, 64).transpose(2, 3) for _ in "kv"],   # one head
+                  [h(3, 2, 1, 16, 64).transpose(1, 2) for _ in "kv"],   # one page
+                  [h(2, 16, 1, 1, 128).transpose(1, 3) for _ in "kv"]):  # one of both
+        assert all(v[0].is_contiguous() for v in views)
+        ops.KVPool(*(v[0] for v in views))
+        assert ops.KVLayers(*views).n_layers == views[0].shape[0]
+    q = [torch.zeros(3, 4, 16, 1, 64, dtype=torch.int8).transpose(2, 3) for _ in "kv"]
+    ops.KVLayers(*q, *(h(3, 4, 16, 1, 2).transpose(2, 3) for _ in "kv"))
+    for bad in (h(3, 4, 16, 2, 64).transpose(2, 3), h(3, 2, 4, 16, 64).transpose(1, 2), h(3, 4, 2, 16, 128)[..., ::2], h(3, 4, 2, 64, 16).transpose(3, 4)):
+        with pytest.raises(ops.MkError):
+            ops.KVLayers(bad, bad.clone(memory_format=torch.preserve_format))
