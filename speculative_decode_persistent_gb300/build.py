@@ -6,7 +6,10 @@ link step produces speculative_decode_persistent_gb300/libmk.so.
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
+import platform
 import subprocess
 import sys
 import sysconfig
@@ -22,6 +25,7 @@ SOURCES = ["mk_kernel.cu", "mk_api.cu", "mk_pack.cu", "ops/kv_rows.cu", "ops/kv_
            "ops/attend.cu", "ops/attend_f16.cu", "ops/attend_q8.cu", "ops/attend_tree_f16.cu", "ops/attend_tree_q8.cu"]
 BIND = os.path.join(HERE, "_bind.so")
 BIND_SOURCE = os.path.join(CSRC, "ops", "bind.cpp")
+BIND_KEY = os.path.join(BUILD, "bind.key")  # what BIND was built for
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
@@ -33,6 +37,19 @@ def _stale(out: str, deps: list[str]) -> bool:
         return True
     t = os.path.getmtime(out)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _bind_key() -> str:
+    """What a built BIND goes with beside its sources: torch's binary interface, Python's, the machine."""
+    spec = importlib.util.find_spec("torch")
+    return "\n".join((platform.machine(), str(sysconfig.get_config_var("SOABI")), str(spec and spec.origin), importlib.metadata.version("torch")))
+
+
+def _bind_stale(headers: list[str]) -> bool:
+    if _stale(BIND, [BIND_SOURCE] + [h for h in headers if h.endswith(".h")]) or not os.path.exists(BIND_KEY):
+        return True
+    with open(BIND_KEY) as f:
+        return f.read() != _bind_key()
 
 
 def _bind_command(out: str) -> list[str]:
@@ -61,7 +78,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             jobs.append(cmd)
 
     tmp_bind = BIND + f".tmp{os.getpid()}"
-    bind = force or _stale(BIND, [BIND_SOURCE] + [h for h in headers if h.endswith(".h")])
+    bind = force or _bind_stale(headers)
     if bind:
         jobs.append(_bind_command(tmp_bind))
 
@@ -77,6 +94,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 raise RuntimeError("compiler failed: " + " ".join(cmd))
     if bind:
         os.replace(tmp_bind, BIND)
+        with open(BIND_KEY, "w") as f:
+            f.write(_bind_key())
     if force or _stale(SO, objs):
         tmp = SO + f".tmp{os.getpid()}"
         cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]

@@ -29,7 +29,10 @@ import ctypes
 
 import torch
 
-from . import _bind
+try:
+    from . import _bind
+except ImportError as e:
+    raise ImportError("_bind.so is missing, or was built for another torch or Python: run __graft_entry__.build() first") from e
 from .mk import MkError, i32, lib, sz, vp
 
 MK_OPS_MAX_SEQS = 1024
