@@ -42,7 +42,11 @@ def _stale(out: str, deps: list[str]) -> bool:
 def _bind_key() -> str:
     """What a built BIND goes with beside its sources: torch's binary interface, Python's, the machine."""
     spec = importlib.util.find_spec("torch")
-    return "\n".join((platform.machine(), str(sysconfig.get_config_var("SOABI")), str(spec and spec.origin), importlib.metadata.version("torch")))
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # not installed as a package: its files' time
+        version = str(spec and os.path.getmtime(spec.origin))
+    return "\n".join((platform.machine(), str(sysconfig.get_config_var("SOABI")), str(spec and spec.origin), version))
 
 
 def _bind_stale(headers: list[str]) -> bool:

@@ -44,3 +44,10 @@ def test_a_missing_module_says_what_to_do(build):
             "import speculative_decode_persistent_gb300.ops")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode and "build()" in r.stderr.splitlines()[-1]
+
+
+def test_a_torch_without_package_data(build, monkeypatch):
+    def none(name):
+        raise build.importlib.metadata.PackageNotFoundError(name)
+    monkeypatch.setattr(build.importlib.metadata, "version", none)
+    assert len(build._bind_key().splitlines()) == 4
