@@ -212,7 +212,7 @@ mk_status mk_rope_write(const mk_kv_pool* pool, const mk_kv_rows* rows, const mk
  * drafts and one token more, -1 behind them; count [n_seqs]: their number (as
  * mk_step's counts; 0 for a sequence without rows). Rows of no sequence are left alone.
  * work: mk_tree_work_bytes() bytes (0 for few logits), 256-byte aligned, as mk_attend's.
- * Errors: MK_ERR_INVALID, MK_ERR_UNSUPPORTED (vocab above 2^30), MK_ERR_CUDA.
+ * Errors: MK_ERR_INVALID, MK_ERR_UNSUPPORTED (vocab or n_rows above 2^30), MK_ERR_CUDA.
  */
 typedef struct mk_tree_args {
     const int32_t* parents;
@@ -243,7 +243,7 @@ typedef struct mk_kv_layers {
  * Copy page src[i] to page dst[i] (device, [n]) in every layer. A pair with an id
  * outside [0, n_pages) is passed over. A page may be copied several times; one that is
  * written must not be another pair's source or target: what it then holds is open.
- * Errors: MK_ERR_INVALID, MK_ERR_UNSUPPORTED (as the pool's), MK_ERR_CUDA.
+ * Errors: MK_ERR_INVALID, MK_ERR_UNSUPPORTED (as the pool's; n above 2^30), MK_ERR_CUDA.
  */
 mk_status mk_kv_copy(const mk_kv_layers* layers, const int32_t* src, const int32_t* dst, int32_t n, void* stream);
 
@@ -256,7 +256,8 @@ mk_status mk_kv_copy(const mk_kv_layers* layers, const int32_t* src, const int32
  * itself) receives base + the entries kept, at least 0. Slots behind that keep what they hold, and
  * pages wholly behind it are the caller's to free. A row whose slot or target has no page
  * does not move. Sequences of one call must not share pages that a row moves to.
- * Errors: MK_ERR_INVALID, MK_ERR_UNSUPPORTED (as the pool's and the rows'), MK_ERR_CUDA.
+ * Errors: MK_ERR_INVALID, MK_ERR_UNSUPPORTED (as the pool's and the rows'; n_rows above
+ * 2^30), MK_ERR_CUDA.
  */
 mk_status mk_kv_keep(const mk_kv_layers* layers, const mk_kv_rows* rows, const int32_t* keep, int32_t* kv_len, void* stream);
 

@@ -214,6 +214,7 @@ extern "C" mk_status mk_kv_copy(const mk_kv_layers* layers, const int32_t* src, 
   const mk_status st = check_layers(layers);
   if (st != MK_OK) return st;
   if (n < 0) return MK_ERR_INVALID;
+  if (n > kMaxList) return MK_ERR_UNSUPPORTED;
   if (n == 0) return MK_OK;
   if (!src || !dst) return MK_ERR_INVALID;
   const mk_kv_pool& p = layers->pool;
@@ -236,6 +237,7 @@ extern "C" mk_status mk_kv_keep(const mk_kv_layers* layers, const mk_kv_rows* ro
   mk_status st = check_layers(layers);
   if (st == MK_OK) st = check_rows(rows);
   if (st != MK_OK) return st;
+  if (rows->n_rows > kMaxList) return MK_ERR_UNSUPPORTED;
   if (rows->n_seqs == 0) return MK_OK;
   if (!keep && rows->n_rows > 0) return MK_ERR_INVALID;
   const mk_kv_pool& p = layers->pool;

@@ -14,6 +14,8 @@ namespace mk {
 namespace ops {
 
 constexpr int kPage = 16;
+// Entries of a list, or rows, that a kernel steps through in strides of up to 2^17: the next index stays within 32 bits.
+constexpr int kMaxList = 1 << 30;
 
 // ------------------------------------------------------------- host checks
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

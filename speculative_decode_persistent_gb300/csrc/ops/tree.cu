@@ -233,7 +233,7 @@ cudaError_t launch(const TreeArgs& a, bool vec, cudaStream_t stream) {
 
 extern "C" size_t mk_tree_work_bytes(const mk_kv_rows* rows, int32_t vocab) {
   using namespace mk::ops;
-  if (check_rows(rows) != MK_OK || vocab <= 0 || vocab > kMaxVocab || small(*rows, vocab)) return 0;
+  if (check_rows(rows) != MK_OK || rows->n_rows > kMaxList || vocab <= 0 || vocab > kMaxVocab || small(*rows, vocab)) return 0;
   return static_cast<size_t>(part_bytes(rows->n_rows, vocab)) + static_cast<size_t>(rows->n_rows) * 4 + 256;
 }
 
@@ -242,7 +242,7 @@ extern "C" mk_status mk_tree_accept(const mk_kv_rows* rows, const mk_tree_args* 
   const mk_status st = check_rows(rows);
   if (st != MK_OK) return st;
   if (!t || t->vocab <= 0 || t->dtype < MK_F32 || t->dtype > MK_BF16) return MK_ERR_INVALID;
-  if (t->vocab > kMaxVocab) return MK_ERR_UNSUPPORTED;
+  if (t->vocab > kMaxVocab || rows->n_rows > kMaxList) return MK_ERR_UNSUPPORTED;
   if (rows->n_seqs == 0) return MK_OK;
   if (!t->count) return MK_ERR_INVALID;
   if (rows->n_rows > 0) {

@@ -39,3 +39,16 @@ def test_layers_contiguous_by_torchs_rule(ops):
     for bad in (h(3, 4, 16, 2, 64).transpose(2, 3), h(3, 2, 4, 16, 64).transpose(1, 2), h(3, 4, 2, 16, 128)[..., ::2], h(3, 4, 2, 64, 16).transpose(3, 4)):
         with pytest.raises(ops.MkError):
             ops.KVLayers(bad, bad.clone(memory_format=torch.preserve_format))
+
+
+def test_lists_whose_indices_would_leave_32_bits(ops):
+    """Kernels step through lists in strides: a list that ends near 2^31 would wrap an index to before its start."""
+    from test_tree_ops import _layers, _pool, _rows, _tree
+    assert _pool(ops).n_pages
+    L = ops.lib
+    for n in ((1 << 30) + 1, 2 ** 31 - 1, 2 ** 31 - 65536):
+        assert L.mk_kv_copy(_layers(ops), 4096, 4096, n, None) == -8
+        assert L.mk_kv_keep(_layers(ops), _rows(ops, n_rows=n), 4096, None, None) == -8
+        assert L.mk_tree_accept(_rows(ops, n_rows=n), _tree(ops, work_bytes=1 << 62), None) == -8
+        assert L.mk_tree_work_bytes(_rows(ops, n_rows=n), 100) == 0
+    assert L.mk_tree_work_bytes(_rows(ops, n_rows=1 << 30), 100) > 0
