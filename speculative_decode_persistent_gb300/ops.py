@@ -36,6 +36,8 @@ except ImportError as e:
 from .mk import MkError, i32, lib, sz, vp
 
 MK_OPS_MAX_SEQS = 1024
+PAGE_TOKENS = 16
+DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # MK_F32, MK_F16, MK_BF16
 _INVALID = -1
 
 i64, u64, f32 = ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
@@ -117,7 +119,7 @@ class KVPool:
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         self.h = _bind.pool(k, v, k_scale, v_scale)
-        self.tensors = (k, v, k_scale, v_scale)
+        self.tensors = (k, v) if k_scale is None else (k, v, k_scale, v_scale)
 
     device = property(lambda self: self.tensors[0].device)
     q8 = property(lambda self: self.tensors[0].dtype == torch.int8)
@@ -135,7 +137,7 @@ class KVLayers:
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         self.h = _bind.layers(k, v, k_scale, v_scale)
-        self.tensors = (k, v, k_scale, v_scale)
+        self.tensors = (k, v) if k_scale is None else (k, v, k_scale, v_scale)
 
     device, q8, n_pages, hkv, dh = KVPool.device, KVPool.q8, KVPool.n_pages, KVPool.hkv, KVPool.dh
     n_layers = property(lambda self: self.tensors[0].shape[0])

@@ -52,3 +52,19 @@ def test_lists_whose_indices_would_leave_32_bits(ops):
         assert L.mk_tree_accept(_rows(ops, n_rows=n), _tree(ops, work_bytes=1 << 62), None) == -8
         assert L.mk_tree_work_bytes(_rows(ops, n_rows=n), 100) == 0
     assert L.mk_tree_work_bytes(_rows(ops, n_rows=1 << 30), 100) > 0
+
+
+def test_names_and_tensors(ops):
+    """What the module and its handles offered before their marshalling was compiled."""
+    assert ops.PAGE_TOKENS == 16 and ops.MK_OPS_MAX_SEQS == 1024
+    assert ops.DTYPES == {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+    k, v = h(4, 2, 16, 64), h(4, 2, 16, 64)
+    pool = ops.KVPool(k, v)
+    assert pool.tensors[0] is k and pool.tensors[1] is v and len(pool.tensors) == 2
+    assert (pool.device, pool.q8, pool.n_pages, pool.hkv, pool.dh) == (k.device, False, 4, 2, 64)
+    q, s = torch.zeros(4, 2, 16, 64, dtype=torch.int8), h(4, 2, 16, 2)
+    pool = ops.KVPool(q, q, s, s)
+    assert len(pool.tensors) == 4 and pool.q8
+    assert len(ops.KVLayers(k[None], v[None]).tensors) == 2 and len(ops.KVLayers(q[None], q[None], s[None], s[None]).tensors) == 4
+    rows = ops.KVRows(i(3), i(2), i(2, 3), n_rows=5, max_q=4)
+    assert (rows.device, rows.n_seqs, rows.n_rows, rows.max_q) == (k.device, 2, 5, 4)
