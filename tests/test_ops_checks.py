@@ -1,6 +1,8 @@
 """The checks of the pool operators' Python calls, each shown by its own message: a call with one fault alone is
 refused for that fault. (CPU: what is asked of devices comes last.)"""
+import ctypes
 import os
+import subprocess
 import sys
 
 import pytest
@@ -68,3 +70,57 @@ def test_names_and_tensors(ops):
     assert len(ops.KVLayers(k[None], v[None]).tensors) == 2 and len(ops.KVLayers(q[None], q[None], s[None], s[None]).tensors) == 4
     rows = ops.KVRows(i(3), i(2), i(2, 3), n_rows=5, max_q=4)
     assert (rows.device, rows.n_seqs, rows.n_rows, rows.max_q) == (k.device, 2, 5, 4)
+
+
+STRUCTS = ("mk_kv_pool", "mk_kv_rows", "mk_dense", "mk_attend_args", "mk_rope", "mk_rope_args", "mk_tree_args", "mk_kv_layers")
+
+
+def test_ctypes_structures_are_the_headers(ops, tmp_path):
+    """The ctypes structures lie in memory as the C compiler lays the header's out."""
+    lines = []
+    for s in STRUCTS:
+        lines.append(f'printf("{s} %zu\\n", sizeof({s}));')
+        lines += [f'printf("{s}.{n} %zu\\n", offsetof({s}, {n}));' for n, _ in getattr(ops, s)._fields_]
+    src, exe = tmp_path / "layout.c", tmp_path / "layout"
+    src.write_text("#include <stddef.h>\n#include <stdio.h>\n#include \"mk_ops.h\"\nint main(void) {\n" + "\n".join(lines) + "\nreturn 0;\n}\n")
+    subprocess.run(["gcc", "-std=c11", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = dict(x.split() for x in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.splitlines())
+    for s in STRUCTS:
+        t = getattr(ops, s)
+        assert int(got[s]) == ctypes.sizeof(t), s
+        for n, _ in t._fields_:
+            assert int(got[f"{s}.{n}"]) == getattr(t, n).offset, (s, n)
+
+
+def _cases(ops, i, h):
+    """(call, what its message says) with one fault each that is found before devices are asked for."""
+    pool, rows = ops.KVPool(h(4, 2, 16, 64), h(4, 2, 16, 64)), ops.KVRows(i(2), i(1), i(1, 3), n_rows=5)
+    q, k = h(5, 4, 64), h(5, 2, 64)
+    rope = ops.Rope(64, device="cpu")
+    lg = torch.zeros(5, 7)
+    rw = lambda *a, **kw: lambda: ops.rope_write(pool, rows, rope, *a, **kw)  # noqa: E731
+    ta = lambda *a: lambda: ops.tree_accept(rows, *a)  # noqa: E731
+    at = lambda *a, **kw: lambda: ops.attend(pool, rows, *a, **kw)  # noqa: E731
+    return [
+        (rw(q[:4], k[:4], k[:4]), "differ from KVRows.n_rows"), (rw(q, k[:4], k), "one number of rows"), (rw(q, k, k[:4]), "one number of rows"),
+        (rw(q, k, h(5, 3, 64)), "rope_write v ("), (rw(q, h(5, 2, 128), k), "rope_write k ("), (rw(h(5, 4, 32), k, k), "rope_write q ("),
+        (rw(q[0], k, k), "rope_write q ("), (rw(q, k, k.float()), "of one type"), (rw(q.double(), k.double(), k.double()), "float32, float16 or bfloat16"),
+        (rw(h(5, 4, 64).requires_grad_(), k, k), "no gradient"), (rw(q, k, k, out=h(1, 4, 64).expand(5, 4, 64)), "must not overlap"),
+        (rw(q, k, k, out=h(5, 3, 64)), "rope_write out ("), (rw(h(5, 4, 128)[..., ::2], k, k), "contiguous head dim"), (rw(q, k, None), "(a tensor)"),
+        (rw(q, k, k), "one CUDA device"),
+        (at(q, out=h(4, 4, 64)), "one number of rows"), (at(q, out=q.float()), "of one type"), (at(q, gate=h(5, 4, 128)), "attend gate ("),
+        (at(q, out=h(1, 4, 64).expand(5, 4, 64)), "must not overlap"), (at(q), "one CUDA device"),
+        (ta(i(5), i(5), lg.double()), "logits [rows]"), (ta(i(5), i(5), lg[0]), "logits [rows]"), (ta(i(5), i(5), torch.zeros(5, 14)[:, ::2]), "logits [rows]"),
+        (ta(i(5), i(5), lg[:, :0]), "logits [rows]"), (ta(i(5), i(5), lg[:4]), "rows of the logits"), (ta(i(5), i(5), lg), "one CUDA device"),
+        (lambda: ops.kv_copy(ops.KVLayers(h(3, 4, 2, 16, 64), h(3, 4, 2, 16, 64)), i(3, 1), i(3)), "kv_copy (int32 [n])"),
+        (lambda: ops.kv_copy(ops.KVLayers(h(3, 4, 2, 16, 64), h(3, 4, 2, 16, 64)), i(3), i(3)), "a CUDA device"),
+        (lambda: ops.kv_keep(ops.KVLayers(h(3, 4, 2, 16, 64), h(3, 4, 2, 16, 64)), rows, i(5)), "one CUDA device"),
+        (lambda: ops.kv_keep(pool, rows, i(5)), "handle"), (lambda: ops.attend(rows, pool, q), "handle"), (lambda: ops.attend(pool, rows, [1]), "(a tensor)"),
+    ]
+
+
+def test_each_fault_by_its_own_message(ops):
+    for n, (call, says) in enumerate(_cases(ops, i, h)):
+        with pytest.raises(ops.MkError) as e:
+            call()
+        assert e.value.status == -1 and says in str(e.value), (n, says, str(e.value))
