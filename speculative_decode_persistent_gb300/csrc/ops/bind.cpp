@@ -410,7 +410,7 @@ PyObject* rope_write(PyObject* const* a) {  // pool, rows, rope, q, k, v, parent
 PyObject* tree_accept(PyObject* const* a) {  // rows, parents, tokens, logits
   const RowsHandle rows = get<RowsHandle>(a[0]);
   const at::Tensor& logits = tensor(a[3], "tree_accept logits");
-  if (logits.dim() != 2 || dtype_of(logits.scalar_type()) < 0 || logits.size(1) == 0 || logits.stride(1) != 1)
+  if (logits.dim() != 2 || dtype_of(logits.scalar_type()) < 0 || logits.size(1) == 0 || (logits.size(1) > 1 && logits.stride(1) != 1))
     refuse("tree_accept (logits [rows][vocabulary], float32, float16 or bfloat16, a row contiguous)");
   const int64_t n = logits.size(0), vocab = logits.size(1);
   if (rows.c.n_rows >= 0 && rows.c.n_rows != n) refuse("rows of the logits differ from KVRows.n_rows");

@@ -112,6 +112,7 @@ def _cases(ops, i, h):
         (at(q, out=h(1, 4, 64).expand(5, 4, 64)), "must not overlap"), (at(q), "one CUDA device"),
         (ta(i(5), i(5), lg.double()), "logits [rows]"), (ta(i(5), i(5), lg[0]), "logits [rows]"), (ta(i(5), i(5), torch.zeros(5, 14)[:, ::2]), "logits [rows]"),
         (ta(i(5), i(5), lg[:, :0]), "logits [rows]"), (ta(i(5), i(5), lg[:4]), "rows of the logits"), (ta(i(5), i(5), lg), "one CUDA device"),
+        (ta(i(5), i(5), torch.zeros(9, 5).t()[:, :1]), "one CUDA device"),  # (one logit a row: its stride says nothing)
         (lambda: ops.kv_copy(ops.KVLayers(h(3, 4, 2, 16, 64), h(3, 4, 2, 16, 64)), i(3, 1), i(3)), "kv_copy (int32 [n])"),
         (lambda: ops.kv_copy(ops.KVLayers(h(3, 4, 2, 16, 64), h(3, 4, 2, 16, 64)), i(3), i(3)), "a CUDA device"),
         (lambda: ops.kv_keep(ops.KVLayers(h(3, 4, 2, 16, 64), h(3, 4, 2, 16, 64)), rows, i(5)), "one CUDA device"),
