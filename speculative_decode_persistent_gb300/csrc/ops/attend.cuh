@@ -66,9 +66,9 @@
 // products; 2,048 rows over 20,512 fp16 tokens in 559 us, 1,755 TFLOP/s, over
 // q8 tokens in 682 us, where converting the codes takes as long. Few rows: the
 // pages; 4 x 3 rows over 23,003 fp16 tokens each in 71 us, 5.3 TB/s, q8 in 71 us
-// (200 MB; converting again). One row over 4,097 tokens: 15.8 us, latency. Trees: 64 nodes over
-// 96,064 fp16 tokens in 132 us (1.15 PFLOP/s, 3.0 TB/s), 4 x 16 nodes over 23,016 q8 tokens in 81 us
-// (converting), 8 nodes over 4,104 in 17.6 us.
+// (200 MB; converting again). One row over 4,097 tokens: 14.8 us, latency. Trees: 64 nodes over
+// 96,064 fp16 tokens in 143 us (1.05 PFLOP/s, 2.8 TB/s), 4 x 16 nodes over 23,016 q8 tokens in 82 us
+// (converting), 8 nodes over 4,104 in 17.7 us.
 //
 // Every wait is bounded; a worker that gives up writes NaN for its rows. Before its
 // blocks end it waits (with a limit again) for the copies and products that are
@@ -399,20 +399,23 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {
   }
   return x;
 }
-// One sequence whose few tiles all read a context that does not fit the L2 cache: every tile is cut at the same blocks,
-// into as many pieces as there are workers for a tile, so that workers at the same blocks read them at the same time
-// and memory is read once, not once a tile. (In the even cut the pieces of two tiles lie half a piece apart. 64 nodes,
-// two tiles, over 96K binary16 tokens 150 -> 132 us, 128 nodes 227 -> 200, over 32K 65 -> 63; over 23K, which the cache
-// holds, 56 in the even cut.) Where more than an eighth of the workers would be left without work the even cut stays.
+// One sequence whose few tiles all read a binary16 context that does not fit the L2 cache: every tile is cut at the same
+// blocks, into as many pieces as there are workers for a tile, so that workers at the same blocks read them at the same time
+// and memory is read once, not once a tile. (In the even cut the pieces of two tiles lie half a piece apart. 24 heads, 4 kv
+// heads of 256, GPU time in the even cut against this one: 64 rows, two tiles, over 96K 145 -> 130 us, 128 rows 210 -> 192,
+// 768 rows over 48K 623 -> 514; over 32K 64 rows 66 -> 64; over 23K, which the cache holds, 56 both.) Where more than an
+// eighth of the workers would be left without work the even cut stays, and over q8 pools, where converting the codes and not
+// memory sets the pace (64 rows over 96K: 162 us in the even cut, 166 in this one; 128 rows 230 and 234).
 // Called by one warp; false where the line is to be cut evenly.
 constexpr int64_t kFar = 96ll << 20;
 template <int M, bool TREE>
 __device__ bool aligned_start(const AttendParams& a, Start* out, int worker, bool leader) {
+  if (a.pool.kv_dtype == MK_KV_Q8) return false;
   const int lane = threadIdx.x & 31;
   const SeqView v = seq_view(a.rows, 0);
   const int n_mt = tiles_of(v, a.G, M), pieces = n_mt > 1 ? a.workers / (n_mt * a.pool.hkv) : 0;
   if (pieces == 0 || (a.workers - pieces * n_mt * a.pool.hkv) * 8 > a.workers) return false;
-  if (static_cast<int64_t>(v.kv_len) * a.pool.hkv * a.pool.dh * (a.pool.kv_dtype == MK_KV_Q8 ? 2 : 4) < kFar) return false;
+  if (static_cast<int64_t>(v.kv_len) * a.pool.hkv * a.pool.dh * 4 < kFar) return false;
   int top = 0;
   for (int mt = lane; mt < n_mt; mt += 32) top = max(top, make_tile(v, a.G, M, mt, a.window, a.sinks, TREE).nblk + item_cost(M));
   const int quota = (__reduce_max_sync(0xffffffffu, top) + pieces - 1) / pieces;
