@@ -278,6 +278,7 @@ class Engine:
         Sv, Cv = self.state_views()
         if Sv is None:
             S = conv = None
+        self._check_seq(seq, "seq_set")
         self._before_current()
         if S is not None:
             Sv[seq, 0].copy_(self._tensor(S))
@@ -289,6 +290,10 @@ class Engine:
 
     def _tensor(self, x):
         return x.detach() if self.torch.is_tensor(x) else self.torch.from_numpy(np.ascontiguousarray(x, np.float32))
+
+    def _check_seq(self, seq, what):
+        if not 0 <= seq < self.max_seqs:
+            raise MkError(-1, f"{what} (sequence)")
 
     def _states(self, what, S, conv):
         """S and conv of a sequence as fp32 tensors on the device, checked; None where not given."""
@@ -320,6 +325,7 @@ class Engine:
     def seq_new(self, seq: int):
         """Install an empty sequence (no cached token) with a zero recurrent state."""
         Sv, Cv = self.state_views()
+        self._check_seq(seq, "seq_new")
         if Sv is not None:
             self._before_current()
             Sv[seq, 0].zero_()
@@ -334,6 +340,7 @@ class Engine:
         src must have no pending step)."""
         torch = self.torch
         info = self.seq_get(src)
+        self._check_seq(dst, "clone_sequence")
         used = set()
         for s in range(self.max_seqs):
             if s != dst:
@@ -433,8 +440,7 @@ class Engine:
         torch = self.torch
         if k.dim() != 4 or k.shape != v.shape or k.shape[0] != self.n_kv:
             raise MkError(-1, "seq_load (k, v [kv layers][tokens][kv heads][head dim])")
-        if not 0 <= seq < self.max_seqs:
-            raise MkError(-1, "seq_load (sequence)")
+        self._check_seq(seq, "seq_load")
         state = self._states("seq_load", S, conv)
         used = set()
         for s in range(self.max_seqs):

@@ -147,3 +147,25 @@ def test_a_refused_keep_leaves_everything(mk):
     assert eng.seq_keep(0, 1, [], None, conv * 2) == 3
     assert torch.equal(eng.seq_get(0)["S"], S) and torch.equal(eng.seq_get(0)["conv"], conv * 2)
     eng.close()
+
+
+def test_a_sequence_that_there_is_not(mk):
+    """A number below 0 would index the last sequence's state from behind: refused before anything is written."""
+    eng = _engine(mk)
+    last = eng.max_seqs - 1
+    for s in (0, last):
+        eng.seq_new(s)
+        eng.step([5 + s], [0], [s])
+        eng.commit([s], [1])
+    eng.clone_sequence(last, last)  # state in slot 0
+    before = [eng.seq_get(last)[x].clone() for x in ("S", "conv")]
+    k = eng.seq_kv(0)
+    for seq in (-1, -last - 1, eng.max_seqs):
+        for call in (lambda: eng.seq_set(seq, 0, [], before[0] * 2, before[1] * 2), lambda: eng.seq_new(seq), lambda: eng.clone_sequence(0, seq),
+                     lambda: eng.seq_load(seq, *k), lambda: eng.seq_keep(seq, 0, []), lambda: eng.clone_sequence(seq, 0)):
+            with pytest.raises(mk.MkError) as e:
+                call()
+            assert e.value.status == -1
+    now = eng.seq_get(last)
+    assert torch.equal(now["S"], before[0]) and torch.equal(now["conv"], before[1])
+    eng.close()
