@@ -2,9 +2,9 @@
 // (a prefix for another sequence) and kept tokens (the accepted path of a tree of
 // drafts, or a context that loses old tokens). Nothing is computed: both are bound by
 // HBM traffic when much moves, by the launch when little does. Measured: 3 x 256 pages in 17
-// layers copied in 168 us (binary16, 1.14 GB, 6.8 TB/s, the copy rate) and 92 us (q8, 606 MB, 6.6 TB/s); 8,176 of 23,000 tokens moved
-// in 17 layers (q8, 605 MB) in 128 us, 4.7 TB/s (a column's batches follow each other: the latency
-// of 64 of them); the paths of four trees in 17 layers in 5 us.
+// layers copied in 168 us (binary16, 1.14 GB, 6.8 TB/s, the copy rate) and 92 us (q8, 606 MB,
+// 6.6 TB/s); 8,176 of 23,000 tokens moved in 17 layers (q8, 605 MB) in 128 us, 4.7 TB/s (a column's
+// batches follow each other: the latency of 64 of them); the paths of four trees in 17 layers in 5 us.
 #include <cuda_runtime.h>
 
 #include "ops_internal.cuh"
@@ -63,8 +63,9 @@ __global__ void __launch_bounds__(kCopyBlock) kv_copy_kernel(const __grid_consta
 // through the whole list, a batch of entries at a time: all of a batch are read, the
 // block meets, all are written. What later entries read lies behind everything that
 // earlier ones write, so columns need no order among blocks, and the next batch is read
-// while this one is on its way: its pages were looked up a batch before, its list's entries read two before. LANES lanes of 16 bytes take a token: 4 in long lists
-// (128 entries a batch, narrow columns, many blocks), 16 in shorter ones (32 entries).
+// while this one is on its way: its pages were looked up a batch before, its list's entries
+// read two before. LANES lanes of 16 bytes take a token: 4 in long lists (128 entries a
+// batch, narrow columns, many blocks), 16 in shorter ones (32 entries).
 constexpr int kThreads = 128, kDeep = 4;  // threads of a block, tokens that a thread moves at a time
 
 struct KeepArgs {

@@ -24,8 +24,8 @@
 // Bound and measured. Many rows: 8,192 rows of 24 + 4 + 4 heads of 256 (bf16, 268 MB) in 49 us,
 // 5.4 TB/s; ncu has 57 % of the issue slots busy and 16 warps an SM, which wait on their own
 // arithmetic and on shared memory. The same into a q8 pool takes 80 us (3.1 TB/s; the codec's
-// instructions on top: 51 % of the issue slots, DRAM at 34 %), in fp32
-// 100 us into an fp16 pool and 99 into a q8 one (5.0 and 4.9 TB/s). Few rows: the launch and three dependent loads of the lookup
+// instructions on top: 51 % of the issue slots, DRAM at 34 %), in fp32 100 us into an fp16 pool and
+// 99 into a q8 one (5.0 and 4.9 TB/s). Few rows: the launch and three dependent loads of the lookup
 // (64 rows into a q8 pool with their reading back, two calls: 12 to 13 us).
 #include <cmath>
 #include <type_traits>

@@ -9,8 +9,9 @@
 // early) joins the parts and walks, a block per sequence. Where a sequence's logits are few,
 // tree_small does both in one launch. Bound by the logits' bytes when the vocabulary is large,
 // by the launches when it is small. 64 rows of 248,320 fp32 logits (64 MB): 15 us, of which
-// tree_top takes 12 (5.3 TB/s) and tree_walk 3 (the parts' latency); of 16-bit logits (32 MB) 16 to 17
-// us in replayed graphs, where fp32 takes 18.5: as many comparisons (issue slots 48 % active, DRAM at 28 %). 8 rows of 2,048: 7 us through Python.
+// tree_top takes 12 (5.3 TB/s) and tree_walk 3 (the parts' latency); of 16-bit logits (32 MB) 16
+// to 17 us in replayed graphs, where fp32 takes 18.5: as many comparisons (issue slots 48 %
+// active, DRAM at 28 %). 8 rows of 2,048: 7 us through Python.
 #include <climits>
 
 #include <cuda_runtime.h>
